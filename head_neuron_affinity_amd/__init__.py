@@ -12,8 +12,11 @@ from ._binding import (HnaError, HNA_BF16, HNA_F32, HNA_ACCUMULATE, hna_dims, hn
                        last_error, unit_mass, layout_objective, neuron_step,
                        head_step, layout_search, DUAL_ITERS, loo_workspace_bytes,
                        affinity_loo, static_scratch_bytes, affinity_up_static,
-                       mfma_rate_probe)
-from .pipeline import AffinityPass, StackPass, pass_for_layer, affinity_layer
+                       mfma_rate_probe, hna_norm_dims, block_norm, block_norm_quant,
+                       block_norm_backward, block_norm_workspace_bytes, quant_pitch, quant_rows,
+                       quant_matmul)
+from .pipeline import (AffinityPass, StackPass, FfnInputs, pass_for_layer, affinity_layer,
+                       ffn_inputs)
 
 __all__ = [
     "HnaError", "HNA_BF16", "HNA_F32", "HNA_ACCUMULATE", "hna_dims", "hna_down_dims", "make_dims",
@@ -24,4 +27,6 @@ __all__ = [
     "pass_for_layer", "affinity_layer", "unit_mass", "layout_objective",
     "neuron_step", "head_step", "layout_search", "DUAL_ITERS", "loo_workspace_bytes",
     "affinity_loo", "static_scratch_bytes", "affinity_up_static", "mfma_rate_probe",
+    "hna_norm_dims", "block_norm", "block_norm_quant", "block_norm_backward",
+    "block_norm_workspace_bytes", "quant_pitch", "quant_rows", "quant_matmul", "FfnInputs", "ffn_inputs",
 ]

@@ -43,7 +43,9 @@ EXPORTED = [
     "hna_layout_objective", "hna_neuron_step", "hna_head_step",
     "hna_layout_search_workspace_bytes", "hna_layout_search", "hna_loo_workspace_bytes",
     "hna_affinity_loo", "hna_static_scratch_bytes", "hna_affinity_up_static",
-    "hna_mfma_rate_probe",
+    "hna_mfma_rate_probe", "hna_block_norm", "hna_block_norm_quant",
+    "hna_block_norm_workspace_bytes", "hna_block_norm_backward", "hna_quant_pitch",
+    "hna_quant_rows", "hna_quant_matmul",
 ]
 
 
@@ -56,6 +58,11 @@ class hna_dims(ctypes.Structure):
 class hna_down_dims(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int32), ("I", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("G", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class hna_norm_dims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("gate_tokens", ctypes.c_int64), ("hidden", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32)]
 
 
 class HnaError(RuntimeError):
@@ -79,6 +86,7 @@ def lib() -> ctypes.CDLL:
     vp, sz, i32, i64, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     dp = ctypes.POINTER(hna_dims)
     ddp = ctypes.POINTER(hna_down_dims)
+    ndp = ctypes.POINTER(hna_norm_dims)
     ip = ctypes.POINTER(ctypes.c_int32)
     sig = {
         "hna_abi_version": (ctypes.c_int, []),
@@ -106,6 +114,15 @@ def lib() -> ctypes.CDLL:
                                                   ctypes.c_int, vp, vp, vp, vp]),
         "hna_affinity_loo": (ctypes.c_int, [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ip, f32, vp, vp,
                                             sz, vp]),
+        "hna_block_norm": (ctypes.c_int, [ndp, vp, vp, vp, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp]),
+        "hna_block_norm_quant": (ctypes.c_int, [ndp, vp, vp, vp, vp, vp, f32, f32, f32, vp, vp, vp,
+                                                vp, vp, vp]),
+        "hna_block_norm_workspace_bytes": (sz, [ndp]),
+        "hna_block_norm_backward": (ctypes.c_int, [ndp, vp, vp, vp, vp, vp, vp, vp, vp, vp, f32, f32,
+                                                   vp, vp, vp, vp, vp, vp, sz, vp]),
+        "hna_quant_pitch": (i32, [i32]),
+        "hna_quant_rows": (ctypes.c_int, [i64, i32, i32, vp, vp, vp, vp]),
+        "hna_quant_matmul": (ctypes.c_int, [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp]),
         "hna_mfma_rate_probe": (ctypes.c_int, [i32, i32, i32, vp, vp, vp]),
         "hna_layout_search": (ctypes.c_int, [i32, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp,
                                               ctypes.POINTER(ctypes.c_double), ip, vp, sz, vp]),
@@ -552,3 +569,227 @@ def affinity_up_static(dims: hna_dims, a, g, u, r, r_next, M, wd_sq, group_of_he
                                         _ptr(S_fo), _ptr(S_add), _ptr(c_down), _stream(M.device)),
            "hna_affinity_up_static")
     return S_fo, S_add, c_down
+
+
+# ------------------------------------- norm step between blocks, 8-bit products
+class _on:
+    """The tensors' device as the current one while a call is enqueued, so that
+    launches go to their GPU and its current stream."""
+
+    def __init__(self, *ts):
+        _need_cuda(*ts)
+        given = [t for t in ts if t is not None]
+        self.device = given[0].device
+        if any(t.device != self.device for t in given):
+            raise ValueError("all tensors must live on the same GPU")
+        same = self.device.index == torch.cuda.current_device()
+        self.guard = None if same else torch.cuda.device(self.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.device)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _norm_dims(like, dtype, gate, gate_tokens, name) -> hna_norm_dims:
+    """dims of a norm step over rows of `like` [T, hidden], the residual; checks the gate."""
+    if like.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(like.shape)}, expected [T, hidden]")
+    T, hidden = like.shape
+    if gate is None:
+        return hna_norm_dims(T, 1, hidden, dtype, _dtype_code(like))
+    gate_tokens = max(T, 1) if gate_tokens is None else int(gate_tokens)
+    if gate_tokens < 1:
+        raise ValueError(f"gate_tokens: {gate_tokens} < 1")
+    _expect(gate, "gate", (-(-T // gate_tokens), hidden), torch.bfloat16 if dtype == HNA_BF16 else torch.float32)
+    return hna_norm_dims(T, gate_tokens, hidden, dtype, _dtype_code(like))
+
+
+def _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, dtype, outs):
+    """Checks a forward norm step's arguments; (dims, dtype of y and n)."""
+    dt = y.dtype if y is not None else (dtype or x.dtype)
+    dims = _norm_dims(x, HNA_BF16 if dt == torch.bfloat16 else HNA_F32, gate, gate_tokens, "x")
+    if dt not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dt}: bf16 or fp32 only")
+    T, C = x.shape
+    _expect(y, "y", (T, C), dt)
+    _expect(gamma, "gamma", (C,), torch.float32)
+    _expect(gamma_post, "gamma_post", (C,), torch.float32)
+    for t, name, shape, want in outs(T, C, dt):
+        _expect(t, name, shape, want)
+    if y is None and (gate is not None or gamma_post is not None or res_scale != 1.0):
+        raise ValueError("without y, gate and gamma_post must be None and res_scale 1")
+    return dims, dt
+
+
+def block_norm(x, y=None, gamma=None, *, gamma_post=None, gate=None, gate_tokens: Optional[int] = None,
+               res_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6,
+               dtype: Optional[torch.dtype] = None, x_out=None, n=None, r=None, r_post=None):
+    """The norm step between two blocks (hna_block_norm).
+
+    x' = res_scale x + block_scale gate * N(y; gamma_post), n = gamma * x' / r with
+    r = sqrt(mean(x'^2) + eps); x [T, hidden] is the residual, y the block's output (None: x' = x),
+    gate [ceil(T / gate_tokens), hidden] (default one row for all tokens).  n has y's type (`dtype`,
+    or x's, without y).  Returns (x', n, r [T], r_post [T] or None); x_out may be x and n may be y.
+    """
+    dims, dt = _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, dtype,
+                          lambda T, C, dt: ((x_out, "x_out", (T, C), x.dtype), (n, "n", (T, C), dt),
+                                            (r, "r", (T,), torch.float32),
+                                            (r_post, "r_post", (T,), torch.float32)))
+    with _on(x, y, gamma, gamma_post, gate, x_out, n, r, r_post) as stream:
+        if x_out is None and y is not None:
+            x_out = torch.empty_like(x)
+        if n is None:
+            n = torch.empty(x.shape, dtype=dt, device=x.device)
+        if r is None:
+            r = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        if r_post is None and gamma_post is not None:
+            r_post = torch.empty_like(r)
+        _check(lib().hna_block_norm(ctypes.byref(dims), _ptr(x), _ptr(y), _ptr(gate), _ptr(gamma),
+                                    _ptr(gamma_post), float(res_scale), float(block_scale), float(eps),
+                                    _ptr(x_out), _ptr(n), _ptr(r), _ptr(r_post), stream), "hna_block_norm")
+    return (x if y is None else x_out), n, r, r_post
+
+
+def block_norm_quant(x, y=None, gamma=None, *, gamma_post=None, gate=None, gate_tokens: Optional[int] = None,
+                     res_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6, x_out=None,
+                     q=None, q_scale=None, r=None, r_post=None):
+    """block_norm with n as 8-bit rows (see quant_rows): returns (x', q, q_scale, r, r_post)."""
+    pitch = lambda C: -(-C // 16) * 16  # noqa: E731
+    dims, _ = _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, None,
+                         lambda T, C, dt: ((x_out, "x_out", (T, C), x.dtype), (q, "q", (T, pitch(C)), torch.int8),
+                                           (q_scale, "q_scale", (T,), torch.float32),
+                                           (r, "r", (T,), torch.float32),
+                                           (r_post, "r_post", (T,), torch.float32)))
+    with _on(x, y, gamma, gamma_post, gate, x_out, q, q_scale, r, r_post) as stream:
+        T, C = x.shape
+        if x_out is None and y is not None:
+            x_out = torch.empty_like(x)
+        if q is None:
+            q = torch.empty((T, pitch(C)), dtype=torch.int8, device=x.device)
+        if q_scale is None:
+            q_scale = torch.empty(T, dtype=torch.float32, device=x.device)
+        if r is None:
+            r = torch.empty(T, dtype=torch.float32, device=x.device)
+        if r_post is None and gamma_post is not None:
+            r_post = torch.empty_like(r)
+        _check(lib().hna_block_norm_quant(ctypes.byref(dims), _ptr(x), _ptr(y), _ptr(gate), _ptr(gamma),
+                                          _ptr(gamma_post), float(res_scale), float(block_scale),
+                                          float(eps), _ptr(x_out), _ptr(q), _ptr(q_scale), _ptr(r),
+                                          _ptr(r_post), stream), "hna_block_norm_quant")
+    return (x if y is None else x_out), q, q_scale, r, r_post
+
+
+def block_norm_workspace_bytes(dims: hna_norm_dims) -> int:
+    return int(lib().hna_block_norm_workspace_bytes(ctypes.byref(dims)))
+
+
+def block_norm_backward(x_out, r, *, dn=None, dx_out=None, gamma=None, y=None, gamma_post=None, r_post=None,
+                        gate=None, gate_tokens: Optional[int] = None, res_scale: float = 1.0,
+                        block_scale: float = 1.0, want_dy: Optional[bool] = None, dx=None, dy=None,
+                        dgamma=None, dgamma_post=None, dgate=None, workspace=None) -> dict:
+    """Gradients of block_norm (hna_block_norm_backward) from dn and dx_out, the gradients of n and x'.
+
+    x_out, r and r_post are the forward call's outputs, the rest its arguments.  Returns a dict of
+    dx, dy (unless want_dy is False; by default if y is given), dgamma (with gamma and dn),
+    dgamma_post (with gamma_post), dgate (with gate and y); None for the others.  dx may be dx_out,
+    dy may be dn or y.
+    """
+    dt = next((t.dtype for t in (y, dn, gate, dy) if t is not None), x_out.dtype)
+    if dt not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dt}: bf16 or fp32 only")
+    if dn is None and dx_out is None:
+        raise ValueError("dn and dx_out are both None")
+    dims = _norm_dims(x_out, HNA_BF16 if dt == torch.bfloat16 else HNA_F32, gate, gate_tokens, "x_out")
+    T, C = x_out.shape
+    f32 = torch.float32
+    want_dy = (y is not None or dy is not None) if want_dy is None else want_dy
+    if gamma_post is not None and (y is None or r_post is None):
+        raise ValueError("gamma_post needs y and r_post")
+    for t, name, shape, want in ((dn, "dn", (T, C), dt), (dx_out, "dx_out", (T, C), x_out.dtype),
+                                 (y, "y", (T, C), dt), (gamma, "gamma", (C,), f32),
+                                 (gamma_post, "gamma_post", (C,), f32), (r, "r", (T,), f32),
+                                 (r_post, "r_post", (T,), f32), (dx, "dx", (T, C), x_out.dtype),
+                                 (dy, "dy", (T, C), dt), (dgamma, "dgamma", (C,), f32),
+                                 (dgamma_post, "dgamma_post", (C,), f32)):
+        _expect(t, name, shape, want)
+    if dgate is not None:
+        if gate is None or y is None:
+            raise ValueError("dgate needs gate and y")
+        _expect(dgate, "dgate", gate.shape, dt)
+    with _on(x_out, r, dn, dx_out, gamma, y, gamma_post, r_post, gate, dx, dy, dgamma, dgamma_post, dgate,
+             workspace) as stream:
+        dev = x_out.device
+        if dx is None:
+            dx = torch.empty_like(x_out)
+        if dy is None and want_dy:
+            dy = torch.empty((T, C), dtype=dt, device=dev)
+        if dgamma is None and gamma is not None and dn is not None:
+            dgamma = torch.empty_like(gamma)
+        if dgamma_post is None and gamma_post is not None:
+            dgamma_post = torch.empty_like(gamma_post)
+        if dgate is None and gate is not None and y is not None:
+            dgate = torch.empty_like(gate)
+        if workspace is None:
+            workspace = torch.empty(max(block_norm_workspace_bytes(dims), 16), dtype=torch.uint8, device=dev)
+        _check(lib().hna_block_norm_backward(
+            ctypes.byref(dims), _ptr(dn), _ptr(dx_out), _ptr(x_out), _ptr(y), _ptr(gate), _ptr(gamma),
+            _ptr(gamma_post), _ptr(r), _ptr(r_post), float(res_scale), float(block_scale), _ptr(dx),
+            _ptr(dy), _ptr(dgamma), _ptr(dgamma_post), _ptr(dgate), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), stream), "hna_block_norm_backward")
+    return {"dx": dx, "dy": dy if want_dy else None, "dgamma": dgamma, "dgamma_post": dgamma_post,
+            "dgate": dgate}
+
+
+def quant_pitch(K: int) -> int:
+    """Bytes of an 8-bit row of K elements."""
+    return int(lib().hna_quant_pitch(int(K)))
+
+
+def quant_rows(x, q=None, scale=None):
+    """Rows of x [rows, K] as 8-bit integers with one scale each (hna_quant_rows): q int8
+    [rows, K rounded up to 16], scale fp32 [rows].  Activations per token, weights per channel."""
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [rows, K]")
+    rows, K = x.shape
+    code = _dtype_code(x)
+    pitch = -(-K // 16) * 16
+    _expect(q, "q", (rows, pitch), torch.int8)
+    _expect(scale, "scale", (rows,), torch.float32)
+    with _on(x, q, scale) as stream:
+        if q is None:
+            q = torch.empty((rows, pitch), dtype=torch.int8, device=x.device)
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        _check(lib().hna_quant_rows(int(rows), int(K), code, _ptr(x), _ptr(q), _ptr(scale), stream),
+               "hna_quant_rows")
+    return q, scale
+
+
+def quant_matmul(q, q_scale, w, w_scale, out=None, dtype: torch.dtype = torch.bfloat16):
+    """out [T, N] = (q w^T) * q_scale[:, None] * w_scale (hna_quant_matmul): q int8 [T, K] and w int8
+    [N, K] as quant_rows writes them; the sums are exact."""
+    if q.dim() != 2 or w.dim() != 2:
+        raise ValueError("q and w must be [T, K] and [N, K]")
+    T, K = q.shape
+    N = w.shape[0]
+    _expect(q, "q", (T, K), torch.int8)
+    _expect(w, "w", (N, K), torch.int8)
+    _expect(q_scale, "q_scale", (T,), torch.float32)
+    _expect(w_scale, "w_scale", (N,), torch.float32)
+    if out is not None:
+        dtype = out.dtype
+        _expect(out, "out", (T, N), dtype)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32 only")
+    with _on(q, q_scale, w, w_scale, out) as stream:
+        if out is None:
+            out = torch.empty((T, N), dtype=dtype, device=q.device)
+        _check(lib().hna_quant_matmul(int(T), int(N), int(K), HNA_BF16 if dtype == torch.bfloat16 else HNA_F32,
+                                      _ptr(q), _ptr(q_scale), _ptr(w), _ptr(w_scale), _ptr(out), stream),
+               "hna_quant_matmul")
+    return out

@@ -3,6 +3,7 @@
 // negative status and leave a thread-local message (see include/hna.h).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -132,6 +133,101 @@ size_t down_ws_transposed(const hna_down_dims* dm) {
 }
 size_t down_ws_bytes(const hna_down_dims* dm) {
   return down_ws_transposed(dm) + align256((size_t)(dm->H + 2 * dm->G) * dm->I * sizeof(float));
+}
+
+// ---- norm step and 8-bit rows ----
+constexpr int32_t kMaxQuantK = 131056;   // 128 * 128 * K < 2^31, a multiple of 16
+constexpr int64_t kMaxQuantTokens = (int64_t)1 << 30;
+constexpr int64_t kMaxQuantOut = (int64_t)1 << 36;   // at most 2^24 tiles of 128 x 128
+
+int check_norm_dims(const char* fn, const hna_norm_dims* dm) {
+  if (!dm) return fail(HNA_ERR_INVALID_ARG, "%s: dims is NULL", fn);
+  int rc = check_dtype(fn, dm->dtype);
+  if (rc) return rc;
+  rc = check_dtype(fn, dm->res_dtype);
+  if (rc) return rc;
+  if (dm->T < 0) return fail(HNA_ERR_INVALID_ARG, "%s: T=%lld < 0", fn, (long long)dm->T);
+  if (dm->hidden < 1) return fail(HNA_ERR_INVALID_ARG, "%s: hidden=%d < 1", fn, dm->hidden);
+  if (dm->T > (int64_t)INT32_MAX)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: T=%lld > 2^31 - 1", fn, (long long)dm->T);
+  if (dm->hidden % 8 != 0 || dm->hidden > kMaxNormWidth)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: hidden=%d must be a multiple of 8 and <= %d", fn, dm->hidden,
+                kMaxNormWidth);
+  return HNA_OK;
+}
+
+int check_gate_tokens(const char* fn, const hna_norm_dims* dm) {
+  if (dm->gate_tokens < 1)
+    return fail(HNA_ERR_INVALID_ARG, "%s: gate_tokens=%lld < 1", fn, (long long)dm->gate_tokens);
+  return HNA_OK;
+}
+
+// tokens per gate row within the call (the kernels divide 32-bit row numbers by it)
+int64_t gate_span(const hna_norm_dims* dm) { return std::min(dm->gate_tokens, std::max<int64_t>(dm->T, 1)); }
+
+size_t norm_grad_part_bytes(const NormGradGeometry& g, int C) { return align256((size_t)g.n_wg * C * sizeof(float)); }
+
+// partial rows of dgamma and dgamma_post, then of dgate; with or without gates
+size_t norm_grad_ws_bytes(const hna_norm_dims* dm) {
+  size_t most = 3 * norm_grad_part_bytes(norm_grad_geometry(dm->T, dm->hidden, 0), dm->hidden);
+  if (dm->gate_tokens >= 1)
+    most = std::max(most, 3 * norm_grad_part_bytes(norm_grad_geometry(dm->T, dm->hidden, gate_span(dm)), dm->hidden));
+  return most;
+}
+
+#define OPTIONAL_PTR(p)                                                                      \
+  do {                                                                                       \
+    if ((p) && !aligned16(p)) return fail(HNA_ERR_ALIGNMENT, "%s: %s is not 16-byte aligned", fn, #p); \
+  } while (0)
+
+int block_norm(const char* fn, bool quant, const hna_norm_dims* dm, const void* x, const void* y,
+               const void* gate, const float* gamma, const float* gamma_post, float res_scale,
+               float block_scale, float eps, void* x_out, void* n, int8_t* q, float* q_scale, float* r,
+               float* r_post, void* stream) {
+  int rc = check_norm_dims(fn, dm);
+  if (rc) return rc;
+  if (!(eps >= 0.f)) return fail(HNA_ERR_INVALID_ARG, "%s: eps=%g must be >= 0", fn, (double)eps);
+  if (gate && (rc = check_gate_tokens(fn, dm))) return rc;
+  OPTIONAL_PTR(gate);
+  OPTIONAL_PTR(gamma);
+  OPTIONAL_PTR(gamma_post);
+  if (dm->T > 0) {   // without tokens every buffer is empty and may be NULL
+    if (!y && (gate || gamma_post || x_out || r_post || res_scale != 1.f))
+      return fail(HNA_ERR_INVALID_ARG, "%s: without y, gate, gamma_post, x_out and r_post must be NULL and res_scale 1", fn);
+    if (r_post && !gamma_post) return fail(HNA_ERR_INVALID_ARG, "%s: r_post without gamma_post", fn);
+    if (!quant && !n && !x_out && !r) return fail(HNA_ERR_INVALID_ARG, "%s: no output is wanted", fn);
+    REQUIRE_PTR(x);
+    OPTIONAL_PTR(y);
+    if (y) REQUIRE_PTR(x_out);
+    OPTIONAL_PTR(n);
+    OPTIONAL_PTR(r);
+    OPTIONAL_PTR(r_post);
+    if (quant) {
+      REQUIRE_PTR(q);
+      REQUIRE_PTR(q_scale);
+    }
+  }
+  NormParams p{};
+  p.x = x;
+  p.y = y;
+  p.gate = gate;
+  p.gamma = gamma;
+  p.gamma_post = gamma_post;
+  p.x_out = x_out;
+  p.n = n;
+  p.q = quant ? q : nullptr;
+  p.q_scale = q_scale;
+  p.r = r;
+  p.r_post = r_post;
+  p.T = dm->T;
+  p.gate_tokens = gate ? gate_span(dm) : 1;
+  p.C = dm->hidden;
+  p.pitch = round_up(dm->hidden, 16);
+  p.res_scale = res_scale;
+  p.block_scale = block_scale;
+  p.eps = eps;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_block_norm(p, dm->res_dtype == HNA_BF16, dm->dtype == HNA_BF16, st), st, fn);
 }
 
 }  // namespace
@@ -1031,6 +1127,155 @@ int hna_layout_search(int32_t N, int32_t G, int32_t I, int32_t L, const float* S
       return hip_fail(e, fn);
   }
   return finish(hipSuccess, st, fn);
+}
+
+// ---- norm step and 8-bit products ----
+int hna_block_norm(const hna_norm_dims* dm, const void* x, const void* y, const void* gate,
+                   const float* gamma, const float* gamma_post, float res_scale, float block_scale,
+                   float eps, void* x_out, void* n, float* r, float* r_post, void* stream) {
+  return block_norm("hna_block_norm", false, dm, x, y, gate, gamma, gamma_post, res_scale, block_scale, eps,
+                    x_out, n, nullptr, nullptr, r, r_post, stream);
+}
+
+int hna_block_norm_quant(const hna_norm_dims* dm, const void* x, const void* y, const void* gate,
+                         const float* gamma, const float* gamma_post, float res_scale,
+                         float block_scale, float eps, void* x_out, int8_t* q, float* q_scale, float* r,
+                         float* r_post, void* stream) {
+  return block_norm("hna_block_norm_quant", true, dm, x, y, gate, gamma, gamma_post, res_scale, block_scale,
+                    eps, x_out, nullptr, q, q_scale, r, r_post, stream);
+}
+
+size_t hna_block_norm_workspace_bytes(const hna_norm_dims* dm) {
+  if (check_norm_dims("hna_block_norm_workspace_bytes", dm)) return 0;
+  return std::max(norm_grad_ws_bytes(dm), size_t(256));
+}
+
+int hna_block_norm_backward(const hna_norm_dims* dm, const void* dn, const void* dx_out,
+                            const void* x_out, const void* y, const void* gate, const float* gamma,
+                            const float* gamma_post, const float* r, const float* r_post,
+                            float res_scale, float block_scale, void* dx, void* dy, float* dgamma,
+                            float* dgamma_post, void* dgate, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  const char* fn = "hna_block_norm_backward";
+  int rc = check_norm_dims(fn, dm);
+  if (rc) return rc;
+  if (gate && (rc = check_gate_tokens(fn, dm))) return rc;
+  const bool block = dy || dgamma_post || dgate;
+  OPTIONAL_PTR(gate);
+  OPTIONAL_PTR(gamma);
+  OPTIONAL_PTR(gamma_post);
+  OPTIONAL_PTR(dgamma);
+  OPTIONAL_PTR(dgamma_post);
+  OPTIONAL_PTR(dgate);
+  if (dm->T > 0) {   // without tokens only the sums over them are there to be written
+    if (dgate && !gate) return fail(HNA_ERR_INVALID_ARG, "%s: dgate without gate", fn);
+    if (dgamma_post && !gamma_post) return fail(HNA_ERR_INVALID_ARG, "%s: dgamma_post without gamma_post", fn);
+    if (!dx && !dy && !dgamma && !dgamma_post && !dgate)
+      return fail(HNA_ERR_INVALID_ARG, "%s: no gradient is wanted", fn);
+    if (!dn && !dx_out) return fail(HNA_ERR_INVALID_ARG, "%s: dn and dx_out are both NULL", fn);
+    if (!dn && dgamma) return fail(HNA_ERR_INVALID_ARG, "%s: dgamma without dn", fn);
+    OPTIONAL_PTR(dn);
+    OPTIONAL_PTR(dx_out);
+    if (dn) {
+      REQUIRE_PTR(x_out);
+      REQUIRE_PTR(r);
+    }
+    if (block && (gamma_post || dgate)) REQUIRE_PTR(y);
+    if (block && gamma_post) REQUIRE_PTR(r_post);
+    OPTIONAL_PTR(dx);
+    OPTIONAL_PTR(dy);
+  }
+  REQUIRE_PTR(workspace);
+  const size_t need = norm_grad_ws_bytes(dm);
+  if (workspace_bytes < need)
+    return fail(HNA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, need);
+  const NormGradGeometry geo = norm_grad_geometry(dm->T, dm->hidden, dgate ? gate_span(dm) : 0);
+  const size_t part = norm_grad_part_bytes(geo, dm->hidden);
+  char* ws = static_cast<char*>(workspace);
+  NormGradParams p{};
+  p.dn = dn;
+  p.dx_out = dx_out;
+  p.x_out = x_out;
+  p.y = block && (gamma_post || dgate) ? y : nullptr;
+  p.gate = block ? gate : nullptr;
+  p.gamma = gamma;
+  p.gamma_post = block ? gamma_post : nullptr;
+  p.r = r;
+  p.r_post = r_post;
+  p.dx = dx;
+  p.dy = dy;
+  p.dgate = dgate;
+  p.part_g = dgamma ? reinterpret_cast<float*>(ws) : nullptr;
+  p.part_p = dgamma_post ? reinterpret_cast<float*>(ws + part) : nullptr;
+  p.part_t = dgate && geo.gate_parts ? reinterpret_cast<float*>(ws + 2 * part) : nullptr;
+  p.T = dm->T;
+  p.gate_tokens = gate ? gate_span(dm) : 1;
+  p.chunk = geo.chunk;
+  p.group_rows = geo.group_rows;
+  p.flush_rows = geo.flush_rows;
+  p.n_wg = geo.n_wg;
+  p.C = dm->hidden;
+  p.spans = geo.spans;
+  p.block = block;
+  p.gate_each = geo.gate_each;
+  p.res_scale = res_scale;
+  p.block_scale = block_scale;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_block_norm_backward(p, dm->res_dtype == HNA_BF16, dm->dtype == HNA_BF16, dgamma,
+                                           dgamma_post, st), st, fn);
+}
+
+int32_t hna_quant_pitch(int32_t K) { return K < 1 || K > kMaxQuantK ? 0 : round_up(K, 16); }
+
+int hna_quant_rows(int64_t rows, int32_t K, int32_t dtype, const void* x, int8_t* q, float* scale,
+                   void* stream) {
+  const char* fn = "hna_quant_rows";
+  int rc = check_dtype(fn, dtype);
+  if (rc) return rc;
+  if (rows < 0 || K < 1) return fail(HNA_ERR_INVALID_ARG, "%s: rows=%lld, K=%d", fn, (long long)rows, K);
+  if (rows > (int64_t)INT32_MAX || K > kMaxQuantK)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: rows=%lld > 2^31 - 1 or K=%d > %d", fn, (long long)rows, K, kMaxQuantK);
+  if (rows > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(scale);
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_quant_rows(x, rows, K, round_up(K, 16), dtype == HNA_BF16, q, scale, st), st, fn);
+}
+
+int hna_quant_matmul(int64_t T, int32_t N, int32_t K, int32_t out_dtype, const int8_t* q,
+                     const float* q_scale, const int8_t* w, const float* w_scale, void* out,
+                     void* stream) {
+  const char* fn = "hna_quant_matmul";
+  int rc = check_dtype(fn, out_dtype);
+  if (rc) return rc;
+  if (T < 0 || N < 1 || K < 1)
+    return fail(HNA_ERR_INVALID_ARG, "%s: T=%lld, N=%d, K=%d", fn, (long long)T, N, K);
+  if (K % 16 != 0 || K > kMaxQuantK)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: K=%d must be a multiple of 16 and <= %d", fn, K, kMaxQuantK);
+  if (T > kMaxQuantTokens || N > (1 << 22) || T * N > kMaxQuantOut)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: T=%lld, N=%d: more than 2^30 tokens, 2^22 channels or 2^36 outputs",
+                fn, (long long)T, N);
+  if (T > 0) {
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(q_scale);
+    REQUIRE_PTR(w);
+    REQUIRE_PTR(w_scale);
+    REQUIRE_PTR(out);
+  }
+  IntMmParams p{};
+  p.q = q;
+  p.w = w;
+  p.q_scale = q_scale;
+  p.w_scale = w_scale;
+  p.out = out;
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.out_bf16 = out_dtype == HNA_BF16;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_mm_int(p, st), st, fn);
 }
 
 }  // extern "C"

@@ -90,6 +90,41 @@ __device__ inline uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(lds_ptr)const_cast<void*>(p);
 }
 
+constexpr uint32_t kMaxResourceBytes = 0x7ffff000u;   // below the out-of-range offset
+
+// Asynchronous 16-byte buffer -> LDS copy with a scalar offset soff added to
+// the address (voff is what the range check covers); lane l writes LDS
+// m0 + 16 l.  The resource is passed as its four descriptor words.
+__device__ inline void dma16s(u32x4 rs, uint32_t voff, uint32_t soff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(m0), "v"(voff), "s"(rs), "s"(soff) : "memory");
+}
+
+// Raw buffer descriptor words (32-bit data format, no swizzle, stride 0) over
+// [base, base + bytes), built from values the compiler may not see as uniform
+// (they are): each word goes through readfirstlane, so the descriptor lives
+// in scalar registers.
+__device__ inline u32x4 uniform_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  u32x4 d;
+  d.x = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  d.y = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) & 0xffffu;
+  d.z = __builtin_amdgcn_readfirstlane(bytes);
+  d.w = 0x00020000u;
+  return d;
+}
+
+// XOR applied to the 16-byte chunk index in row r of a stage whose rows hold
+// CPR chunks: any 8 consecutive rows put one chunk column in 8 distinct
+// 16-byte slots of the 128-byte lines they span
+template <int CPR>
+__device__ inline int swz(int r) {
+  // 128-byte rows: a 64-bank LDS serves 16 lanes (16 rows) of a 16-byte read
+  // at once, so every 16 rows must also cover 16 distinct slots of the
+  // 256-byte lines they span
+  if constexpr (CPR == 8) return (r & 7) ^ ((r >> 3) & 1);
+  return (r / (8 / CPR)) % CPR;
+}
 
 }  // namespace hot
 }  // namespace hna

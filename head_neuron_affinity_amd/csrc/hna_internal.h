@@ -285,4 +285,54 @@ hipError_t launch_scale_transpose(const void* in, const float* s, void* out, int
 // or batches / K chunks (store); K and k_split multiples of 4
 hipError_t launch_gemm_f32(const GemmParams& p, int epilogue, int ny, hipStream_t st);
 
+// ------------------------------------------------ norm step and 8-bit rows (k_norm.hip)
+constexpr int kMaxNormWidth = 16384;      // a row is held in registers
+struct NormParams {
+  const void* x;            // [T][C] residual type
+  const void* y;            // [T][C] io type, or NULL: x' = x
+  const void* gate;         // [ceil(T / gate_tokens)][C] io type, or NULL
+  const float* gamma;       // [C] or NULL (ones)
+  const float* gamma_post;  // [C] or NULL (no norm of y)
+  void* x_out;              // [T][C] residual type (y given)
+  void* n;                  // [T][C] io type, or NULL
+  int8_t* q;                // [T][pitch]: n as 8-bit integers instead
+  float *q_scale, *r, *r_post;
+  int64_t T, gate_tokens;
+  int C, pitch;
+  float res_scale, block_scale, eps;
+};
+hipError_t launch_block_norm(const NormParams& p, int res_bf16, int io_bf16, hipStream_t st);
+
+struct NormGradGeometry {
+  int64_t chunk, group_rows, flush_rows, n_wg;
+  int spans;
+  int gate_parts;           // dgate through partial rows
+  int gate_each;            // a gate row per token
+};
+NormGradGeometry norm_grad_geometry(int64_t T, int C, int64_t gate_tokens);
+struct NormGradParams {
+  const void *dn, *dx_out, *x_out, *y, *gate;
+  const float *gamma, *gamma_post, *r, *r_post;
+  void *dx, *dy, *dgate;
+  float *part_g, *part_p, *part_t;   // [n_wg][C] partial rows of dgamma, dgamma_post, dgate (or NULL)
+  int64_t T, gate_tokens, chunk, group_rows, flush_rows, n_wg;
+  int C, spans, block, gate_each;
+  float res_scale, block_scale;
+};
+hipError_t launch_block_norm_backward(const NormGradParams& p, int res_bf16, int io_bf16, float* dgamma,
+                                      float* dgamma_post, hipStream_t st);
+hipError_t launch_quant_rows(const void* x, int64_t n, int K, int pitch, int x_bf16, int8_t* q, float* scale,
+                             hipStream_t st);
+
+// ------------------------------------------------ 8-bit product (k_mm_int.hip)
+// out[t][n] = (sum_k q[t][k] w[n][k]) q_scale[t] w_scale[n], rows of K bytes, K a multiple of 16
+struct IntMmParams {
+  const int8_t *q, *w;
+  const float *q_scale, *w_scale;
+  void* out;
+  int64_t T;
+  int N, K, out_bf16;
+};
+hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st);
+
 }  // namespace hna

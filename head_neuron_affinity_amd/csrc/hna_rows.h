@@ -1,0 +1,143 @@
+// Device helpers of the row kernels (norms and 8-bit rows): 8-element loads and
+// stores in fp32, sums and maxima over the lanes that hold one row, and the
+// rounding of a row to 8-bit integers.
+#pragma once
+
+#include "hna_internal.h"
+
+namespace hna {
+namespace rows {
+
+// ---- 8 consecutive elements, 16-byte aligned ----
+__device__ inline void load8(const __bf16* p, float (&v)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ inline void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ inline void store8(__bf16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ inline void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+// v as it will be read back from a tensor of type R
+template <typename R>
+__device__ inline float as_stored(float v) {
+  if constexpr (sizeof(R) == 2) return __uint_as_float(pack_bf16x2(v, 0.f) << 16);
+  return v;
+}
+
+// ---- one value per lane combined over the 64 lanes of a wave; every lane gets
+// the same bits (each step combines the same two values in both lanes) ----
+template <int CTRL>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+template <typename F>
+__device__ inline uint32_t wave_all(uint32_t v, F f) {
+  v = f(v, dpp<0xB1>(v));    // lane ^ 1
+  v = f(v, dpp<0x4E>(v));    // lane ^ 2
+  v = f(v, dpp<0x141>(v));   // the other four of eight
+  v = f(v, dpp<0x140>(v));   // the other eight of sixteen
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = f(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return f(b[0], b[1]);
+}
+__device__ inline uint32_t add_bits(uint32_t a, uint32_t b) {
+  return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+}
+__device__ inline uint32_t max_bits(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The same over the NT lanes that hold one row (whole waves), NT / 64 partials
+// through LDS.  `box` holds 2 x (workgroup waves) words and `phase` alternates
+// between its halves: a half is written again only after the barrier of the
+// other half, which every wave reaches after its reads of this one, so one
+// barrier per call is enough.  Every thread of the workgroup must call it.
+template <int NT, int WG, typename F>
+__device__ inline uint32_t row_all(uint32_t v, uint32_t* box, int& phase, F f) {
+  v = wave_all(v, f);
+  if constexpr (NT > 64) {
+    uint32_t* b = box + phase * (WG / 64);
+    phase ^= 1;
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) b[w] = v;
+    __syncthreads();
+    const int w0 = w & ~(NT / 64 - 1);
+    v = b[w0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; ++i) v = f(v, b[w0 + i]);
+  }
+  return v;
+}
+template <int NT, int WG>
+__device__ inline float row_sum(float v, uint32_t* box, int& phase) {
+  return __uint_as_float(row_all<NT, WG>(__float_as_uint(v), box, phase, add_bits));
+}
+// Largest |v| of a row as bits: the order of the bits of |v| is that of |v|,
+// with infinity and every NaN above the finite values
+template <int NT, int WG>
+__device__ inline uint32_t row_max_bits(uint32_t v, uint32_t* box, int& phase) {
+  return row_all<NT, WG>(v, box, phase, max_bits);
+}
+
+// ---- a row as 8-bit integers ----
+// q = the integer nearest to 127 v / top, top = max|v| of the row, ties to even,
+// exactly: t = v * (127 / top) is within 2e-5 of the quotient (two roundings,
+// |t| <= 127), so its nearest integer is right unless t lies that close to a
+// half; there the sign of 254 |v| - (2 k + 1) top decides, k = floor |t|.  With
+// b + bl = (2 k + 1) top exactly (b rounded, bl the remainder), 254 |v| - b is
+// a difference of close numbers of at most 32 bits and comes out exactly, so
+// the sign of its difference with bl is exact too.
+// `pre` is a power of two that keeps top within 2^-100 .. 2^100, so that
+// neither 127 / top nor the products leave the range of fp32.
+struct RowScale {
+  float scale;   // what one step of q stands for: top / 127 (NaN for a row with a NaN or an infinity)
+  float inv;     // 127 / (top pre), 0 where every q is 0
+  float top;     // top pre
+  float pre;
+};
+__device__ inline RowScale row_scale(uint32_t top_bits) {
+  RowScale s;
+  const float top = __uint_as_float(top_bits);
+  const bool finite = top_bits < 0x7f800000u;
+  s.pre = top < 0x1p-100f ? 0x1p100f : (top > 0x1p100f ? 0x1p-100f : 1.f);
+  s.top = top * s.pre;
+  s.scale = finite ? top / 127.f : __uint_as_float(0x7fc00000u);
+  s.inv = finite && top > 0.f ? 127.f / s.top : 0.f;
+  return s;
+}
+__device__ inline float quant_exact(float v, float t, const RowScale& s) {
+  const float av = fabsf(v), k = floorf(fabsf(t)), odd = 2.f * k + 1.f;
+  const float b = odd * s.top, bl = fmaf(odd, s.top, -b);
+  const float d = fmaf(254.f, av, -b) - bl;
+  const float q = k + ((d > 0.f || (d == 0.f && ((int)k & 1))) ? 1.f : 0.f);
+  return copysignf(q, v);
+}
+// 8 elements to 8 bytes
+__device__ inline uint2 quant8(const float (&v)[8], const RowScale& s) {
+  uint32_t w[2] = {0u, 0u};
+  if (s.inv == 0.f) return make_uint2(0u, 0u);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float u = v[e] * s.pre, t = u * s.inv;
+    float q = rintf(t);
+    if (fabsf(fabsf(t - q) - 0.5f) < 1e-4f) q = quant_exact(u, t, s);
+    w[e >> 2] |= ((uint32_t)(int)q & 0xffu) << (8 * (e & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+}  // namespace rows
+}  // namespace hna

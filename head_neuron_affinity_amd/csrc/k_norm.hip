@@ -1,0 +1,514 @@
+// The norm step between two blocks, and its gradients.
+//
+//   b  = y / r_post * gamma_post (r_post = sqrt(mean y^2 + eps)), or y;  b *= gate
+//   x' = res_scale x + block_scale b, rounded to the residual's type
+//   n  = gamma x' / r,  r = sqrt(mean x'^2 + eps),  of x' as stored;
+//        or n as 8-bit integers with one scale per token
+//
+// One pass over the data: NT lanes hold a row in registers (CH chunks of 8
+// elements each), so x' and y are read once and n needs no second read.  Sums
+// run in fp32 over 8 CH elements per lane, then across lanes in a fixed order.
+// Bound by HBM.  A row sits in one wave up to 1024 elements (no barrier), in
+// NT / 64 waves above; a workgroup walks over rows with the gains in registers.
+#include <algorithm>
+
+#include "hna_rows.h"
+
+namespace hna {
+namespace {
+
+using namespace rows;
+
+constexpr int wg_of(int nt) { return nt < 256 ? 256 : nt; }
+
+// 1 / r, or 0 for a row whose mean square and eps are both 0: it normalises to zeros
+__device__ inline float inv_or_zero(float r) { return r > 0.f ? 1.f / r : (r == 0.f ? 0.f : r); }
+
+template <typename R, typename D, int NT, int CH, bool Q8>
+__global__ __launch_bounds__(wg_of(NT)) void block_norm_kernel(const NormParams p) {
+  constexpr int WG = wg_of(NT), NR = WG / NT;
+  __shared__ uint32_t box[2 * (WG / 64)];
+  int phase = 0;
+  const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
+  const float inv_c = 1.f / (float)p.C;
+
+  float ga[CH][8], gp[CH][8];
+  bool in[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int j = (c * NT + lane) * 8;
+    in[c] = j < p.C;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ga[c][e] = gp[c][e] = 1.f;
+    if (in[c] && p.gamma) load8(p.gamma + j, ga[c]);
+    if (in[c] && p.gamma_post) load8(p.gamma_post + j, gp[c]);
+  }
+
+  for (int64_t row0 = (int64_t)blockIdx.x * NR; row0 < p.T; row0 += (int64_t)gridDim.x * NR) {
+    const int64_t row = row0 + sub;
+    const bool live = row < p.T;
+    const int64_t base = row * p.C;
+    float h[CH][8], y[CH][8];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t o = base + (c * NT + lane) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[c][e] = y[c][e] = 0.f;
+      if (live && in[c]) {
+        load8(static_cast<const R*>(p.x) + o, h[c]);
+        if (p.y) load8(static_cast<const D*>(p.y) + o, y[c]);
+      }
+    }
+    if (p.y) {
+      float m = p.block_scale;
+      if (p.gamma_post) {
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s = fmaf(y[c][e], y[c][e], s);
+        const float rp = sqrtf(fmaf(row_sum<NT, WG>(s, box, phase), inv_c, p.eps));
+        if (live && lane == 0 && p.r_post) p.r_post[row] = rp;
+        m *= inv_or_zero(rp);
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float g[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = gp[c][e];
+        if (p.gate && live && in[c]) {
+          float v[8];
+          load8(static_cast<const D*>(p.gate) +
+                    (int64_t)((uint32_t)row / (uint32_t)p.gate_tokens) * p.C + (c * NT + lane) * 8, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] *= v[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          h[c][e] = as_stored<R>(fmaf(p.res_scale, h[c][e], y[c][e] * m * g[e]));
+        if (live && in[c]) store8(static_cast<R*>(p.x_out) + base + (c * NT + lane) * 8, h[c]);
+      }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = fmaf(h[c][e], h[c][e], s);
+    const float r = sqrtf(fmaf(row_sum<NT, WG>(s, box, phase), inv_c, p.eps));
+    if (live && lane == 0 && p.r) p.r[row] = r;
+    const float inv = inv_or_zero(r);
+    if constexpr (!Q8) {
+      if (!p.n) continue;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = h[c][e] * inv * ga[c][e];
+        if (live && in[c]) store8(static_cast<D*>(p.n) + base + (c * NT + lane) * 8, v);
+      }
+    } else {
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          h[c][e] = h[c][e] * inv * ga[c][e];
+          if (in[c]) top = max_bits(top, __float_as_uint(h[c][e]) & 0x7fffffffu);
+        }
+      const RowScale rs = row_scale(row_max_bits<NT, WG>(top, box, phase));
+      if (live && lane == 0) p.q_scale[row] = rs.scale;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int j = (c * NT + lane) * 8;   // columns from C up to the pitch get zeros
+        if (live && j < p.pitch)
+          *reinterpret_cast<uint2*>(p.q + row * p.pitch + j) = in[c] ? quant8(h[c], rs) : make_uint2(0u, 0u);
+      }
+    }
+  }
+}
+
+// Rows of x as 8-bit integers.  VEC: rows start on 16 bytes.
+template <typename D, int NT, int CH, bool VEC>
+__global__ __launch_bounds__(wg_of(NT)) void quant_rows_kernel(const D* __restrict__ x, int64_t n_rows,
+                                                               int K, int pitch, int8_t* __restrict__ q,
+                                                               float* __restrict__ scale) {
+  constexpr int WG = wg_of(NT), NR = WG / NT;
+  __shared__ uint32_t box[2 * (WG / 64)];
+  int phase = 0;
+  const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
+  for (int64_t row0 = (int64_t)blockIdx.x * NR; row0 < n_rows; row0 += (int64_t)gridDim.x * NR) {
+    const int64_t row = row0 + sub;
+    const bool live = row < n_rows;
+    float v[CH][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * NT + lane) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
+      if (live && j < K) {
+        if constexpr (VEC) {
+          load8(x + row * K + j, v[c]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (j + e < K) v[c][e] = (float)x[row * K + j + e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max_bits(top, __float_as_uint(v[c][e]) & 0x7fffffffu);
+    }
+    const RowScale rs = row_scale(row_max_bits<NT, WG>(top, box, phase));
+    if (live && lane == 0) scale[row] = rs.scale;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * NT + lane) * 8;
+      if (live && j < pitch) *reinterpret_cast<uint2*>(q + row * pitch + j) = quant8(v[c], rs);
+    }
+  }
+}
+
+// Rows too long for registers (K > 16384): read twice, one workgroup per row.
+template <typename D>
+__global__ __launch_bounds__(1024) void quant_long_rows_kernel(const D* __restrict__ x, int64_t n_rows, int K,
+                                                               int pitch, int8_t* __restrict__ q,
+                                                               float* __restrict__ scale) {
+  __shared__ uint32_t box[2 * 16];
+  int phase = 0;
+  for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x) {
+    const D* xr = x + row * K;
+    uint32_t top = 0;
+    for (int j = threadIdx.x; j < K; j += 1024) top = max_bits(top, __float_as_uint((float)xr[j]) & 0x7fffffffu);
+    const RowScale rs = row_scale(row_max_bits<1024, 1024>(top, box, phase));
+    if (threadIdx.x == 0) scale[row] = rs.scale;
+    for (int j = threadIdx.x * 8; j < pitch; j += 8192) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = j + e < K ? (float)xr[j + e] : 0.f;
+      *reinterpret_cast<uint2*>(q + row * pitch + j) = quant8(v, rs);
+    }
+  }
+}
+
+// Gradients of the norm step.  With xh = x' / r, w = gamma dn and mean over a row:
+//   d  = dx' + (w - xh mean(w xh)) / r         gradient at x' (its rounding passes it on)
+//   dx = res_scale d,  e = block_scale d
+//   dgamma += dn xh
+//   with yh = y / r_post (or y), b = yh gamma_post, f = gate e, v = gamma_post f:
+//   dgate += e b (over the tokens of a gate row),  dgamma_post += f yh
+//   dy = (v - yh mean(v yh)) / r_post, or f without a block norm
+// A workgroup takes `chunk` consecutive rows and keeps its column sums in
+// registers.  Without gates, or where a gate row spans several workgroups, it
+// ends with one fp32 partial row per sum; where gate rows are shorter than a
+// chunk the chunk holds whole gate rows and writes each dgate row itself; a
+// gate row per token needs no sum.
+// col_sum_kernel adds the partial rows, in their order: no atomics.
+template <typename R, typename D, int NT, int CH>
+__global__ __launch_bounds__(wg_of(NT)) void block_norm_backward_kernel(const NormGradParams p) {
+  constexpr int WG = wg_of(NT), NR = WG / NT;
+  __shared__ uint32_t box[2 * (WG / 64)];
+  __shared__ float cols[NR > 1 ? NR * NT * 8 : 1];
+  int phase = 0;
+  const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
+  const float inv_c = 1.f / (float)p.C;
+  const bool has_y = p.y != nullptr, post = p.gamma_post != nullptr;
+
+  bool in[CH];
+  float acc_g[CH][8], acc_p[CH][8], acc_t[CH][8];   // dgamma, dgamma_post, dgate
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    in[c] = (c * NT + lane) * 8 < p.C;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc_g[c][e] = acc_p[c][e] = acc_t[c][e] = 0.f;
+  }
+
+  // sum of acc over the NR rows a workgroup holds side by side, chunk by chunk;
+  // the lanes of sub-row 0 get it and hand it to `put`
+  auto fold = [&](float (&acc)[CH][8], auto put) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if constexpr (NR > 1) {
+        __syncthreads();
+        store8(cols + threadIdx.x * 8, acc[c]);
+        __syncthreads();
+        if (sub == 0) {
+#pragma unroll
+          for (int i = 1; i < NR; ++i) {
+            float v[8];
+            load8(cols + (i * NT + lane) * 8, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[c][e] += v[e];
+          }
+        }
+      }
+      if (sub == 0 && in[c]) put((c * NT + lane) * 8, acc[c]);
+    }
+  };
+
+  // rows of this workgroup: chunk `i` of the gate row group it belongs to
+  const int64_t group = blockIdx.x / p.spans, i = blockIdx.x % p.spans;
+  const int64_t beg = group * p.group_rows + i * p.chunk;
+  const int64_t end = min(min(beg + p.chunk, (group + 1) * p.group_rows), p.T);
+
+  for (int64_t seg = beg; seg < end; seg += p.flush_rows) {
+    const int64_t seg_end = min(seg + p.flush_rows, end);
+    for (int64_t row0 = seg; row0 < seg_end; row0 += NR) {
+      const int64_t row = row0 + sub;
+      const bool live = row < seg_end;
+      const int64_t base = row * p.C;
+      const float inv = live && p.dn ? inv_or_zero(p.r[row]) : 0.f;
+      const float invp = live && post ? inv_or_zero(p.r_post[row]) : 1.f;
+      float xh[CH][8], w[CH][8], d[CH][8], y[CH][8];
+      float s = 0.f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int j = (c * NT + lane) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xh[c][e] = w[c][e] = d[c][e] = y[c][e] = 0.f;
+        if (live && in[c]) {
+          if (p.dx_out) load8(static_cast<const R*>(p.dx_out) + base + j, d[c]);
+          if (has_y) load8(static_cast<const D*>(p.y) + base + j, y[c]);
+          if (p.dn) {
+            load8(static_cast<const R*>(p.x_out) + base + j, xh[c]);
+            load8(static_cast<const D*>(p.dn) + base + j, w[c]);
+          }
+        }
+      }
+      if (p.dn) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+          if (p.gamma && in[c]) load8(p.gamma + (c * NT + lane) * 8, g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            xh[c][e] *= inv;
+            acc_g[c][e] = fmaf(w[c][e], xh[c][e], acc_g[c][e]);
+            w[c][e] *= g[e];
+            s = fmaf(w[c][e], xh[c][e], s);
+          }
+        }
+        const float m = row_sum<NT, WG>(s, box, phase) * inv_c;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d[c][e] = fmaf(fmaf(-xh[c][e], m, w[c][e]), inv, d[c][e]);
+      }
+      s = 0.f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int j = (c * NT + lane) * 8;
+        float v[8];
+        if (p.dx) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = p.res_scale * d[c][e];
+          if (live && in[c]) store8(static_cast<R*>(p.dx) + base + j, v);
+        }
+        if (!p.block) continue;
+        float g[8], gp[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = gp[e] = 1.f;
+        if (post && in[c]) load8(p.gamma_post + j, gp);
+        if (p.gate && live && in[c])
+          load8(static_cast<const D*>(p.gate) + (int64_t)((uint32_t)row / (uint32_t)p.gate_tokens) * p.C + j, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          d[c][e] *= p.block_scale;
+          y[c][e] *= invp;
+          v[e] = d[c][e] * (y[c][e] * gp[e]);
+          acc_t[c][e] += v[e];
+          d[c][e] *= g[e];
+          acc_p[c][e] = fmaf(d[c][e], y[c][e], acc_p[c][e]);
+          d[c][e] *= gp[e];
+          s = fmaf(d[c][e], y[c][e], s);
+        }
+        if (p.gate_each && live && in[c]) store8(static_cast<D*>(p.dgate) + base + j, v);
+      }
+      if (p.block) {
+        float m = 0.f;
+        if (post) m = row_sum<NT, WG>(s, box, phase) * inv_c;
+        if (p.dy) {
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(-y[c][e], m, d[c][e]) * invp;
+            if (live && in[c]) store8(static_cast<D*>(p.dy) + base + (c * NT + lane) * 8, v);
+          }
+        }
+      }
+    }
+    if (p.dgate && !p.part_t && !p.gate_each) {
+      const int64_t gate_row = seg / p.gate_tokens;
+      fold(acc_t, [&](int j, const float (&v)[8]) { store8(static_cast<D*>(p.dgate) + gate_row * p.C + j, v); });
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc_t[c][e] = 0.f;
+    }
+  }
+  if (p.part_t)
+    fold(acc_t, [&](int j, const float (&v)[8]) { store8(p.part_t + (int64_t)blockIdx.x * p.C + j, v); });
+  if (p.part_g)
+    fold(acc_g, [&](int j, const float (&v)[8]) { store8(p.part_g + (int64_t)blockIdx.x * p.C + j, v); });
+  if (p.part_p)
+    fold(acc_p, [&](int j, const float (&v)[8]) { store8(p.part_p + (int64_t)blockIdx.x * p.C + j, v); });
+}
+
+// out[o][c] = sum over i < parts of part[o * parts + i][c], i in a fixed tree:
+// 32 columns x 32 row lanes per workgroup, then the row lanes pairwise.
+template <typename D>
+__global__ __launch_bounds__(1024) void col_sum_kernel(const float* __restrict__ part, int parts, int C,
+                                                       D* __restrict__ out) {
+  __shared__ float box[32][33];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cx;
+  const int64_t first = (int64_t)blockIdx.y * parts;
+  float s = 0.f;
+  if (c < C)
+    for (int i = ry; i < parts; i += 32) s += part[(first + i) * C + c];
+  box[ry][cx] = s;
+  __syncthreads();
+  for (int half = 16; half >= 1; half >>= 1) {
+    if (ry < half) box[ry][cx] += box[ry + half][cx];
+    __syncthreads();
+  }
+  if (ry == 0 && c < C) {
+    if constexpr (sizeof(D) == 2) out[(int64_t)blockIdx.y * C + c] = __builtin_bit_cast(__bf16, (uint16_t)pack_bf16x2(box[0][cx], 0.f));
+    else out[(int64_t)blockIdx.y * C + c] = box[0][cx];
+  }
+}
+
+// rows of the grid: at most `per_cu` workgroups on each of the 256 CUs
+int row_grid(int64_t T, int nr, int per_cu) {
+  const int64_t need = (T + nr - 1) / nr;
+  return (int)(need < 256 * per_cu ? need : 256 * per_cu);
+}
+
+template <typename R, typename D, int NT, int CH>
+hipError_t launch_norm_t(const NormParams& p, hipStream_t st) {
+  constexpr int WG = wg_of(NT);
+  const dim3 grid(row_grid(p.T, WG / NT, 2048 / WG));
+  if (p.q) hipLaunchKernelGGL((block_norm_kernel<R, D, NT, CH, true>), grid, dim3(WG), 0, st, p);
+  else hipLaunchKernelGGL((block_norm_kernel<R, D, NT, CH, false>), grid, dim3(WG), 0, st, p);
+  return hipGetLastError();
+}
+template <typename R, typename D, int NT, int CH>
+hipError_t launch_norm_grad_t(const NormGradParams& p, hipStream_t st) {
+  hipLaunchKernelGGL((block_norm_backward_kernel<R, D, NT, CH>), dim3(p.n_wg), dim3(wg_of(NT)), 0, st, p);
+  return hipGetLastError();
+}
+
+// NT lanes x CH chunks of 8 that hold a row of C elements
+template <typename F>
+hipError_t by_width(int C, F f) {
+  using std::integral_constant;
+  if (C <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (C <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (C <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+  if (C <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (C <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+}
+template <typename F>
+hipError_t by_types(int res_bf16, int io_bf16, F f) {
+  if (res_bf16) return io_bf16 ? f((__bf16*)0, (__bf16*)0) : f((__bf16*)0, (float*)0);
+  return io_bf16 ? f((float*)0, (__bf16*)0) : f((float*)0, (float*)0);
+}
+
+}  // namespace
+
+hipError_t launch_block_norm(const NormParams& p, int res_bf16, int io_bf16, hipStream_t st) {
+  if (p.T == 0) return hipSuccess;
+  return by_types(res_bf16, io_bf16, [&](auto r, auto d) {
+    return by_width(p.C, [&](auto nt, auto ch) {
+      return launch_norm_t<std::remove_pointer_t<decltype(r)>, std::remove_pointer_t<decltype(d)>,
+                           decltype(nt)::value, decltype(ch)::value>(p, st);
+    });
+  });
+}
+
+// Workgroups and rows of a backward pass (see block_norm_backward_kernel).
+NormGradGeometry norm_grad_geometry(int64_t T, int C, int64_t gate_tokens) {
+  NormGradGeometry g{};
+  const int nt = C <= 1024 ? 64 : (C <= 2048 ? 128 : (C <= 4096 ? 256 : (C <= 8192 ? 512 : 1024)));
+  const int nr = wg_of(nt) / nt;
+  const int64_t most = 256 * (1024 / wg_of(nt));   // workgroups: 16 waves on each CU
+  int64_t rows = std::max<int64_t>(1, (T + most - 1) / most);
+  rows = (rows + nr - 1) / nr * nr;
+  if (gate_tokens <= 0) {                          // no gate: one chunk after the other
+    g.chunk = g.group_rows = g.flush_rows = rows;
+    g.spans = 1;
+  } else if (gate_tokens == 1) {                   // a gate row per token: written with the token
+    g.chunk = g.group_rows = g.flush_rows = rows;
+    g.spans = 1;
+    g.gate_each = 1;
+  } else if (gate_tokens <= rows) {                // whole gate rows in a chunk
+    g.chunk = g.group_rows = rows / gate_tokens * gate_tokens;
+    g.flush_rows = gate_tokens;
+    g.spans = 1;
+  } else {                                         // a gate row over `spans` chunks
+    g.spans = (int)((gate_tokens + rows - 1) / rows);
+    g.chunk = (gate_tokens + g.spans - 1) / g.spans;
+    g.flush_rows = g.chunk;
+    g.group_rows = gate_tokens;
+    g.gate_parts = 1;
+  }
+  const int64_t groups = (T + g.group_rows - 1) / g.group_rows;
+  g.n_wg = groups * g.spans;
+  return g;
+}
+
+hipError_t launch_block_norm_backward(const NormGradParams& p, int res_bf16, int io_bf16, float* dgamma,
+                                      float* dgamma_post, hipStream_t st) {
+  hipError_t e = p.n_wg == 0 ? hipSuccess : by_types(res_bf16, io_bf16, [&](auto r, auto d) {
+    return by_width(p.C, [&](auto nt, auto ch) {
+      return launch_norm_grad_t<std::remove_pointer_t<decltype(r)>, std::remove_pointer_t<decltype(d)>,
+                                decltype(nt)::value, decltype(ch)::value>(p, st);
+    });
+  });
+  const int cb = (p.C + 31) / 32;
+  if (e == hipSuccess && p.part_g) {
+    hipLaunchKernelGGL((col_sum_kernel<float>), dim3(cb), dim3(1024), 0, st, p.part_g, (int)p.n_wg, p.C, dgamma);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && p.part_p) {
+    hipLaunchKernelGGL((col_sum_kernel<float>), dim3(cb), dim3(1024), 0, st, p.part_p, (int)p.n_wg, p.C, dgamma_post);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && p.part_t && p.n_wg > 0) {
+    const dim3 grid(cb, (unsigned)(p.n_wg / p.spans));
+    if (io_bf16)
+      hipLaunchKernelGGL((col_sum_kernel<__bf16>), grid, dim3(1024), 0, st, p.part_t, p.spans, p.C, static_cast<__bf16*>(p.dgate));
+    else
+      hipLaunchKernelGGL((col_sum_kernel<float>), grid, dim3(1024), 0, st, p.part_t, p.spans, p.C, static_cast<float*>(p.dgate));
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+namespace {
+template <typename D>
+hipError_t launch_quant_t(const D* x, int64_t n, int K, int pitch, int8_t* q, float* scale, hipStream_t st) {
+  if (pitch > 16384) {
+    hipLaunchKernelGGL((quant_long_rows_kernel<D>), dim3(row_grid(n, 1, 2)), dim3(1024), 0, st, x, n, K, pitch, q, scale);
+    return hipGetLastError();
+  }
+  const bool vec = (K * (int)sizeof(D)) % 16 == 0 && K % 8 == 0;
+  return by_width(pitch, [&](auto nt, auto ch) {
+    constexpr int NT = decltype(nt)::value, CH = decltype(ch)::value, WG = wg_of(NT);
+    const dim3 grid(row_grid(n, WG / NT, 2048 / WG));
+    if (vec) hipLaunchKernelGGL((quant_rows_kernel<D, NT, CH, true>), grid, dim3(WG), 0, st, x, n, K, pitch, q, scale);
+    else hipLaunchKernelGGL((quant_rows_kernel<D, NT, CH, false>), grid, dim3(WG), 0, st, x, n, K, pitch, q, scale);
+    return hipGetLastError();
+  });
+}
+}  // namespace
+
+hipError_t launch_quant_rows(const void* x, int64_t n, int K, int pitch, int x_bf16, int8_t* q, float* scale,
+                             hipStream_t st) {
+  if (n == 0) return hipSuccess;
+  return x_bf16 ? launch_quant_t(static_cast<const __bf16*>(x), n, K, pitch, q, scale, st)
+                : launch_quant_t(static_cast<const float*>(x), n, K, pitch, q, scale, st);
+}
+
+}  // namespace hna

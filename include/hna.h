@@ -402,6 +402,104 @@ int hna_layout_search(int32_t N, int32_t G, int32_t I, int32_t L, const float* S
                       int32_t* neuron_stats, double* J_history, int32_t* n_sweeps,
                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------ the layer's own inputs */
+
+/*
+ * The norm step between two blocks, and 8-bit products: what a calibration
+ * forward runs to give the calls above their r, r_next, g, u and x.
+ *
+ *   b  = N(y; gamma_post) = gamma_post * y / r_post,  r_post = sqrt(mean(y^2) + eps)
+ *        (b = y without gamma_post),  then  b = gate * b  with a gate
+ *   x' = res_scale x + block_scale b         rounded to the residual's type
+ *   n  = gamma * x' / r,  r = sqrt(mean(x'^2) + eps)     of x' as stored
+ *
+ * y is the block's output (attention or FFN); block_scale is the own-scaling
+ * sqrt(L) of the delayed update (section 2, eqs. (1)-(3)) or 1.
+ *   T            rows; rows of the buffers behind them are left as they are
+ *   gate_tokens  with a gate: consecutive tokens that share a gate row, >= 1
+ *                (T or more: one row for all; 1: a row per token); ignored
+ *                without one.  gate is [ceil(T / gate_tokens), hidden]
+ *   hidden       a positive multiple of 8, at most 16384
+ *   dtype        type of y, n, gate and their gradients
+ *   res_dtype    type of x, x' and their gradients
+ * gamma, gamma_post [hidden], r, r_post [T] and their gradients are fp32, as
+ * are all sums.  A row whose mean square and eps are both 0 has r = 0 and
+ * normalises to zeros.  A row that holds a NaN or an infinity affects itself
+ * only (and the sums over tokens).
+ */
+typedef struct hna_norm_dims {
+  int64_t T;
+  int64_t gate_tokens;
+  int32_t hidden;
+  int32_t dtype;
+  int32_t res_dtype;
+} hna_norm_dims;
+
+/*
+ *   x [T, hidden]; y [T, hidden] or NULL; gate, gamma, gamma_post or NULL
+ *   x_out [T, hidden] (x' ; may be x), n [T, hidden] (may be y, or NULL: only
+ *   x' and r), r [T] or NULL, r_post [T] or NULL
+ * Without y: x' = x, and gate, gamma_post, x_out and r_post are NULL and
+ * res_scale is 1.  eps >= 0.
+ */
+int hna_block_norm(const hna_norm_dims* dims, const void* x, const void* y, const void* gate,
+                   const float* gamma, const float* gamma_post, float res_scale, float block_scale,
+                   float eps, void* x_out, void* n, float* r, float* r_post, void* stream);
+
+/* The same with n as 8-bit rows for hna_quant_matmul (see hna_quant_rows):
+ * q int8 [T, hna_quant_pitch(hidden)], q_scale fp32 [T]. */
+int hna_block_norm_quant(const hna_norm_dims* dims, const void* x, const void* y, const void* gate,
+                         const float* gamma, const float* gamma_post, float res_scale,
+                         float block_scale, float eps, void* x_out, int8_t* q, float* q_scale,
+                         float* r, float* r_post, void* stream);
+
+/* Bytes of workspace hna_block_norm_backward needs (0 for invalid dims). */
+size_t hna_block_norm_workspace_bytes(const hna_norm_dims* dims);
+
+/*
+ * Gradients of hna_block_norm from those of n (dn, or NULL) and of x' (dx_out,
+ * or NULL; not both NULL), at the x', r and r_post that it wrote:
+ *   dx [T, hidden] (may be dx_out), dy [T, hidden] (may be dn, or y), dgamma,
+ *   dgamma_post [hidden], dgate [ceil(T / gate_tokens), hidden]; each may be NULL
+ * x_out, r: needed with dn.  y: needed with gamma_post or dgate.  r_post:
+ * needed with gamma_post, which is given exactly where the forward had it.
+ * dgamma, dgamma_post and dgate are written, not added to (zeros for T = 0),
+ * and summed over tokens in fp32 in a fixed order: no atomics.
+ */
+int hna_block_norm_backward(const hna_norm_dims* dims, const void* dn, const void* dx_out,
+                            const void* x_out, const void* y, const void* gate, const float* gamma,
+                            const float* gamma_post, const float* r, const float* r_post,
+                            float res_scale, float block_scale, void* dx, void* dy, float* dgamma,
+                            float* dgamma_post, void* dgate, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Bytes of an 8-bit row of K elements: K rounded up to 16 (0 for K outside 1 .. 131056). */
+int32_t hna_quant_pitch(int32_t K);
+
+/*
+ * Rows of x [rows, K] (dtype) as 8-bit integers with one scale each:
+ *   scale[i] = max_k |x[i, k]| / 127,  q[i, k] = the integer nearest to
+ *   127 x[i, k] / max_k |x[i, k]|, ties to even (decided exactly)
+ * q is int8 [rows, hna_quant_pitch(K)], the columns behind K zeros.  A row of
+ * zeros has scale 0; a row that holds a NaN or an infinity has scale NaN and
+ * zeros, so that its products are NaN.  1 <= K <= 131056, rows < 2^31.
+ * Activations are quantised per token this way, weights [N, K] per channel.
+ */
+int hna_quant_rows(int64_t rows, int32_t K, int32_t dtype, const void* x, int8_t* q, float* scale,
+                   void* stream);
+
+/*
+ * out[t, n] = (sum_k q[t, k] w[n, k]) q_scale[t] w_scale[n]
+ *   q int8 [T, K], w int8 [N, K] (K a multiple of 16, at most 131056: the
+ *   pitch of hna_quant_rows), q_scale [T], w_scale [N] fp32,
+ *   out [T, N] in out_dtype
+ * The sums are exact (int32).  1 <= N <= 2^22, 0 <= T <= 2^30, at most 2^36
+ * outputs (HNA_ERR_UNSUPPORTED above).
+ */
+int hna_quant_matmul(int64_t T, int32_t N, int32_t K, int32_t out_dtype, const int8_t* q,
+                     const float* q_scale, const int8_t* w, const float* w_scale, void* out,
+                     void* stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /*
