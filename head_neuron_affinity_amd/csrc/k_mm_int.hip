@@ -151,6 +151,164 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mm_int_kernel(const IntMmParam
   }
 }
 
+// Large products: a 256 x 256 tile on 4 waves, one per SIMD, each 128 x 128
+// (16 accumulators of 32 x 32: the largest wave tile, so that the fragment
+// reads and the copies together keep LDS busy 3/4 of the MFMA time).  64 bytes
+// of k a step in a ring of four stages.  A step is two halves of 32 bytes; the
+// fragments of the next half are read while the MFMAs of this one run:
+//   MFMA half 0, reading half 1 of step k
+//   wait for the reads and for step k + 1's copies; barrier
+//   MFMA half 1, reading half 0 of step k + 1, copying step k + 4 over step k
+// The barrier says that every wave holds step k in registers (its buffer is
+// free) and that every wave's part of step k + 1 is in LDS.  Copies past K read
+// zeros, so the loop needs no tail.
+__global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p) {
+  constexpr int BM = 256, BN = 256, BK = 64, NST = 4, STAGE = (BM + BN) * BK;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[NST * STAGE];
+  __shared__ __attribute__((aligned(16))) float sw[BM];
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w >> 1, wn = w & 1;
+
+  const int ntm = (p.N + BM - 1) / BM;
+  const int64_t ntn = (p.T + BN - 1) / BN, ntiles = ntm * ntn;
+  const int64_t per_xcd = (ntiles + 7) / 8;
+  const int64_t t = (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per_xcd || t >= ntiles) return;
+  constexpr int GM = 4;
+  const int64_t gsize = GM * ntn;
+  const int g0 = (int)(t / gsize) * GM, gm = min(GM, ntm - g0);
+  const int64_t tg = t - (t / gsize) * gsize;
+  const int n0 = (g0 + (int)(tg % gm)) * BM;
+  const int64_t t0 = tg / gm * BN;
+
+  const int64_t xb = (int64_t)(p.N - n0) * p.K, yb = (p.T - t0) * p.K;
+  const u32x4 rx = uniform_rsrc(p.w + (int64_t)n0 * p.K, xb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)xb);
+  const u32x4 ry = uniform_rsrc(p.q + t0 * p.K, yb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)yb);
+
+  // a stage holds rows of 64 bytes, the four 16-byte chunks of row r in slots
+  // c ^ (r / 4 % 4): any 16 consecutive rows put one chunk column into the 16
+  // slots of a 256-byte line.  Copy i of wave w fills rows 64 i + 16 w + l / 4.
+  const int kc = 16 * ((l & 3) ^ ((l >> 4) & 3));
+  uint32_t voff[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) voff[i] = (uint32_t)((64 * i + 16 * w + (l >> 2)) * p.K + kc);
+  const uint32_t lds0 = lds_addr(lds) + (uint32_t)w * 1024u;
+  // copy c of 8 of step kt: rows 64 (c / 2) + .. of w (c even) or q (c odd)
+  auto issue = [&](int kt, int c) __attribute__((always_inline)) {
+    const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)(kt * BK));
+    const uint32_t v = kt * BK + kc >= p.K ? kOutOfRange : voff[c >> 1];
+    dma16s(c & 1 ? ry : rx, v, soff,
+           lds0 + (uint32_t)((kt & (NST - 1)) * STAGE + (c & 1) * BM * BK + (c >> 1) * 4096));
+  };
+  i32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
+  uint4 fa[2][4], fb[2][4];
+  const int sl = (l & 31) >> 2 & 3, up = l >> 5;
+  const int ra = (wm * 128 + (l & 31)) * BK, rb = (BM + wn * 128 + (l & 31)) * BK;
+  // fragment f of 8 (4 of the channels, 4 of the tokens) of half h of step kt
+  auto rd = [&](int kt, auto half, int f) __attribute__((always_inline)) {
+    constexpr int h = decltype(half)::value;
+    const unsigned char* sb = lds + (kt & (NST - 1)) * STAGE + (((2 * h + up) ^ sl) << 4);
+    if (f < 4) fa[h][f] = *reinterpret_cast<const uint4*>(sb + ra + f * 32 * BK);
+    else fb[h][f - 4] = *reinterpret_cast<const uint4*>(sb + rb + (f - 4) * 32 * BK);
+  };
+  // the 16 MFMAs of a half, after(i) right behind the i-th
+  auto mm = [&](auto half, auto after) __attribute__((always_inline)) {
+    constexpr int h = decltype(half)::value;
+    static_for<0, 16>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      mma_int(acc[i / 4][i % 4], fa[h][i / 4], fb[h][i % 4]);
+      after(ic);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  constexpr std::integral_constant<int, 0> H0{};
+  constexpr std::integral_constant<int, 1> H1{};
+
+  sw[tid] = n0 + tid < p.N ? p.w_scale[n0 + tid] : 0.f;   // read after the loop's barriers
+  const int nk = (p.K + BK - 1) / BK;
+#pragma unroll
+  for (int s = 0; s < NST; ++s)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) issue(s, c);
+  __builtin_amdgcn_s_waitcnt(vm_wait(24));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int f = 0; f < 8; ++f) rd(0, H0, f);
+  for (int kt = 0; kt < nk; ++kt) {
+    mm(H0, [&](auto i) __attribute__((always_inline)) {
+      if constexpr (i < 8) rd(kt, H1, i);
+    });
+    asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    mm(H1, [&](auto i) __attribute__((always_inline)) {
+      if constexpr (i < 8) rd(kt + 1, H0, i);
+      else issue(kt + NST, i - 8);
+    });
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+
+  // lane l holds token (l & 31) and channels 8 a + 4 (l / 32) + e of each tile:
+  // scaled, rounded and staged through this wave's quarter of LDS, 32 tokens x
+  // 128 channels at a time, so that out is written in full runs of a token's
+  // 128 channels
+  unsigned char* stg = lds + w * (NST * STAGE / 4);
+  const int nw = n0 + wm * 128;
+  auto write = [&](auto bf16) __attribute__((always_inline)) {
+    constexpr int E = decltype(bf16)::value ? 2 : 4;      // bytes per output
+    constexpr int PITCH = 128 * E + 16;
+    static_assert(32 * PITCH <= NST * STAGE / 4, "staging fits");
+    constexpr int PER = 16 / E, LPR = 128 / PER, RPW = 64 / LPR;   // outputs and lanes per 16 bytes, rows per store
+    const bool wide = p.N % PER == 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t tj = t0 + wn * 128 + j * 32;
+      const float st = tj + (l & 31) < p.T ? p.q_scale[tj + (l & 31)] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int n = i * 32 + 8 * a + 4 * up;
+          const float4 s4 = *reinterpret_cast<const float4*>(sw + wm * 128 + n);
+          const float f[4] = {(float)acc[i][j][4 * a] * st * s4.x, (float)acc[i][j][4 * a + 1] * st * s4.y,
+                              (float)acc[i][j][4 * a + 2] * st * s4.z, (float)acc[i][j][4 * a + 3] * st * s4.w};
+          unsigned char* d = stg + (l & 31) * PITCH + n * E;
+          if constexpr (E == 2) *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+          else *reinterpret_cast<float4*>(d) = make_float4(f[0], f[1], f[2], f[3]);
+        }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < 32 / RPW; ++k) {
+        const int row = k * RPW + l / LPR, c = (l % LPR) * PER;
+        if (tj + row >= p.T || nw + c >= p.N) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(stg + row * PITCH + c * E);
+        unsigned char* o = static_cast<unsigned char*>(p.out) + ((tj + row) * p.N + nw + c) * E;
+        if (wide) {
+          *reinterpret_cast<uint4*>(o) = v;
+        } else {
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          const int m = min(PER, p.N - nw - c);
+          for (int e = 0; e < m; ++e) {
+            if constexpr (E == 2) reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+            else reinterpret_cast<uint32_t*>(o)[e] = u[e];
+          }
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  };
+  if (p.out_bf16) write(std::true_type{});
+  else write(std::false_type{});
+}
+
 template <int BM, int BN, int WGM, int WGN, int NST>
 hipError_t launch_t(const IntMmParams& p, hipStream_t st) {
   const int64_t ntiles = (int64_t)((p.N + BM - 1) / BM) * ((p.T + BN - 1) / BN);
@@ -163,6 +321,11 @@ hipError_t launch_t(const IntMmParams& p, hipStream_t st) {
 
 hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
+  const int64_t tiles = (int64_t)((p.N + 255) / 256) * ((p.T + 255) / 256);
+  if (tiles >= 256) {
+    hipLaunchKernelGGL(mm_int_big_kernel, dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(256), 0, st, p);
+    return hipGetLastError();
+  }
   return launch_t<128, 128, 2, 2, 2>(p, st);
 }
 
