@@ -163,7 +163,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mm_int_kernel(const IntMmParam
 // free) and that every wave's part of step k + 1 is in LDS.  Copies past K read
 // zeros, so the loop needs no tail.
 __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p) {
-  constexpr int BM = 256, BN = 256, BK = 64, NST = 4, STAGE = (BM + BN) * BK;
+  constexpr int BM = 256, BN = 256, BK = 128, NST = 2, STAGE = (BM + BN) * BK;
   __shared__ __attribute__((aligned(16))) unsigned char lds[NST * STAGE];
   __shared__ __attribute__((aligned(16))) float sw[BM];
   const int tid = threadIdx.x, l = tid & 63;
@@ -186,15 +186,15 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
   const u32x4 rx = uniform_rsrc(p.w + (int64_t)n0 * p.K, xb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)xb);
   const u32x4 ry = uniform_rsrc(p.q + t0 * p.K, yb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)yb);
 
-  // a stage holds rows of 64 bytes, the four 16-byte chunks of row r in slots
-  // c ^ (r / 4 % 4): any 16 consecutive rows put one chunk column into the 16
-  // slots of a 256-byte line.  Copy i of wave w fills rows 64 i + 16 w + l / 4.
-  const int kc = 16 * ((l & 3) ^ ((l >> 4) & 3));
-  uint32_t voff[4];
+  // a stage holds rows of 128 bytes (whole cache lines: copies of 64 bytes a row
+  // took twice the L2 requests and 1.2 times as long), chunk c of row r in slot
+  // c ^ swz(r).  Copy i of wave w fills rows 32 i + 8 w + l / 8.
+  const int kc = 16 * ((l & 7) ^ swz<8>(8 * w + (l >> 3)));
+  uint32_t voff[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) voff[i] = (uint32_t)((64 * i + 16 * w + (l >> 2)) * p.K + kc);
+  for (int i = 0; i < 8; ++i) voff[i] = (uint32_t)((32 * i + 8 * w + (l >> 3)) * p.K + kc);
   const uint32_t lds0 = lds_addr(lds) + (uint32_t)w * 1024u;
-  // copy c of 8 of step kt: rows 64 (c / 2) + .. of w (c even) or q (c odd)
+  // copy c of 16 of step kt: rows 32 (c / 2) + .. of w (c even) or q (c odd)
   auto issue = [&](int kt, int c) __attribute__((always_inline)) {
     const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)(kt * BK));
     const uint32_t v = kt * BK + kc >= p.K ? kOutOfRange : voff[c >> 1];
@@ -207,18 +207,17 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
   uint4 fa[2][4], fb[2][4];
-  const int sl = (l & 31) >> 2 & 3, up = l >> 5;
+  const int sl = swz<8>(l & 31), up = l >> 5;
   const int ra = (wm * 128 + (l & 31)) * BK, rb = (BM + wn * 128 + (l & 31)) * BK;
-  // fragment f of 8 (4 of the channels, 4 of the tokens) of half h of step kt
-  auto rd = [&](int kt, auto half, int f) __attribute__((always_inline)) {
-    constexpr int h = decltype(half)::value;
+  // fragment f of 8 (4 of the channels, 4 of the tokens) of quarter h of step kt
+  auto rd = [&](int kt, auto h, int f) __attribute__((always_inline)) {
     const unsigned char* sb = lds + (kt & (NST - 1)) * STAGE + (((2 * h + up) ^ sl) << 4);
-    if (f < 4) fa[h][f] = *reinterpret_cast<const uint4*>(sb + ra + f * 32 * BK);
-    else fb[h][f - 4] = *reinterpret_cast<const uint4*>(sb + rb + (f - 4) * 32 * BK);
+    if (f < 4) fa[h & 1][f] = *reinterpret_cast<const uint4*>(sb + ra + f * 32 * BK);
+    else fb[h & 1][f - 4] = *reinterpret_cast<const uint4*>(sb + rb + (f - 4) * 32 * BK);
   };
-  // the 16 MFMAs of a half, after(i) right behind the i-th
-  auto mm = [&](auto half, auto after) __attribute__((always_inline)) {
-    constexpr int h = decltype(half)::value;
+  // the 16 MFMAs of quarter h, after(i) right behind the i-th
+  auto mm = [&](auto quarter, auto after) __attribute__((always_inline)) {
+    constexpr int h = decltype(quarter)::value & 1;
     static_for<0, 16>([&](auto ic) __attribute__((always_inline)) {
       constexpr int i = decltype(ic)::value;
       mma_int(acc[i / 4][i % 4], fa[h][i / 4], fb[h][i % 4]);
@@ -226,30 +225,38 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
       __builtin_amdgcn_sched_barrier(0);
     });
   };
-  constexpr std::integral_constant<int, 0> H0{};
-  constexpr std::integral_constant<int, 1> H1{};
+  constexpr std::integral_constant<int, 0> Q0{};
+  constexpr std::integral_constant<int, 1> Q1{};
+  constexpr std::integral_constant<int, 2> Q2{};
+  constexpr std::integral_constant<int, 3> Q3{};
 
   sw[tid] = n0 + tid < p.N ? p.w_scale[n0 + tid] : 0.f;   // read after the loop's barriers
   const int nk = (p.K + BK - 1) / BK;
 #pragma unroll
   for (int s = 0; s < NST; ++s)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) issue(s, c);
-  __builtin_amdgcn_s_waitcnt(vm_wait(24));
+    for (int c = 0; c < 16; ++c) issue(s, c);
+  __builtin_amdgcn_s_waitcnt(vm_wait(16));
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int f = 0; f < 8; ++f) rd(0, H0, f);
+  for (int f = 0; f < 8; ++f) rd(0, Q0, f);
   for (int kt = 0; kt < nk; ++kt) {
-    mm(H0, [&](auto i) __attribute__((always_inline)) {
-      if constexpr (i < 8) rd(kt, H1, i);
+    mm(Q0, [&](auto i) __attribute__((always_inline)) {
+      if constexpr (i < 8) rd(kt, Q1, i);
     });
-    asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)" ::: "memory");
+    mm(Q1, [&](auto i) __attribute__((always_inline)) {
+      if constexpr (i < 8) rd(kt, Q2, i);
+    });
+    mm(Q2, [&](auto i) __attribute__((always_inline)) {
+      if constexpr (i < 8) rd(kt, Q3, i);
+    });
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    mm(H1, [&](auto i) __attribute__((always_inline)) {
-      if constexpr (i < 8) rd(kt + 1, H0, i);
-      else issue(kt + NST, i - 8);
+    mm(Q3, [&](auto i) __attribute__((always_inline)) {
+      if constexpr (i < 8) rd(kt + 1, Q0, i);
+      issue(kt + NST, i);
     });
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
