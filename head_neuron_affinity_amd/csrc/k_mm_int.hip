@@ -151,77 +151,167 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mm_int_kernel(const IntMmParam
   }
 }
 
-// Large products: a 256 x 256 tile on 4 waves, one per SIMD, each 128 x 128
-// (16 accumulators of 32 x 32: the largest wave tile, so that the fragment
-// reads and the copies together keep LDS busy 3/4 of the MFMA time).  64 bytes
-// of k a step in a ring of four stages.  A step is two halves of 32 bytes; the
-// fragments of the next half are read while the MFMAs of this one run:
-//   MFMA half 0, reading half 1 of step k
-//   wait for the reads and for step k + 1's copies; barrier
-//   MFMA half 1, reading half 0 of step k + 1, copying step k + 4 over step k
-// The barrier says that every wave holds step k in registers (its buffer is
-// free) and that every wave's part of step k + 1 is in LDS.  Copies past K read
-// zeros, so the loop needs no tail.
+// Large products: 256 x 256 tiles on 4 waves, one per SIMD, each 128 x 128 (16
+// accumulators of 32 x 32: the largest wave tile, so that fragment reads and
+// copies together keep LDS busy 3/4 of the MFMA time).  128 bytes of k a step
+// (whole cache lines) in two stages.  A step is four quarters of 32 bytes; the
+// fragments of the next quarter are read while the MFMAs of this one run:
+//   quarters 0 .. 2 of step g, reading quarters 1 .. 3
+//   wait for the reads and for step g + 1's copies; barrier
+//   quarter 3, reading quarter 0 of step g + 1 and copying step g + 2 over step g
+// The barrier says that every wave holds step g in registers (its stage is
+// free) and that every wave's part of step g + 1 is in LDS.
+// One workgroup a CU walks over its tiles, and the steps of all of them are one
+// stream: the last two steps of a tile copy the first two of the next, so the
+// copies never drain, and the output's stores overlap the next tile's MFMAs.
+// Copies have one step (about 1 us) to arrive, which the L2 keeps to and HBM
+// does not: a third stream touches the lines of step g + 3, each workgroup of
+// an XCD its share of the panels it has in common with its neighbours.
+// (The scales of a tile come with its first step, into the half of their
+// buffer that the tile before the last one had: a tile has two steps at least.)
+// Every wait counts operations in flight, so a step issues the same number of
+// them everywhere: reads past the end of an operand return zeros and stores
+// past the end of out are dropped by the buffer's range.
+struct IntTiles {
+  int ntm, gsize, ntiles, last, slots;
+};
+// where a tile lies, and its operands from its first row on
+struct IntPanels {
+  u32x4 w, q;
+  int n0, ni, ti;   // first channel; position in its group of 4 x (tokens) tiles
+  __device__ inline void set(const IntMmParams& p, const IntTiles& g, int t) {
+    const int grp = t / g.gsize, tg = t - grp * g.gsize;
+    const int gm = min(4, g.ntm - grp * 4);
+    ti = tg / max(gm, 1);
+    ni = tg - ti * gm;
+    n0 = (grp * 4 + ni) * 256;
+    const bool none = t >= g.ntiles;
+    const int64_t t0 = (int64_t)ti * 256;
+    const int64_t xb = none ? 0 : (int64_t)(p.N - n0) * p.K, yb = none ? 0 : (p.T - t0) * p.K;
+    w = uniform_rsrc(p.w + (none ? 0 : (int64_t)n0 * p.K), xb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)xb);
+    q = uniform_rsrc(p.q + (none ? 0 : t0 * p.K), yb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)yb);
+  }
+};
+
+// The lane number, computed anew: values made from it are not kept in registers
+// over the loops
+__device__ inline int lane_id() {
+  int v;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(v));
+  return v;
+}
+
+// asynchronous 4-byte copy of 64 lanes to 256 bytes of LDS
+__device__ inline void dma4s(u32x4 rs, uint32_t voff, uint32_t soff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :: "s"(m0), "v"(voff), "s"(rs), "s"(soff) : "memory");
+}
+
+// WIDE: out's rows start on 16 bytes
+template <bool BF16, bool WIDE>
 __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p) {
-  constexpr int BM = 256, BN = 256, BK = 128, NST = 2, STAGE = (BM + BN) * BK;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[NST * STAGE];
-  __shared__ __attribute__((aligned(16))) float sw[BM];
+  constexpr int BM = 256, BK = 128, STAGE = 2 * BM * BK, AHEAD = 1;
+  constexpr int E = BF16 ? 2 : 4;                       // bytes per output
+  constexpr int PITCH = 128 + 16;                       // a staged token: 128 bytes of outputs
+  constexpr int NST = 16 * E;                           // stores of a tile (per thread)
+  __shared__ __attribute__((aligned(16))) unsigned char lds[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) unsigned char stage_out[4 * 32 * PITCH];
+  __shared__ __attribute__((aligned(16))) float scales[2][2 * BM];   // of w, then q, by tile parity
+  __shared__ __attribute__((aligned(16))) uint32_t touched[BM];
   const int tid = threadIdx.x, l = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = w >> 1, wn = w & 1;
 
-  const int ntm = (p.N + BM - 1) / BM;
-  const int64_t ntn = (p.T + BN - 1) / BN, ntiles = ntm * ntn;
-  const int64_t per_xcd = (ntiles + 7) / 8;
-  const int64_t t = (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-  if ((blockIdx.x >> 3) >= per_xcd || t >= ntiles) return;
-  constexpr int GM = 4;
-  const int64_t gsize = GM * ntn;
-  const int g0 = (int)(t / gsize) * GM, gm = min(GM, ntm - g0);
-  const int64_t tg = t - (t / gsize) * gsize;
-  const int n0 = (g0 + (int)(tg % gm)) * BM;
-  const int64_t t0 = tg / gm * BN;
-
-  const int64_t xb = (int64_t)(p.N - n0) * p.K, yb = (p.T - t0) * p.K;
-  const u32x4 rx = uniform_rsrc(p.w + (int64_t)n0 * p.K, xb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)xb);
-  const u32x4 ry = uniform_rsrc(p.q + t0 * p.K, yb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)yb);
-
-  // a stage holds rows of 128 bytes (whole cache lines: copies of 64 bytes a row
-  // took twice the L2 requests and 1.2 times as long), chunk c of row r in slot
-  // c ^ swz(r).  Copy i of wave w fills rows 32 i + 8 w + l / 8.
-  const int kc = 16 * ((l & 7) ^ swz<8>(8 * w + (l >> 3)));
-  uint32_t voff[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) voff[i] = (uint32_t)((32 * i + 8 * w + (l >> 3)) * p.K + kc);
-  const uint32_t lds0 = lds_addr(lds) + (uint32_t)w * 1024u;
-  // copy c of 16 of step kt: rows 32 (c / 2) + .. of w (c even) or q (c odd)
-  auto issue = [&](int kt, int c) __attribute__((always_inline)) {
-    const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)(kt * BK));
-    const uint32_t v = kt * BK + kc >= p.K ? kOutOfRange : voff[c >> 1];
-    dma16s(c & 1 ? ry : rx, v, soff,
-           lds0 + (uint32_t)((kt & (NST - 1)) * STAGE + (c & 1) * BM * BK + (c >> 1) * 4096));
+  IntTiles g;
+  g.ntm = (p.N + 255) / 256;
+  const int ntn = (int)((p.T + 255) / 256);
+  g.ntiles = g.ntm * ntn;
+  g.gsize = 4 * ntn;
+  g.slots = gridDim.x >> 3;
+  // tiles of an XCD (workgroup ids go round the XCDs) are consecutive; its workgroups take them in turn
+  const int per_xcd = (g.ntiles + 7) / 8, first = (int)(blockIdx.x & 7) * per_xcd;
+  g.last = min(first + per_xcd, g.ntiles);
+  int tile = first + (int)(blockIdx.x >> 3);
+  if (tile >= g.last) return;
+  auto after = [&](int t) __attribute__((always_inline)) {
+    return t + g.slots < g.last ? t + g.slots : g.ntiles;   // ntiles: no tile, its copies read zeros
   };
+  const int nk = (p.K + BK - 1) / BK;
+
+  // copy c of 16 of a step: rows 32 (c / 2) + 8 w + l / 8 of w (c even) or q (c
+  // odd), chunk x of row r in slot x ^ swz(r)
+  const int kc = 16 * ((l & 7) ^ swz<8>(8 * w + (l >> 3)));
+  const uint32_t voff = (uint32_t)((8 * w + (l >> 3)) * p.K + kc), rows32 = 32u * (uint32_t)p.K;
+  const uint32_t lds0 = lds_addr(lds) + (uint32_t)w * 1024u;
+  IntPanels cp;                                           // the copies' tile, step and parity
+  int cp_tile = tile;
+  int cp_k = 0, cp_par = 0;
+  cp.set(p, g, cp_tile);
+  auto issue = [&](int buf, int c) __attribute__((always_inline)) {
+    const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)(cp_k * BK));
+    const uint32_t v = cp_k * BK + kc >= p.K ? kOutOfRange : voff + (uint32_t)(c >> 1) * rows32;
+    dma16s(c & 1 ? cp.q : cp.w, v, soff, lds0 + (uint32_t)(buf * STAGE + (c & 1) * BM * BK + (c >> 1) * 4096));
+  };
+  // the scales of the copies' tile (issued with its first step)
+  auto issue_scales = [&]() __attribute__((always_inline)) {
+    const bool none = cp_tile >= g.ntiles;
+    const int64_t sb = none ? 0 : (int64_t)(p.N - cp.n0) * 4, qb = none ? 0 : (p.T - (int64_t)cp.ti * 256) * 4;
+    const uint32_t m0 = lds_addr(scales[cp_par]) + (uint32_t)w * 256u;
+    dma4s(uniform_rsrc(p.w_scale + (none ? 0 : cp.n0), sb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)sb),
+          (uint32_t)tid * 4, 0u, m0);
+    dma4s(uniform_rsrc(p.q_scale + (none ? 0 : (int64_t)cp.ti * 256), qb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)qb),
+          (uint32_t)tid * 4, 0u, m0 + 4 * BM);
+  };
+  auto next_copy = [&]() __attribute__((always_inline)) {
+    if (++cp_k == nk) {
+      cp_k = 0;
+      cp_par ^= 1;
+      cp_tile = after(cp_tile);
+      cp.set(p, g, cp_tile);
+    }
+  };
+  // touch: a 4-byte load to LDS (never read) of each line of this workgroup's
+  // share of a step: 32 rows of w (waves 0, 1), which 8 neighbours have in
+  // common, and 64 rows of q (waves 2, 3), which 4 have
+  const uint32_t lds_t = lds_addr(touched) + (uint32_t)w * 256u;
+  IntPanels tc;
+  int tc_tile = tile;
+  int tc_k = 0;
+  uint32_t toff = 0;
+  auto touch_tile = [&]() __attribute__((always_inline)) {
+    tc.set(p, g, tc_tile);
+    const int i = lane_id(), row = w < 2 ? 32 * (tc.ti % 8) + 16 * w + i : 64 * tc.ni + 32 * (w - 2) + i;
+    toff = i < (w < 2 ? 16 : 32) ? (uint32_t)(row * p.K) : kOutOfRange;
+  };
+  auto next_touch = [&]() __attribute__((always_inline)) {
+    if (++tc_k == nk) {
+      tc_k = 0;
+      tc_tile = after(tc_tile);
+      touch_tile();
+    }
+  };
+  auto touch = [&]() __attribute__((always_inline)) {
+    dma4s(w < 2 ? tc.w : tc.q, toff,
+          __builtin_amdgcn_readfirstlane((uint32_t)(tc_k * BK)), lds_t);
+  };
+
   i32x16 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
   uint4 fa[2][4], fb[2][4];
   const int sl = swz<8>(l & 31), up = l >> 5;
   const int ra = (wm * 128 + (l & 31)) * BK, rb = (BM + wn * 128 + (l & 31)) * BK;
-  // fragment f of 8 (4 of the channels, 4 of the tokens) of quarter h of step kt
-  auto rd = [&](int kt, auto h, int f) __attribute__((always_inline)) {
-    const unsigned char* sb = lds + (kt & (NST - 1)) * STAGE + (((2 * h + up) ^ sl) << 4);
+  // fragment f of 8 (4 of the channels, 4 of the tokens) of quarter h of a stage
+  auto rd = [&](int buf, auto h, int f) __attribute__((always_inline)) {
+    const unsigned char* sb = lds + buf * STAGE + (((2 * h + up) ^ sl) << 4);
     if (f < 4) fa[h & 1][f] = *reinterpret_cast<const uint4*>(sb + ra + f * 32 * BK);
     else fb[h & 1][f - 4] = *reinterpret_cast<const uint4*>(sb + rb + (f - 4) * 32 * BK);
   };
-  // the 16 MFMAs of quarter h, after(i) right behind the i-th
-  auto mm = [&](auto quarter, auto after) __attribute__((always_inline)) {
+  // the 16 MFMAs of quarter h, behind(i) right behind the i-th
+  auto mm = [&](auto quarter, auto behind) __attribute__((always_inline)) {
     constexpr int h = decltype(quarter)::value & 1;
     static_for<0, 16>([&](auto ic) __attribute__((always_inline)) {
       constexpr int i = decltype(ic)::value;
       mma_int(acc[i / 4][i % 4], fa[h][i / 4], fb[h][i % 4]);
-      after(ic);
+      behind(ic);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -230,90 +320,127 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
   constexpr std::integral_constant<int, 2> Q2{};
   constexpr std::integral_constant<int, 3> Q3{};
 
-  sw[tid] = n0 + tid < p.N ? p.w_scale[n0 + tid] : 0.f;   // read after the loop's barriers
-  const int nk = (p.K + BK - 1) / BK;
+  issue_scales();
 #pragma unroll
-  for (int s = 0; s < NST; ++s)
+  for (int c = 0; c < 16; ++c) issue(0, c);
+  next_copy();
 #pragma unroll
-    for (int c = 0; c < 16; ++c) issue(s, c);
-  __builtin_amdgcn_s_waitcnt(vm_wait(16));
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
+  for (int c = 0; c < 16; ++c) issue(1, c);
+  next_copy();
+  touch_tile();
 #pragma unroll
-  for (int f = 0; f < 8; ++f) rd(0, Q0, f);
-  for (int kt = 0; kt < nk; ++kt) {
-    mm(Q0, [&](auto i) __attribute__((always_inline)) {
-      if constexpr (i < 8) rd(kt, Q1, i);
-    });
-    mm(Q1, [&](auto i) __attribute__((always_inline)) {
-      if constexpr (i < 8) rd(kt, Q2, i);
-    });
-    mm(Q2, [&](auto i) __attribute__((always_inline)) {
-      if constexpr (i < 8) rd(kt, Q3, i);
-    });
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    mm(Q3, [&](auto i) __attribute__((always_inline)) {
-      if constexpr (i < 8) rd(kt + 1, Q0, i);
-      issue(kt + NST, i);
-    });
+  for (int s = 0; s < 2; ++s) next_touch();
+#pragma unroll
+  for (int s = 0; s < AHEAD; ++s) {
+    touch();
+    next_touch();
   }
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(vm_wait(16 + AHEAD));       // the first step and its scales are in
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 
-  // lane l holds token (l & 31) and channels 8 a + 4 (l / 32) + e of each tile:
-  // scaled, rounded and staged through this wave's quarter of LDS, 32 tokens x
-  // 128 channels at a time, so that out is written in full runs of a token's
-  // 128 channels
-  unsigned char* stg = lds + w * (NST * STAGE / 4);
-  const int nw = n0 + wm * 128;
-  auto write = [&](auto bf16) __attribute__((always_inline)) {
-    constexpr int E = decltype(bf16)::value ? 2 : 4;      // bytes per output
-    constexpr int PITCH = 128 * E + 16;
-    static_assert(32 * PITCH <= NST * STAGE / 4, "staging fits");
-    constexpr int PER = 16 / E, LPR = 128 / PER, RPW = 64 / LPR;   // outputs and lanes per 16 bytes, rows per store
-    const bool wide = p.N % PER == 0;
+  int buf = 0, par = 0;
+  bool stored = false;                                    // the previous tile's stores may be in flight
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
+#pragma unroll
+    for (int f = 0; f < 8; ++f) rd(buf, Q0, f);           // not kept over the epilogue
+    for (int kt = 0; kt < nk; ++kt) {
+      mm(Q0, [&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < 8) rd(buf, Q1, i);
+      });
+      mm(Q1, [&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < 8) rd(buf, Q2, i);
+        if constexpr (i == 8) touch();
+      });
+      next_touch();
+      mm(Q2, [&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < 8) rd(buf, Q3, i);
+      });
+      // step g + 1's copies are older than the touch of this step and, in a
+      // tile's first step, than the stores of the tile before
+      if (kt == 0 && stored) {
+        constexpr int N1 = NST + 1 > 63 ? 63 : NST + 1;
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N1) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(1) lgkmcnt(0)" ::: "memory");
+      }
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      if (cp_k == 0) issue_scales();
+      mm(Q3, [&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < 8) rd(buf ^ 1, Q0, i);
+        issue(buf, i);
+      });
+      next_copy();
+      buf ^= 1;
+    }
+
+    // lane l holds token (l & 31) and channels 8 a + 4 (l / 32) + e of each 32 x
+    // 32 tile: scaled, rounded and staged through LDS, 32 tokens x 128 bytes at a
+    // time, so that out is written in whole lines
+    const int le = lane_id();
+    IntPanels here;
+    here.set(p, g, tile);
+    const int64_t t0 = (int64_t)here.ti * 256 + wn * 128;
+    const int n0 = here.n0 + wm * 128;
+    unsigned char* stg = stage_out + w * 32 * PITCH;
+    const float* sw = scales[par] + wm * 128;
+    const float* sq = scales[par] + BM + wn * 128;
+    constexpr int CH = 128 / E / 32;                      // 32-channel tiles per 128 bytes
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t tj = t0 + wn * 128 + j * 32;
-      const float st = tj + (l & 31) < p.T ? p.q_scale[tj + (l & 31)] : 0.f;
+      const int64_t tj = t0 + j * 32;
+      const float st = sq[j * 32 + (le & 31)];
+      const int64_t rows = min<int64_t>(32, p.T - tj), ob = rows > 0 ? rows * p.N * E : 0;
+      const __amdgpu_buffer_rsrc_t ro = buffer_rsrc(static_cast<unsigned char*>(p.out) + (rows > 0 ? tj * p.N * E : 0), (uint32_t)ob);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i0 = 0; i0 < 4; i0 += CH) {
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const int n = i * 32 + 8 * a + 4 * up;
-          const float4 s4 = *reinterpret_cast<const float4*>(sw + wm * 128 + n);
-          const float f[4] = {(float)acc[i][j][4 * a] * st * s4.x, (float)acc[i][j][4 * a + 1] * st * s4.y,
-                              (float)acc[i][j][4 * a + 2] * st * s4.z, (float)acc[i][j][4 * a + 3] * st * s4.w};
-          unsigned char* d = stg + (l & 31) * PITCH + n * E;
-          if constexpr (E == 2) *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-          else *reinterpret_cast<float4*>(d) = make_float4(f[0], f[1], f[2], f[3]);
-        }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        for (int i = i0; i < i0 + CH; ++i)
 #pragma unroll
-      for (int k = 0; k < 32 / RPW; ++k) {
-        const int row = k * RPW + l / LPR, c = (l % LPR) * PER;
-        if (tj + row >= p.T || nw + c >= p.N) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(stg + row * PITCH + c * E);
-        unsigned char* o = static_cast<unsigned char*>(p.out) + ((tj + row) * p.N + nw + c) * E;
-        if (wide) {
-          *reinterpret_cast<uint4*>(o) = v;
-        } else {
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-          const int m = min(PER, p.N - nw - c);
-          for (int e = 0; e < m; ++e) {
-            if constexpr (E == 2) reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
-            else reinterpret_cast<uint32_t*>(o)[e] = u[e];
+          for (int a = 0; a < 4; ++a) {
+            const int n = i * 32 + 8 * a + 4 * (le >> 5);
+            const float4 s4 = *reinterpret_cast<const float4*>(sw + n);
+            const float f[4] = {(float)acc[i][j][4 * a] * st * s4.x, (float)acc[i][j][4 * a + 1] * st * s4.y,
+                                (float)acc[i][j][4 * a + 2] * st * s4.z, (float)acc[i][j][4 * a + 3] * st * s4.w};
+            unsigned char* d = stg + (le & 31) * PITCH + (n - i0 * 32) * E;
+            if constexpr (BF16) *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+            else *reinterpret_cast<float4*>(d) = make_float4(f[0], f[1], f[2], f[3]);
+          }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = k * 8 + (le >> 3), c = (le & 7) * (16 / E);
+          const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * PITCH + (le & 7) * 16);
+          const int n = n0 + i0 * 32 + c;
+          if constexpr (WIDE) {
+            const uint32_t off = n < p.N ? (uint32_t)(row * p.N + n) * E : 0xfffffff0u;
+            __builtin_amdgcn_raw_buffer_store_b128(v, ro, (int)off, 0, 0);
+          } else if (row < rows) {
+            unsigned char* o = static_cast<unsigned char*>(p.out) + ((tj + row) * p.N + n) * E;
+            const int m = min(16 / E, p.N - n);
+            for (int e = 0; e < m; ++e) {
+              if constexpr (BF16) reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+              else reinterpret_cast<uint32_t*>(o)[e] = v[e];
+            }
           }
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-  };
-  if (p.out_bf16) write(std::true_type{});
-  else write(std::false_type{});
+    if constexpr (WIDE) stored = true;
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // a varying number of stores
+    tile = after(tile);
+    if (tile >= g.ntiles) break;
+    par ^= 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <int BM, int BN, int WGM, int WGN, int NST>
@@ -329,8 +456,14 @@ hipError_t launch_t(const IntMmParams& p, hipStream_t st) {
 hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
   const int64_t tiles = (int64_t)((p.N + 255) / 256) * ((p.T + 255) / 256);
-  if (tiles >= 256) {
-    hipLaunchKernelGGL(mm_int_big_kernel, dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(256), 0, st, p);
+  if (tiles >= 256 && p.K > 128) {   // two steps a tile at least: its scales are in before the tile before it ends
+    auto go = [&](auto bf16, auto wide) {
+      hipLaunchKernelGGL((mm_int_big_kernel<decltype(bf16)::value, decltype(wide)::value>), dim3(256), dim3(256), 0, st, p);
+    };
+    if (p.out_bf16 && p.N % 8 == 0) go(std::true_type{}, std::true_type{});
+    else if (p.out_bf16) go(std::true_type{}, std::false_type{});
+    else if (p.N % 4 == 0) go(std::false_type{}, std::true_type{});
+    else go(std::false_type{}, std::false_type{});
     return hipGetLastError();
   }
   return launch_t<128, 128, 2, 2, 2>(p, st);

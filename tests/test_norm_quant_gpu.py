@@ -376,7 +376,9 @@ def test_product_sizes(hna, T, N, K):
 
 @pytest.mark.parametrize("T,N,K", [(1, 14336, 4096), (1, 4096, 14336), (3, 1000, 131056), (20, 2531, 5000),
                                    (48, 4096, 1024), (150, 4096, 2048), (520, 2056, 1536), (1100, 1030, 528),
-                                   (2048, 4096, 1024), (4100, 2050, 272), (300, 9000, 640)])
+                                   (2048, 4096, 1024), (4100, 2050, 272), (300, 9000, 640),
+                                   (33000, 520, 144), (20003, 1030, 272), (70000, 261, 130), (9000, 2304, 100),
+                                   (66000, 260, 640), (257, 70000, 400)])
 def test_product_larger(hna, T, N, K):
     print(f"product T={T} N={N} K={K}", flush=True)
     g = gen(T + N + K)
