@@ -4,7 +4,10 @@
 // K < 2^17), the scales applied in fp32, one rounding to the output type.
 // The channels are the MFMA rows and the tokens its columns, so a lane ends up
 // with 4 consecutive channels of one token: out's contiguous direction.
-// Tiles of 128 x 128 on 4 waves, 128 bytes of k a step through LDS.
+// Three kernels: 256 x 256 tiles (bound by the matrix cores' power: 2.2 to 2.4
+// PFLOP/s on random data, 3.2 to 3.5 on zeros; a library product of the same
+// sizes 2.2 to 2.5), smaller tiles where those would leave CUs idle, and no
+// tiles at all for a few tokens.  The borders are in launch_mm_int.
 #include "hna_internal.h"
 #include "hna_hot.h"
 
@@ -41,19 +44,27 @@ __device__ inline void put4(const IntMmParams& p, int64_t t, int n, const int (&
   }
 }
 
-template <int BM, int BN, int WGM, int WGN, int NST>
-__global__ __launch_bounds__(64 * WGM * WGN) void mm_int_kernel(const IntMmParams p) {
-  constexpr int NW = WGM * WGN;
+// Tiles of BM x BN: KG groups of WGM x WGN waves, each group with a part of k of
+// its own (128 bytes of a step of KG 128), the steps in a ring of NST stages.
+// Several groups shorten the chain of steps where there are few tiles: a step
+// takes about 0.26 us however little it computes (a barrier, then LDS reads,
+// then the MFMAs that wait for them).  The groups' sums meet in LDS.
+template <int BM, int BN, int WGM, int WGN, int KG, int NST>
+__global__ __launch_bounds__(64 * WGM * WGN * KG) void mm_int_kernel(const IntMmParams p) {
+  constexpr int NW = WGM * WGN, NT = 64 * NW * KG;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
   constexpr int ROWS = BM + BN, BK = 128, CPR = BK / 16, RPI = 64 / CPR;
-  constexpr int STAGE = ROWS * BK;
+  constexpr int PART = ROWS * BK, STAGE = KG * PART;
   constexpr int NCP = ROWS / (RPI * NW), NCX = BM / (RPI * NW);
+  constexpr int PITCH = BM + 4;                          // ints of a token's row of sums
   static_assert(BM % (RPI * NW) == 0 && BN % (RPI * NW) == 0, "copy rounds cover whole rows");
   static_assert((NST - 2) * NCP <= 63, "copies in flight must fit the wait counter");
-  __shared__ __attribute__((aligned(16))) unsigned char lds[NST * STAGE];
+  constexpr int SUMS = BN * PITCH * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[NST * STAGE > SUMS ? NST * STAGE : SUMS];
 
   const int tid = threadIdx.x, l = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wg = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wg / NW, w = wg % NW;
   const int wm = w / WGN, wn = w % WGN;
 
   // tile of this workgroup: XCD by XCD, in groups of 4 tile rows
@@ -78,19 +89,19 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mm_int_kernel(const IntMmParam
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = i32x16{};
-  const int nk = (p.K + BK - 1) / BK;
+  const int nk = (p.K + KG * BK - 1) / (KG * BK);
 
-  // copy i of wave w fills rows RPI (NW i + w) .. + RPI - 1 of the stage (w
-  // rows first); rows past the end and bytes past K read zeros
+  // copy i of wave w fills rows RPI (NW i + w) .. + RPI - 1 of its group's part
+  // (w rows first); rows past the end and bytes past K read zeros
   uint32_t voff[NCP];
   int kc[NCP];
 #pragma unroll
   for (int i = 0; i < NCP; ++i) {
     const int r = RPI * (NW * i + w) + l / CPR;
-    kc[i] = 16 * ((l % CPR) ^ swz<CPR>(r));
+    kc[i] = grp * BK + 16 * ((l % CPR) ^ swz<CPR>(r));
     voff[i] = (uint32_t)((int64_t)(i < NCX ? r : r - BM) * p.K + kc[i]);
   }
-  const uint32_t lds0 = lds_addr(lds) + (uint32_t)w * 1024u;
+  const uint32_t lds0 = lds_addr(lds) + (uint32_t)(grp * PART + w * 1024);
   auto issue = [&](int k0, int buf) __attribute__((always_inline)) {
     const uint32_t base = lds0 + (uint32_t)(buf * STAGE);
     const uint32_t soff = __builtin_amdgcn_readfirstlane((uint32_t)k0);
@@ -100,18 +111,16 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mm_int_kernel(const IntMmParam
   };
 
 #pragma unroll
-  for (int st = 0; st < NST - 1; ++st)
-    if (st < nk) issue(st * BK, st);
+  for (int st = 0; st < NST - 1; ++st) issue(st * KG * BK, st);
+  int cur = 0;
   for (int kt = 0; kt < nk; ++kt) {
-    // step kt has landed once at most the copies of the steps after it are in
-    // flight; the barrier shows it to every wave and ends their reads of step kt - 1
-    const int ahead = min(NST - 2, nk - 1 - kt);
-    if (NST >= 4 && ahead >= 2) __builtin_amdgcn_s_waitcnt(vm_wait(2 * NCP));
-    else if (NST >= 3 && ahead >= 1) __builtin_amdgcn_s_waitcnt(vm_wait(NCP));
-    else __builtin_amdgcn_s_waitcnt(vm_wait(0));
+    // step kt has landed once at most the copies of the NST - 2 steps after it
+    // are in flight (past k they read zeros); the barrier shows it to every wave
+    // and ends their reads of step kt - 1, whose stage the next copies take
+    __builtin_amdgcn_s_waitcnt(vm_wait((NST - 2) * NCP));
     __syncthreads();
-    if (kt + NST - 1 < nk) issue((kt + NST - 1) * BK, (kt + NST - 1) % NST);
-    const unsigned char* sb = lds + (kt % NST) * STAGE;
+    issue((kt + NST - 1) * KG * BK, cur == 0 ? NST - 1 : cur - 1);
+    const unsigned char* sb = lds + cur * STAGE + grp * PART;
 #pragma unroll
     for (int ks = 0; ks < BK / 32; ++ks) {
       const int col = 2 * ks + (l >> 5);
@@ -131,23 +140,74 @@ __global__ __launch_bounds__(64 * WGM * WGN) void mm_int_kernel(const IntMmParam
 #pragma unroll
         for (int j = 0; j < TN; ++j) mma_int(acc[i][j], fa[i], fb[j]);
     }
+    cur = cur + 1 == NST ? 0 : cur + 1;
   }
 
-  // lane l holds token (l & 31) and channels 8 (v / 4) + 4 (l / 32) + v % 4 of each tile
+  // the sums as rows of a token's BM channels, in the stages: lane l holds token
+  // (l & 31) and channels 8 a + 4 (l / 32) + e of each 32 x 32 tile
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the last copies (zeros) are in
+  __syncthreads();
+  int* sums = reinterpret_cast<int*>(lds);
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int64_t tk = t0 + wn * WN + j * 32 + (l & 31);
-    if (tk >= p.T) continue;
-    const float st = p.q_scale[tk];
+  for (int x = 0; x < KG; ++x) {
+    if (grp == x) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+      for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int n = n0 + wm * WM + i * 32 + 8 * a + 4 * (l >> 5);
-        if (n >= p.N) continue;
-        const int v[4] = {acc[i][j][4 * a], acc[i][j][4 * a + 1], acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]};
-        put4(p, tk, n, v, st);
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            int4* d = reinterpret_cast<int4*>(sums + (wn * WN + j * 32 + (l & 31)) * PITCH + wm * WM + i * 32 + 8 * a + 4 * (l >> 5));
+            int4 v = make_int4(acc[i][j][4 * a], acc[i][j][4 * a + 1], acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]);
+            if (x > 0) {
+              const int4 o = *d;
+              v = make_int4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+            }
+            *d = v;
+          }
+    }
+    __syncthreads();
+  }
+  const int rows = (int)min<int64_t>(BN, p.T - t0);
+  if (p.N % 8 == 0) {
+    for (int x = tid * 8; x < BM * BN; x += NT * 8) {
+      const int r = x / BM, c = x % BM, n = n0 + c;
+      if (r >= rows || n >= p.N) continue;
+      const int4 a = *reinterpret_cast<const int4*>(sums + r * PITCH + c), b = *reinterpret_cast<const int4*>(sums + r * PITCH + c + 4);
+      const float4 s = *reinterpret_cast<const float4*>(p.w_scale + n), u = *reinterpret_cast<const float4*>(p.w_scale + n + 4);
+      const float st = p.q_scale[t0 + r];
+      const int64_t o = (t0 + r) * p.N + n;
+      const float4 v = make_float4((float)a.x * st * s.x, (float)a.y * st * s.y, (float)a.z * st * s.z, (float)a.w * st * s.w);
+      const float4 y = make_float4((float)b.x * st * u.x, (float)b.y * st * u.y, (float)b.z * st * u.z, (float)b.w * st * u.w);
+      if (p.out_bf16) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o) =
+            make_uint4(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+      } else {
+        reinterpret_cast<float4*>(static_cast<float*>(p.out) + o)[0] = v;
+        reinterpret_cast<float4*>(static_cast<float*>(p.out) + o)[1] = y;
       }
+    }
+  } else if (!p.out_bf16) {
+    for (int x = tid; x < BM * BN; x += NT) {
+      const int r = x / BM, c = x % BM, n = n0 + c;
+      if (r >= rows || n >= p.N) continue;
+      static_cast<float*>(p.out)[(t0 + r) * p.N + n] = (float)sums[r * PITCH + c] * p.q_scale[t0 + r] * p.w_scale[n];
+    }
+  } else {
+    // rows that start on any element: pairs that lie on 4 bytes, and the elements left at both ends
+    uint16_t* o = static_cast<uint16_t*>(p.out);
+    const int m = min(BM, p.N - n0);
+    auto value = [&](int r, int c) { return (float)sums[r * PITCH + c] * p.q_scale[t0 + r] * p.w_scale[n0 + c]; };
+    for (int x = tid; x < BM / 2 * BN; x += NT) {
+      const int r = x / (BM / 2), odd = (int)((t0 + r) & p.N & 1), c = 2 * (x % (BM / 2)) + odd;
+      if (r >= rows || c + 1 >= m) continue;
+      *reinterpret_cast<uint32_t*>(o + (t0 + r) * p.N + n0 + c) = pack_bf16x2(value(r, c), value(r, c + 1));
+    }
+    for (int x = tid; x < 2 * BN; x += NT) {
+      const int r = x >> 1, odd = (int)((t0 + r) & p.N & 1), c = x & 1 ? m - 1 : 0;
+      if (r < rows && (x & 1 ? (m - odd) & 1 : odd))
+        o[(t0 + r) * p.N + n0 + c] = (uint16_t)pack_bf16x2(value(r, c), 0.f);
+    }
   }
 }
 
@@ -413,21 +473,38 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
           }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
+        const int nb = n0 + i0 * 32;                      // the first of 128 / E channels
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = k * 8 + (le >> 3), c = (le & 7) * (16 / E);
-          const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * PITCH + (le & 7) * 16);
-          const int n = n0 + i0 * 32 + c;
-          if constexpr (WIDE) {
+          for (int k = 0; k < 4; ++k) {
+            const int row = k * 8 + (le >> 3), n = nb + (le & 7) * (16 / E);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * PITCH + (le & 7) * 16);
             const uint32_t off = n < p.N ? (uint32_t)(row * p.N + n) * E : 0xfffffff0u;
             __builtin_amdgcn_raw_buffer_store_b128(v, ro, (int)off, 0, 0);
-          } else if (row < rows) {
-            unsigned char* o = static_cast<unsigned char*>(p.out) + ((tj + row) * p.N + n) * E;
-            const int m = min(16 / E, p.N - n);
-            for (int e = 0; e < m; ++e) {
-              if constexpr (BF16) reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-              else reinterpret_cast<uint32_t*>(o)[e] = v[e];
-            }
+          }
+        } else if constexpr (!BF16) {
+          for (int k = 0; k < 16; ++k) {
+            const int row = k * 2 + (le >> 5), n = nb + (le & 31);
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(stg + row * PITCH + (le & 31) * 4);
+            const uint32_t off = n < p.N ? (uint32_t)(row * p.N + n) * 4u : 0xfffffff0u;
+            __builtin_amdgcn_raw_buffer_store_b32(v, ro, (int)off, 0, 0);
+          }
+        } else {
+          // rows that start on any element: pairs that lie on 4 bytes, and the
+          // elements left at both ends
+          const int m = min(64, p.N - nb);
+          for (int k = 0; k < 16; ++k) {
+            const int row = k * 2 + (le >> 5), odd = (int)((tj + row) & p.N & 1), c = 2 * (le & 31) + odd;
+            const uint16_t* s = reinterpret_cast<const uint16_t*>(stg + row * PITCH) + c;
+            const uint32_t v = (uint32_t)s[0] | ((uint32_t)s[1] << 16);
+            const uint32_t off = c + 1 < m ? (uint32_t)(row * p.N + nb + c) * 2u : 0xfffffff0u;
+            __builtin_amdgcn_raw_buffer_store_b32(v, ro, (int)off, 0, 0);
+          }
+          const int row = le & 31, odd = (int)((tj + row) & p.N & 1), c = le < 32 ? 0 : m - 1;
+          if (m > 0) {
+            const uint16_t v = reinterpret_cast<const uint16_t*>(stg + row * PITCH)[c];
+            const bool on = le < 32 ? odd : (m - odd) & 1;
+            __builtin_amdgcn_raw_buffer_store_b16(v, ro, on ? (int)((uint32_t)(row * p.N + nb + c) * 2u) : (int)0xfffffff0u, 0, 0);
           }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -443,11 +520,66 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-template <int BM, int BN, int WGM, int WGN, int NST>
+template <int BM, int BN, int WGM, int WGN, int KG, int NST>
 hipError_t launch_t(const IntMmParams& p, hipStream_t st) {
   const int64_t ntiles = (int64_t)((p.N + BM - 1) / BM) * ((p.T + BN - 1) / BN);
   const dim3 grid((unsigned)(8 * ((ntiles + 7) / 8)));
-  hipLaunchKernelGGL((mm_int_kernel<BM, BN, WGM, WGN, NST>), grid, dim3(64 * WGM * WGN), 0, st, p);
+  hipLaunchKernelGGL((mm_int_kernel<BM, BN, WGM, WGN, KG, NST>), grid, dim3(64 * WGM * WGN * KG), 0, st, p);
+  return hipGetLastError();
+}
+
+// Up to 16 tokens: bound by the weights' bytes (one token) or by latency.  A
+// workgroup holds 16 channels against all tokens, its W waves each a part of k,
+// straight from memory into 16 x 16 x 64 MFMA operands: nothing is shared, so
+// LDS only joins the waves' sums (int32: exact in any order).  Rows past N or T
+// are read from the last one and not written.
+template <int W>
+__global__ __launch_bounds__(64 * W) void mm_int_few_kernel(const IntMmParams p) {
+  constexpr int UN = 8;                                   // 64-byte steps of k in flight
+  __shared__ int part[W][4][64];
+  const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
+  const int n0 = blockIdx.x * 16, kl = 16 * (l >> 4);
+  const int8_t* pa = p.w + (int64_t)min(n0 + (l & 15), p.N - 1) * p.K;
+  const int8_t* pb = p.q + (int64_t)min(l & 15, (int)p.T - 1) * p.K;
+  i32x4 acc = {};
+  const int steps = (p.K + 63) / 64, per = (steps + W - 1) / W;
+  const int s1 = min(steps, (w + 1) * per);
+  for (int s = w * per; s < s1; s += UN) {
+    uint4 a[UN], b[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int k = (s + u) * 64 + kl;
+      const bool on = s + u < s1 && k < p.K;              // zeros of w where this wave's part or k ends
+      a[u] = make_uint4(0, 0, 0, 0);
+      if (on) a[u] = *reinterpret_cast<const uint4*>(pa + k);
+      b[u] = *reinterpret_cast<const uint4*>(pb + (on ? k : 0));
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a[u]), __builtin_bit_cast(i32x4, b[u]), acc, 0, 0, 0);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) part[w][e][l] = acc[e];
+  __syncthreads();
+  if (w > 0) return;
+  // lane l holds token l & 15 and channels 4 (l / 16) + e
+  int v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = part[0][e][l];
+#pragma unroll
+    for (int x = 1; x < W; ++x) v[e] += part[x][e][l];
+  }
+  const int t = l & 15, n = n0 + 4 * (l >> 4);
+  if (t < p.T && n < p.N) put4(p, t, n, v, p.q_scale[t]);
+}
+
+// W waves a workgroup: enough for 16 on each CU, with 256 bytes of k each
+hipError_t launch_few(const IntMmParams& p, hipStream_t st) {
+  const int wgs = (p.N + 15) / 16;
+  if (wgs * 4 >= 4096 || p.K <= 1024) hipLaunchKernelGGL(mm_int_few_kernel<4>, dim3(wgs), dim3(256), 0, st, p);
+  else if (wgs * 8 >= 4096 || p.K <= 2048) hipLaunchKernelGGL(mm_int_few_kernel<8>, dim3(wgs), dim3(512), 0, st, p);
+  else hipLaunchKernelGGL(mm_int_few_kernel<16>, dim3(wgs), dim3(1024), 0, st, p);
   return hipGetLastError();
 }
 
@@ -455,8 +587,13 @@ hipError_t launch_t(const IntMmParams& p, hipStream_t st) {
 
 hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  const int64_t tiles = (int64_t)((p.N + 255) / 256) * ((p.T + 255) / 256);
-  if (tiles >= 256 && p.K > 128) {   // two steps a tile at least: its scales are in before the tile before it ends
+  // Variants, by the tiles they make of T x N on 256 CUs; times in us of both
+  // sides of each border.
+  auto tiles = [&](int m, int n) { return (int64_t)((p.N + m - 1) / m) * ((p.T + n - 1) / n); };
+  // 256 x 256 from 160 tiles on.  T x N x K 4096 x 2531 x 1008 (160 tiles): 27
+  // against 34 with 128 x 128; 2048 x 4096 x 1024 (128 tiles): 20 against 17.
+  // Two steps a tile at least: its scales are in before the tile before it ends.
+  if (tiles(256, 256) >= 160 && p.K > 128) {
     auto go = [&](auto bf16, auto wide) {
       hipLaunchKernelGGL((mm_int_big_kernel<decltype(bf16)::value, decltype(wide)::value>), dim3(256), dim3(256), 0, st, p);
     };
@@ -466,7 +603,27 @@ hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st) {
     else go(std::false_type{}, std::false_type{});
     return hipGetLastError();
   }
-  return launch_t<128, 128, 2, 2, 2>(p, st);
+  // One round of 64 x 64 tiles, whatever T: 14336 x 4096 weights 11.4 for 1 to 64
+  // tokens (13.0 for one with mm_int_few_kernel, 22 for 64 with 32 x 32 tiles).
+  const int64_t t64 = tiles(64, 64);
+  if (t64 >= 192 && t64 <= 256 && p.K > 2048) return launch_t<64, 64, 2, 2, 2, 4>(p, st);
+  // No LDS for up to 4 tokens, or 16 with short k: 4096 x 4096 weights, 1, 4 and
+  // 16 tokens 5.6, 6.4, 8.2 against 6.2, 6.3, 6.4 with 32 x 32 tiles; 4096 x
+  // 1024, 16 tokens 3.3 against 3.8.
+  if (p.T <= (p.K <= 1024 ? 16 : 4)) return launch_few(p, st);
+  // 32 x 32 with k in four while they are one round: 4096 x 14336 weights, 64
+  // tokens (256 tiles) 15 against 23 with 64 x 64, 128 tokens 27 against 24.
+  if (tiles(32, 32) <= 256) return launch_t<32, 32, 1, 1, 4, 4>(p, st);
+  // 64 x 64 with k in two up to two rounds, four stages for one round of long k:
+  // 4096 x 14336, 128 tokens 24 against 35 with two stages, 512 tokens (two
+  // rounds) 56 against 52; 4096 x 1024, 512 tokens 6.9 against 8.5 with 128 x
+  // 128, 1024 tokens (four rounds) 13.2 against 10.8.
+  if (t64 <= 256 && p.K > 2048) return launch_t<64, 64, 2, 2, 2, 4>(p, st);
+  if (t64 <= 512) return launch_t<64, 64, 2, 2, 2, 2>(p, st);
+  // 128 x 128, k in two for one round: 4096 x 14336, 1024 tokens (256 tiles) 69
+  // to 83 against 79 to 95, 1500 tokens (384 tiles) 138 against 109.
+  if (tiles(128, 128) <= 256) return launch_t<128, 128, 2, 2, 2, 2>(p, st);
+  return launch_t<128, 128, 2, 2, 1, 2>(p, st);
 }
 
 }  // namespace hna
