@@ -8,20 +8,41 @@
 namespace hna {
 namespace rows {
 
-// ---- 8 consecutive elements, 16-byte aligned ----
-__device__ inline void load8(const __bf16* p, float (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// ---- 8 consecutive elements, 16-byte aligned: as loaded, and in fp32 ----
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__bf16> {
+  uint4 q;
+  __device__ inline void load(const __bf16* p) { q = *reinterpret_cast<const uint4*>(p); }
+  __device__ inline void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ inline void get(float (&v)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
-}
-__device__ inline void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ inline void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ inline void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ inline void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <typename T>
+__device__ inline void load8(const T* p, float (&v)[8]) {
+  Raw8<T> r;
+  r.load(p);
+  r.get(v);
 }
 __device__ inline void store8(__bf16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),

@@ -202,24 +202,38 @@ __global__ __launch_bounds__(1024) void quant_long_rows_kernel(const D* __restri
 // ends with one fp32 partial row per sum; where gate rows are shorter than a
 // chunk the chunk holds whole gate rows and writes each dgate row itself; a
 // gate row per token needs no sum.
-// col_sum_kernel adds the partial rows, in their order: no atomics.
-template <typename R, typename D, int NT, int CH>
-__global__ __launch_bounds__(wg_of(NT)) void block_norm_backward_kernel(const NormGradParams p) {
+// col_sums_kernel adds the partial rows, in their order: no atomics.
+// Bound by HBM: the next row is loaded before the present one is worked on, as
+// it lies in memory (bf16 stays packed); the gains are read from LDS.
+// Y: y is read (a block norm, or dgate is wanted).
+template <typename R, typename D, int NT, int CH, bool Y>
+__global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backward_kernel(const NormGradParams p) {
   constexpr int WG = wg_of(NT), NR = WG / NT;
+  constexpr int CMAX = NT * CH * 8;
+  __shared__ __attribute__((aligned(16))) float gains[(Y ? 2 : 1) * CMAX];   // gamma, then gamma_post
   __shared__ uint32_t box[2 * (WG / 64)];
   __shared__ float cols[NR > 1 ? NR * NT * 8 : 1];
   int phase = 0;
   const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
   const float inv_c = 1.f / (float)p.C;
-  const bool has_y = p.y != nullptr, post = p.gamma_post != nullptr;
+  const bool post = Y && p.gamma_post != nullptr;
+  for (int j = threadIdx.x * 4; j < p.C; j += WG * 4) {
+    if (p.gamma) *reinterpret_cast<float4*>(gains + j) = *reinterpret_cast<const float4*>(p.gamma + j);
+    if constexpr (Y)
+      if (post) *reinterpret_cast<float4*>(gains + CMAX + j) = *reinterpret_cast<const float4*>(p.gamma_post + j);
+  }
+  __syncthreads();
 
   bool in[CH];
-  float acc_g[CH][8], acc_p[CH][8], acc_t[CH][8];   // dgamma, dgamma_post, dgate
+  float acc_g[CH][8], acc_p[Y ? CH : 1][8], acc_t[Y ? CH : 1][8];   // dgamma, dgamma_post, dgate
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     in[c] = (c * NT + lane) * 8 < p.C;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc_g[c][e] = acc_p[c][e] = acc_t[c][e] = 0.f;
+    for (int e = 0; e < 8; ++e) {
+      acc_g[c][e] = 0.f;
+      if constexpr (Y) acc_p[c][e] = acc_t[c][e] = 0.f;
+    }
   }
 
   // sum of acc over the NR rows a workgroup holds side by side, chunk by chunk;
@@ -245,137 +259,209 @@ __global__ __launch_bounds__(wg_of(NT)) void block_norm_backward_kernel(const No
     }
   };
 
+  // a row as it lies in memory
+  struct Row {
+    Raw8<R> x[CH], dx[CH];
+    Raw8<D> dn[CH], y[Y ? CH : 1], gate[CH];
+    float r, r_post;
+  };
+  auto load = [&](Row& a, int64_t row, bool live) __attribute__((always_inline)) {
+    const int64_t base = row * p.C;
+    const int64_t gbase = p.gate && live ? (int64_t)((uint32_t)row / (uint32_t)p.gate_tokens) * p.C : 0;
+    a.r = live && p.dn ? p.r[row] : 0.f;
+    a.r_post = live && post ? p.r_post[row] : 1.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * NT + lane) * 8;
+      const bool on = live && in[c];
+      a.x[c].zero();
+      a.dx[c].zero();
+      a.dn[c].zero();
+      a.gate[c].zero();
+      if constexpr (Y) a.y[c].zero();
+      if (on && p.dn) a.x[c].load(static_cast<const R*>(p.x_out) + base + j);
+      if (on && p.dn) a.dn[c].load(static_cast<const D*>(p.dn) + base + j);
+      if (on && p.dx_out) a.dx[c].load(static_cast<const R*>(p.dx_out) + base + j);
+      if constexpr (Y)
+        if (on) a.y[c].load(static_cast<const D*>(p.y) + base + j);
+      if (on && p.gate) a.gate[c].load(static_cast<const D*>(p.gate) + gbase + j);
+    }
+  };
+
   // rows of this workgroup: chunk `i` of the gate row group it belongs to
   const int64_t group = blockIdx.x / p.spans, i = blockIdx.x % p.spans;
   const int64_t beg = group * p.group_rows + i * p.chunk;
   const int64_t end = min(min(beg + p.chunk, (group + 1) * p.group_rows), p.T);
 
-  for (int64_t seg = beg; seg < end; seg += p.flush_rows) {
+  Row cur;
+  int64_t row0 = beg, seg = beg;                          // segment: the rows up to the next write of dgate
+  if (beg < end) load(cur, beg + sub, beg + sub < min(beg + p.flush_rows, end));
+  while (row0 < end) {
     const int64_t seg_end = min(seg + p.flush_rows, end);
-    for (int64_t row0 = seg; row0 < seg_end; row0 += NR) {
-      const int64_t row = row0 + sub;
-      const bool live = row < seg_end;
-      const int64_t base = row * p.C;
-      const float inv = live && p.dn ? inv_or_zero(p.r[row]) : 0.f;
-      const float invp = live && post ? inv_or_zero(p.r_post[row]) : 1.f;
-      float xh[CH][8], w[CH][8], d[CH][8], y[CH][8];
-      float s = 0.f;
+    int64_t next = row0 + NR, next_seg = seg;
+    if (next >= seg_end) next = next_seg = seg_end;
+    Row ahead;
+    auto load_ahead = [&]() __attribute__((always_inline)) {
+      if (next < end) load(ahead, next + sub, next + sub < min(next_seg + p.flush_rows, end));
+    };
+    if constexpr (NT < 1024) load_ahead();                // 1024 lanes have 128 registers each: no room
+
+    const int64_t row = row0 + sub;
+    const bool live = row < seg_end;
+    const int64_t base = row * p.C;
+    const float inv = p.dn && live ? inv_or_zero(cur.r) : 0.f;
+    const float invp = post && live ? inv_or_zero(cur.r_post) : 1.f;
+    float d[CH][8];
+    float s = 0.f, m = 0.f;
+    if (p.dn) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int j = (c * NT + lane) * 8;
+        float x[8], w[8], g[8];
+        cur.x[c].get(x);
+        cur.dn[c].get(w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) xh[c][e] = w[c][e] = d[c][e] = y[c][e] = 0.f;
-        if (live && in[c]) {
-          if (p.dx_out) load8(static_cast<const R*>(p.dx_out) + base + j, d[c]);
-          if (has_y) load8(static_cast<const D*>(p.y) + base + j, y[c]);
-          if (p.dn) {
-            load8(static_cast<const R*>(p.x_out) + base + j, xh[c]);
-            load8(static_cast<const D*>(p.dn) + base + j, w[c]);
-          }
+        for (int e = 0; e < 8; ++e) g[e] = 1.f;
+        if (p.gamma && in[c]) load8(gains + (c * NT + lane) * 8, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float t = w[e] * (x[e] * inv);
+          acc_g[c][e] += t;
+          s = fmaf(t, g[e], s);
         }
       }
+      m = row_sum<NT, WG>(s, box, phase) * inv_c;
+    }
+    s = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int j = (c * NT + lane) * 8;
+      float v[8];
+      cur.dx[c].get(d[c]);
       if (p.dn) {
+        float x[8], w[8], g[8];
+        cur.x[c].get(x);
+        cur.dn[c].get(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = 1.f;
+        if (p.gamma && in[c]) load8(gains + j, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[c][e] = fmaf(fmaf(-(x[e] * inv), m, w[e] * g[e]), inv, d[c][e]);
+      }
+      if (p.dx) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = p.res_scale * d[c][e];
+        if (live && in[c]) store8(static_cast<R*>(p.dx) + base + j, v);
+      }
+      if (!p.block) continue;
+      float g[8];
+      cur.gate[c].get(g);
+      if (!p.gate) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = 1.f;
+      }
+      if constexpr (Y) {
+        float y[8], gp[8];
+        cur.y[c].get(y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gp[e] = 1.f;
+        if (post && in[c]) load8(gains + CMAX + j, gp);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] *= invp;
+          d[c][e] *= p.block_scale;
+          v[e] = d[c][e] * (y[e] * gp[e]);
+          acc_t[c][e] += v[e];
+          d[c][e] *= g[e];
+          acc_p[c][e] = fmaf(d[c][e], y[e], acc_p[c][e]);
+          d[c][e] *= gp[e];
+          s = fmaf(d[c][e], y[e], s);
+        }
+        if (p.gate_each && live && in[c]) store8(static_cast<D*>(p.dgate) + base + j, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[c][e] *= p.block_scale * g[e];
+      }
+    }
+    if (p.block) {
+      m = 0.f;
+      if (post) m = row_sum<NT, WG>(s, box, phase) * inv_c;
+      if (p.dy) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-          if (p.gamma && in[c]) load8(p.gamma + (c * NT + lane) * 8, g);
+          if constexpr (Y) {
+            float y[8];
+            cur.y[c].get(y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            xh[c][e] *= inv;
-            acc_g[c][e] = fmaf(w[c][e], xh[c][e], acc_g[c][e]);
-            w[c][e] *= g[e];
-            s = fmaf(w[c][e], xh[c][e], s);
+            for (int e = 0; e < 8; ++e) d[c][e] = fmaf(-(y[e] * invp), m, d[c][e]) * invp;
           }
+          if (live && in[c]) store8(static_cast<D*>(p.dy) + base + (c * NT + lane) * 8, d[c]);
         }
-        const float m = row_sum<NT, WG>(s, box, phase) * inv_c;
+      }
+    }
+    if constexpr (Y) {
+      if (next_seg != seg && p.dgate && !p.part_t && !p.gate_each) {
+        const int64_t gate_row = seg / p.gate_tokens;
+        fold(acc_t, [&](int j, const float (&v)[8]) { store8(static_cast<D*>(p.dgate) + gate_row * p.C + j, v); });
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[c][e] = fmaf(fmaf(-xh[c][e], m, w[c][e]), inv, d[c][e]);
-      }
-      s = 0.f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int j = (c * NT + lane) * 8;
-        float v[8];
-        if (p.dx) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = p.res_scale * d[c][e];
-          if (live && in[c]) store8(static_cast<R*>(p.dx) + base + j, v);
-        }
-        if (!p.block) continue;
-        float g[8], gp[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = gp[e] = 1.f;
-        if (post && in[c]) load8(p.gamma_post + j, gp);
-        if (p.gate && live && in[c])
-          load8(static_cast<const D*>(p.gate) + (int64_t)((uint32_t)row / (uint32_t)p.gate_tokens) * p.C + j, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          d[c][e] *= p.block_scale;
-          y[c][e] *= invp;
-          v[e] = d[c][e] * (y[c][e] * gp[e]);
-          acc_t[c][e] += v[e];
-          d[c][e] *= g[e];
-          acc_p[c][e] = fmaf(d[c][e], y[c][e], acc_p[c][e]);
-          d[c][e] *= gp[e];
-          s = fmaf(d[c][e], y[c][e], s);
-        }
-        if (p.gate_each && live && in[c]) store8(static_cast<D*>(p.dgate) + base + j, v);
-      }
-      if (p.block) {
-        float m = 0.f;
-        if (post) m = row_sum<NT, WG>(s, box, phase) * inv_c;
-        if (p.dy) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(-y[c][e], m, d[c][e]) * invp;
-            if (live && in[c]) store8(static_cast<D*>(p.dy) + base + (c * NT + lane) * 8, v);
-          }
-        }
+          for (int e = 0; e < 8; ++e) acc_t[c][e] = 0.f;
       }
     }
-    if (p.dgate && !p.part_t && !p.gate_each) {
-      const int64_t gate_row = seg / p.gate_tokens;
-      fold(acc_t, [&](int j, const float (&v)[8]) { store8(static_cast<D*>(p.dgate) + gate_row * p.C + j, v); });
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc_t[c][e] = 0.f;
-    }
+    if constexpr (NT == 1024) load_ahead();
+    row0 = next;
+    seg = next_seg;
+    cur = ahead;
   }
-  if (p.part_t)
-    fold(acc_t, [&](int j, const float (&v)[8]) { store8(p.part_t + (int64_t)blockIdx.x * p.C + j, v); });
-  if (p.part_g)
-    fold(acc_g, [&](int j, const float (&v)[8]) { store8(p.part_g + (int64_t)blockIdx.x * p.C + j, v); });
-  if (p.part_p)
-    fold(acc_p, [&](int j, const float (&v)[8]) { store8(p.part_p + (int64_t)blockIdx.x * p.C + j, v); });
+  const int64_t part = (int64_t)blockIdx.x * p.C;
+  if constexpr (Y) {
+    if (p.part_t) fold(acc_t, [&](int j, const float (&v)[8]) { store8(p.part_t + part + j, v); });
+    if (p.part_p) fold(acc_p, [&](int j, const float (&v)[8]) { store8(p.part_p + part + j, v); });
+  }
+  if (p.part_g) fold(acc_g, [&](int j, const float (&v)[8]) { store8(p.part_g + part + j, v); });
 }
 
-// out[o][c] = sum over i < parts of part[o * parts + i][c], i in a fixed tree:
-// 32 columns x 32 row lanes per workgroup, then the row lanes pairwise.
-template <typename D>
-__global__ __launch_bounds__(1024) void col_sum_kernel(const float* __restrict__ part, int parts, int C,
-                                                       D* __restrict__ out) {
-  __shared__ float box[32][33];
-  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cx;
-  const int64_t first = (int64_t)blockIdx.y * parts;
-  float s = 0.f;
-  if (c < C)
-    for (int i = ry; i < parts; i += 32) s += part[(first + i) * C + c];
+// Column sums of partial rows, up to three sets in one launch: blockIdx.y 0 is
+// dgamma, 1 dgamma_post (each over all `parts` rows), 2 + g row g of dgate (over
+// its `spans` rows).  A workgroup has 32 columns x 128 row lanes, 4 columns a
+// lane; the lanes' sums are added in a fixed tree.
+struct ColSums {
+  const float *part_g, *part_p, *part_t;
+  float *dgamma, *dgamma_post;
+  void* dgate;
+  int parts, spans, C, bf16;
+};
+__global__ __launch_bounds__(1024) void col_sums_kernel(const ColSums a) {
+  __shared__ float4 box[128][8];
+  const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3, which = blockIdx.y;
+  const int c = blockIdx.x * 32 + cx * 4;
+  const float* part = which == 0 ? a.part_g : (which == 1 ? a.part_p : a.part_t);
+  if (!part) return;
+  const int n = which < 2 ? a.parts : a.spans;
+  const int64_t first = which < 2 ? 0 : (int64_t)(which - 2) * a.spans;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < a.C)
+    for (int i = ry; i < n; i += 128) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (first + i) * a.C + c);
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
   box[ry][cx] = s;
   __syncthreads();
-  for (int half = 16; half >= 1; half >>= 1) {
-    if (ry < half) box[ry][cx] += box[ry + half][cx];
+  for (int half = 64; half >= 1; half >>= 1) {
+    if (ry < half) {
+      const float4 u = box[ry][cx], v = box[ry + half][cx];
+      box[ry][cx] = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
+    }
     __syncthreads();
   }
-  if (ry == 0 && c < C) {
-    if constexpr (sizeof(D) == 2) out[(int64_t)blockIdx.y * C + c] = __builtin_bit_cast(__bf16, (uint16_t)pack_bf16x2(box[0][cx], 0.f));
-    else out[(int64_t)blockIdx.y * C + c] = box[0][cx];
-  }
+  if (ry > 0 || c >= a.C) return;
+  s = box[0][cx];
+  if (which >= 2 && a.bf16)
+    *reinterpret_cast<uint2*>(static_cast<__bf16*>(a.dgate) + (int64_t)(which - 2) * a.C + c) =
+        make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  else
+    *reinterpret_cast<float4*>((which == 0 ? a.dgamma : which == 1 ? a.dgamma_post
+                                : static_cast<float*>(a.dgate) + (int64_t)(which - 2) * a.C) + c) = s;
 }
 
 // rows of the grid: at most `per_cu` workgroups on each of the 256 CUs
@@ -394,7 +480,9 @@ hipError_t launch_norm_t(const NormParams& p, hipStream_t st) {
 }
 template <typename R, typename D, int NT, int CH>
 hipError_t launch_norm_grad_t(const NormGradParams& p, hipStream_t st) {
-  hipLaunchKernelGGL((block_norm_backward_kernel<R, D, NT, CH>), dim3(p.n_wg), dim3(wg_of(NT)), 0, st, p);
+  const dim3 grid((unsigned)p.n_wg), wg(wg_of(NT));
+  if (p.y) hipLaunchKernelGGL((block_norm_backward_kernel<R, D, NT, CH, true>), grid, wg, 0, st, p);
+  else hipLaunchKernelGGL((block_norm_backward_kernel<R, D, NT, CH, false>), grid, wg, 0, st, p);
   return hipGetLastError();
 }
 
@@ -432,7 +520,7 @@ NormGradGeometry norm_grad_geometry(int64_t T, int C, int64_t gate_tokens) {
   NormGradGeometry g{};
   const int nt = C <= 1024 ? 64 : (C <= 2048 ? 128 : (C <= 4096 ? 256 : (C <= 8192 ? 512 : 1024)));
   const int nr = wg_of(nt) / nt;
-  const int64_t most = 256 * (1024 / wg_of(nt));   // workgroups: 16 waves on each CU
+  const int64_t most = nt <= 256 ? 512 : 256;      // workgroups at once: registers leave 8 waves a CU (16 for 1024)
   int64_t rows = std::max<int64_t>(1, (T + most - 1) / most);
   rows = (rows + nr - 1) / nr * nr;
   if (gate_tokens <= 0) {                          // no gate: one chunk after the other
@@ -466,21 +554,10 @@ hipError_t launch_block_norm_backward(const NormGradParams& p, int res_bf16, int
                                 decltype(nt)::value, decltype(ch)::value>(p, st);
     });
   });
-  const int cb = (p.C + 31) / 32;
-  if (e == hipSuccess && p.part_g) {
-    hipLaunchKernelGGL((col_sum_kernel<float>), dim3(cb), dim3(1024), 0, st, p.part_g, (int)p.n_wg, p.C, dgamma);
-    e = hipGetLastError();
-  }
-  if (e == hipSuccess && p.part_p) {
-    hipLaunchKernelGGL((col_sum_kernel<float>), dim3(cb), dim3(1024), 0, st, p.part_p, (int)p.n_wg, p.C, dgamma_post);
-    e = hipGetLastError();
-  }
-  if (e == hipSuccess && p.part_t && p.n_wg > 0) {
-    const dim3 grid(cb, (unsigned)(p.n_wg / p.spans));
-    if (io_bf16)
-      hipLaunchKernelGGL((col_sum_kernel<__bf16>), grid, dim3(1024), 0, st, p.part_t, p.spans, p.C, static_cast<__bf16*>(p.dgate));
-    else
-      hipLaunchKernelGGL((col_sum_kernel<float>), grid, dim3(1024), 0, st, p.part_t, p.spans, p.C, static_cast<float*>(p.dgate));
+  if (e == hipSuccess && (p.part_g || p.part_p || p.part_t)) {
+    const ColSums a{p.part_g, p.part_p, p.part_t, dgamma, dgamma_post, p.dgate, (int)p.n_wg, p.spans, p.C, io_bf16};
+    const unsigned sets = p.part_t ? 2 + (unsigned)(p.n_wg / p.spans) : 2;
+    hipLaunchKernelGGL(col_sums_kernel, dim3((p.C + 31) / 32, sets), dim3(1024), 0, st, a);
     e = hipGetLastError();
   }
   return e;
