@@ -217,13 +217,6 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
   const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
   const float inv_c = 1.f / (float)p.C;
   const bool post = Y && p.gamma_post != nullptr;
-  for (int j = threadIdx.x * 4; j < p.C; j += WG * 4) {
-    if (p.gamma) *reinterpret_cast<float4*>(gains + j) = *reinterpret_cast<const float4*>(p.gamma + j);
-    if constexpr (Y)
-      if (post) *reinterpret_cast<float4*>(gains + CMAX + j) = *reinterpret_cast<const float4*>(p.gamma_post + j);
-  }
-  __syncthreads();
-
   bool in[CH];
   float acc_g[CH][8], acc_p[Y ? CH : 1][8], acc_t[Y ? CH : 1][8];   // dgamma, dgamma_post, dgate
 #pragma unroll
@@ -296,6 +289,12 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
   Row cur;
   int64_t row0 = beg, seg = beg;                          // segment: the rows up to the next write of dgate
   if (beg < end) load(cur, beg + sub, beg + sub < min(beg + p.flush_rows, end));
+  for (int j = threadIdx.x * 4; j < p.C; j += WG * 4) {
+    if (p.gamma) *reinterpret_cast<float4*>(gains + j) = *reinterpret_cast<const float4*>(p.gamma + j);
+    if constexpr (Y)
+      if (post) *reinterpret_cast<float4*>(gains + CMAX + j) = *reinterpret_cast<const float4*>(p.gamma_post + j);
+  }
+  __syncthreads();
   while (row0 < end) {
     const int64_t seg_end = min(seg + p.flush_rows, end);
     int64_t next = row0 + NR, next_seg = seg;
