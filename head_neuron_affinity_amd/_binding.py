@@ -572,55 +572,86 @@ def affinity_up_static(dims: hna_dims, a, g, u, r, r_next, M, wd_sq, group_of_he
 
 
 # ------------------------------------- norm step between blocks, 8-bit products
+# These calls are made token by token too, where a call's time is the host's, so
+# their checks are written for speed: sizes compared as tuples, devices by index,
+# pointers and streams as plain integers.
 class _on:
     """The tensors' device as the current one while a call is enqueued, so that
-    launches go to their GPU and its current stream."""
+    launches go to their GPU and its current stream (the context's value)."""
+    __slots__ = ("index", "guard")
 
     def __init__(self, *ts):
-        _need_cuda(*ts)
-        given = [t for t in ts if t is not None]
-        self.device = given[0].device
-        if any(t.device != self.device for t in given):
-            raise ValueError("all tensors must live on the same GPU")
-        same = self.device.index == torch.cuda.current_device()
-        self.guard = None if same else torch.cuda.device(self.device)
+        index = None
+        for t in ts:
+            if t is not None:
+                i = t.get_device()
+                if i < 0:
+                    raise ValueError("all tensors must live on the GPU")
+                if not t.is_contiguous():
+                    raise ValueError("all tensors must be contiguous")
+                if index is None:
+                    index = i
+                elif i != index:
+                    raise ValueError("all tensors must live on the same GPU")
+        self.index = index
+        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return _stream(self.device)
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
 
-def _norm_dims(like, dtype, gate, gate_tokens, name) -> hna_norm_dims:
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _is(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype):
+    """_expect with `shape` a tuple of ints, the whole shape."""
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        _expect(t, name, shape, dtype)
+
+
+_CODE = {torch.bfloat16: HNA_BF16, torch.float32: HNA_F32}
+
+
+def _code(dtype: torch.dtype) -> int:
+    code = _CODE.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32 only")
+    return code
+
+
+def _norm_dims(like, dtype: torch.dtype, gate, gate_tokens, name) -> hna_norm_dims:
     """dims of a norm step over rows of `like` [T, hidden], the residual; checks the gate."""
     if like.dim() != 2:
         raise ValueError(f"{name}: shape {tuple(like.shape)}, expected [T, hidden]")
     T, hidden = like.shape
     if gate is None:
-        return hna_norm_dims(T, 1, hidden, dtype, _dtype_code(like))
+        return hna_norm_dims(T, 1, hidden, _code(dtype), _code(like.dtype))
     gate_tokens = max(T, 1) if gate_tokens is None else int(gate_tokens)
     if gate_tokens < 1:
         raise ValueError(f"gate_tokens: {gate_tokens} < 1")
-    _expect(gate, "gate", (-(-T // gate_tokens), hidden), torch.bfloat16 if dtype == HNA_BF16 else torch.float32)
-    return hna_norm_dims(T, gate_tokens, hidden, dtype, _dtype_code(like))
+    _is(gate, "gate", (-(-T // gate_tokens), hidden), dtype)
+    return hna_norm_dims(T, gate_tokens, hidden, _code(dtype), _code(like.dtype))
 
 
-def _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, dtype, outs):
+def _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, dtype, x_out, r, r_post):
     """Checks a forward norm step's arguments; (dims, dtype of y and n)."""
     dt = y.dtype if y is not None else (dtype or x.dtype)
-    dims = _norm_dims(x, HNA_BF16 if dt == torch.bfloat16 else HNA_F32, gate, gate_tokens, "x")
-    if dt not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"unsupported dtype {dt}: bf16 or fp32 only")
-    T, C = x.shape
-    _expect(y, "y", (T, C), dt)
-    _expect(gamma, "gamma", (C,), torch.float32)
-    _expect(gamma_post, "gamma_post", (C,), torch.float32)
-    for t, name, shape, want in outs(T, C, dt):
-        _expect(t, name, shape, want)
+    dims = _norm_dims(x, dt, gate, gate_tokens, "x")
+    T, C = rows = x.shape
+    f32 = torch.float32
+    _is(y, "y", rows, dt)
+    _is(gamma, "gamma", (C,), f32)
+    _is(gamma_post, "gamma_post", (C,), f32)
+    _is(x_out, "x_out", rows, x.dtype)
+    _is(r, "r", (T,), f32)
+    _is(r_post, "r_post", (T,), f32)
     if y is None and (gate is not None or gamma_post is not None or res_scale != 1.0):
         raise ValueError("without y, gate and gamma_post must be None and res_scale 1")
     return dims, dt
@@ -636,22 +667,20 @@ def block_norm(x, y=None, gamma=None, *, gamma_post=None, gate=None, gate_tokens
     gate [ceil(T / gate_tokens), hidden] (default one row for all tokens).  n has y's type (`dtype`,
     or x's, without y).  Returns (x', n, r [T], r_post [T] or None); x_out may be x and n may be y.
     """
-    dims, dt = _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, dtype,
-                          lambda T, C, dt: ((x_out, "x_out", (T, C), x.dtype), (n, "n", (T, C), dt),
-                                            (r, "r", (T,), torch.float32),
-                                            (r_post, "r_post", (T,), torch.float32)))
+    dims, dt = _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, dtype, x_out, r, r_post)
+    _is(n, "n", x.shape, dt)
     with _on(x, y, gamma, gamma_post, gate, x_out, n, r, r_post) as stream:
         if x_out is None and y is not None:
             x_out = torch.empty_like(x)
         if n is None:
-            n = torch.empty(x.shape, dtype=dt, device=x.device)
+            n = torch.empty_like(x, dtype=dt)
         if r is None:
             r = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
         if r_post is None and gamma_post is not None:
             r_post = torch.empty_like(r)
-        _check(lib().hna_block_norm(ctypes.byref(dims), _ptr(x), _ptr(y), _ptr(gate), _ptr(gamma),
-                                    _ptr(gamma_post), float(res_scale), float(block_scale), float(eps),
-                                    _ptr(x_out), _ptr(n), _ptr(r), _ptr(r_post), stream), "hna_block_norm")
+        _check(lib().hna_block_norm(ctypes.byref(dims), _at(x), _at(y), _at(gate), _at(gamma), _at(gamma_post),
+                                    res_scale, block_scale, eps, _at(x_out), _at(n), _at(r), _at(r_post),
+                                    stream), "hna_block_norm")
     return (x if y is None else x_out), n, r, r_post
 
 
@@ -659,28 +688,25 @@ def block_norm_quant(x, y=None, gamma=None, *, gamma_post=None, gate=None, gate_
                      res_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6, x_out=None,
                      q=None, q_scale=None, r=None, r_post=None):
     """block_norm with n as 8-bit rows (see quant_rows): returns (x', q, q_scale, r, r_post)."""
-    pitch = lambda C: -(-C // 16) * 16  # noqa: E731
-    dims, _ = _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, None,
-                         lambda T, C, dt: ((x_out, "x_out", (T, C), x.dtype), (q, "q", (T, pitch(C)), torch.int8),
-                                           (q_scale, "q_scale", (T,), torch.float32),
-                                           (r, "r", (T,), torch.float32),
-                                           (r_post, "r_post", (T,), torch.float32)))
+    dims, _ = _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, None, x_out, r, r_post)
+    T, C = x.shape
+    pitch = (C + 15) // 16 * 16
+    _is(q, "q", (T, pitch), torch.int8)
+    _is(q_scale, "q_scale", (T,), torch.float32)
     with _on(x, y, gamma, gamma_post, gate, x_out, q, q_scale, r, r_post) as stream:
-        T, C = x.shape
         if x_out is None and y is not None:
             x_out = torch.empty_like(x)
         if q is None:
-            q = torch.empty((T, pitch(C)), dtype=torch.int8, device=x.device)
+            q = torch.empty((T, pitch), dtype=torch.int8, device=x.device)
         if q_scale is None:
             q_scale = torch.empty(T, dtype=torch.float32, device=x.device)
         if r is None:
-            r = torch.empty(T, dtype=torch.float32, device=x.device)
+            r = torch.empty_like(q_scale)
         if r_post is None and gamma_post is not None:
-            r_post = torch.empty_like(r)
-        _check(lib().hna_block_norm_quant(ctypes.byref(dims), _ptr(x), _ptr(y), _ptr(gate), _ptr(gamma),
-                                          _ptr(gamma_post), float(res_scale), float(block_scale),
-                                          float(eps), _ptr(x_out), _ptr(q), _ptr(q_scale), _ptr(r),
-                                          _ptr(r_post), stream), "hna_block_norm_quant")
+            r_post = torch.empty_like(q_scale)
+        _check(lib().hna_block_norm_quant(ctypes.byref(dims), _at(x), _at(y), _at(gate), _at(gamma),
+                                          _at(gamma_post), res_scale, block_scale, eps, _at(x_out), _at(q),
+                                          _at(q_scale), _at(r), _at(r_post), stream), "hna_block_norm_quant")
     return (x if y is None else x_out), q, q_scale, r, r_post
 
 
@@ -699,48 +725,56 @@ def block_norm_backward(x_out, r, *, dn=None, dx_out=None, gamma=None, y=None, g
     dgamma_post (with gamma_post), dgate (with gate and y); None for the others.  dx may be dx_out,
     dy may be dn or y.
     """
-    dt = next((t.dtype for t in (y, dn, gate, dy) if t is not None), x_out.dtype)
-    if dt not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"unsupported dtype {dt}: bf16 or fp32 only")
+    dt = x_out.dtype
+    for t in (y, dn, gate, dy):
+        if t is not None:
+            dt = t.dtype
+            break
     if dn is None and dx_out is None:
         raise ValueError("dn and dx_out are both None")
-    dims = _norm_dims(x_out, HNA_BF16 if dt == torch.bfloat16 else HNA_F32, gate, gate_tokens, "x_out")
-    T, C = x_out.shape
-    f32 = torch.float32
-    want_dy = (y is not None or dy is not None) if want_dy is None else want_dy
+    dims = _norm_dims(x_out, dt, gate, gate_tokens, "x_out")
+    T, C = rows = x_out.shape
+    f32, res = torch.float32, x_out.dtype
+    if want_dy is None:
+        want_dy = y is not None or dy is not None
     if gamma_post is not None and (y is None or r_post is None):
         raise ValueError("gamma_post needs y and r_post")
-    for t, name, shape, want in ((dn, "dn", (T, C), dt), (dx_out, "dx_out", (T, C), x_out.dtype),
-                                 (y, "y", (T, C), dt), (gamma, "gamma", (C,), f32),
-                                 (gamma_post, "gamma_post", (C,), f32), (r, "r", (T,), f32),
-                                 (r_post, "r_post", (T,), f32), (dx, "dx", (T, C), x_out.dtype),
-                                 (dy, "dy", (T, C), dt), (dgamma, "dgamma", (C,), f32),
-                                 (dgamma_post, "dgamma_post", (C,), f32)):
-        _expect(t, name, shape, want)
+    if dgate is not None and (gate is None or y is None):
+        raise ValueError("dgate needs gate and y")
+    _is(dn, "dn", rows, dt)
+    _is(dx_out, "dx_out", rows, res)
+    _is(y, "y", rows, dt)
+    _is(gamma, "gamma", (C,), f32)
+    _is(gamma_post, "gamma_post", (C,), f32)
+    _is(r, "r", (T,), f32)
+    _is(r_post, "r_post", (T,), f32)
+    _is(dx, "dx", rows, res)
+    _is(dy, "dy", rows, dt)
+    _is(dgamma, "dgamma", (C,), f32)
+    _is(dgamma_post, "dgamma_post", (C,), f32)
     if dgate is not None:
-        if gate is None or y is None:
-            raise ValueError("dgate needs gate and y")
-        _expect(dgate, "dgate", gate.shape, dt)
+        _is(dgate, "dgate", gate.shape, dt)
     with _on(x_out, r, dn, dx_out, gamma, y, gamma_post, r_post, gate, dx, dy, dgamma, dgamma_post, dgate,
              workspace) as stream:
-        dev = x_out.device
         if dx is None:
             dx = torch.empty_like(x_out)
         if dy is None and want_dy:
-            dy = torch.empty((T, C), dtype=dt, device=dev)
+            dy = torch.empty_like(x_out, dtype=dt)
         if dgamma is None and gamma is not None and dn is not None:
             dgamma = torch.empty_like(gamma)
         if dgamma_post is None and gamma_post is not None:
             dgamma_post = torch.empty_like(gamma_post)
         if dgate is None and gate is not None and y is not None:
             dgate = torch.empty_like(gate)
+        L = lib()
         if workspace is None:
-            workspace = torch.empty(max(block_norm_workspace_bytes(dims), 16), dtype=torch.uint8, device=dev)
-        _check(lib().hna_block_norm_backward(
-            ctypes.byref(dims), _ptr(dn), _ptr(dx_out), _ptr(x_out), _ptr(y), _ptr(gate), _ptr(gamma),
-            _ptr(gamma_post), _ptr(r), _ptr(r_post), float(res_scale), float(block_scale), _ptr(dx),
-            _ptr(dy), _ptr(dgamma), _ptr(dgamma_post), _ptr(dgate), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), stream), "hna_block_norm_backward")
+            workspace = torch.empty(L.hna_block_norm_workspace_bytes(ctypes.byref(dims)) or 16,
+                                    dtype=torch.uint8, device=x_out.device)
+        _check(L.hna_block_norm_backward(
+            ctypes.byref(dims), _at(dn), _at(dx_out), _at(x_out), _at(y), _at(gate), _at(gamma), _at(gamma_post),
+            _at(r), _at(r_post), res_scale, block_scale, _at(dx), _at(dy), _at(dgamma), _at(dgamma_post),
+            _at(dgate), _at(workspace), workspace.numel() * workspace.element_size(), stream),
+            "hna_block_norm_backward")
     return {"dx": dx, "dy": dy if want_dy else None, "dgamma": dgamma, "dgamma_post": dgamma_post,
             "dgate": dgate}
 
@@ -756,17 +790,16 @@ def quant_rows(x, q=None, scale=None):
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected [rows, K]")
     rows, K = x.shape
-    code = _dtype_code(x)
-    pitch = -(-K // 16) * 16
-    _expect(q, "q", (rows, pitch), torch.int8)
-    _expect(scale, "scale", (rows,), torch.float32)
+    code = _code(x.dtype)
+    pitch = (K + 15) // 16 * 16
+    _is(q, "q", (rows, pitch), torch.int8)
+    _is(scale, "scale", (rows,), torch.float32)
     with _on(x, q, scale) as stream:
         if q is None:
             q = torch.empty((rows, pitch), dtype=torch.int8, device=x.device)
         if scale is None:
             scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-        _check(lib().hna_quant_rows(int(rows), int(K), code, _ptr(x), _ptr(q), _ptr(scale), stream),
-               "hna_quant_rows")
+        _check(lib().hna_quant_rows(rows, K, code, _at(x), _at(q), _at(scale), stream), "hna_quant_rows")
     return q, scale
 
 
@@ -777,19 +810,17 @@ def quant_matmul(q, q_scale, w, w_scale, out=None, dtype: torch.dtype = torch.bf
         raise ValueError("q and w must be [T, K] and [N, K]")
     T, K = q.shape
     N = w.shape[0]
-    _expect(q, "q", (T, K), torch.int8)
-    _expect(w, "w", (N, K), torch.int8)
-    _expect(q_scale, "q_scale", (T,), torch.float32)
-    _expect(w_scale, "w_scale", (N,), torch.float32)
+    _is(q, "q", (T, K), torch.int8)
+    _is(w, "w", (N, K), torch.int8)
+    _is(q_scale, "q_scale", (T,), torch.float32)
+    _is(w_scale, "w_scale", (N,), torch.float32)
     if out is not None:
         dtype = out.dtype
-        _expect(out, "out", (T, N), dtype)
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"unsupported dtype {dtype}: bf16 or fp32 only")
+        _is(out, "out", (T, N), dtype)
+    code = _code(dtype)
     with _on(q, q_scale, w, w_scale, out) as stream:
         if out is None:
             out = torch.empty((T, N), dtype=dtype, device=q.device)
-        _check(lib().hna_quant_matmul(int(T), int(N), int(K), HNA_BF16 if dtype == torch.bfloat16 else HNA_F32,
-                                      _ptr(q), _ptr(q_scale), _ptr(w), _ptr(w_scale), _ptr(out), stream),
+        _check(lib().hna_quant_matmul(T, N, K, code, _at(q), _at(q_scale), _at(w), _at(w_scale), _at(out), stream),
                "hna_quant_matmul")
     return out
