@@ -115,14 +115,15 @@ __device__ inline uint32_t row_max_bits(uint32_t v, uint32_t* box, int& phase) {
 
 // ---- a row as 8-bit integers ----
 // q = the integer nearest to 127 v / top, top = max|v| of the row, ties to even,
-// exactly: t = v * (127 / top) is within 2e-5 of the quotient (two roundings,
-// |t| <= 127), so its nearest integer is right unless t lies that close to a
-// half; there the sign of 254 |v| - (2 k + 1) top decides, k = floor |t|.  With
+// exactly: v * (127 / top) is within 2e-5 of the quotient (two roundings, at most
+// 127), so its nearest integer is right unless it lies that close to a half;
+// there the sign of 254 |v| - (2 k + 1) top decides, k the integer below.  With
 // b + bl = (2 k + 1) top exactly (b rounded, bl the remainder), 254 |v| - b is
 // a difference of close numbers of at most 32 bits and comes out exactly, so
 // the sign of its difference with bl is exact too.
 // `pre` is a power of two that keeps top within 2^-100 .. 2^100, so that
-// neither 127 / top nor the products leave the range of fp32.
+// neither 127 / top nor the products leave the range of fp32; 1 for nearly
+// every row.
 struct RowScale {
   float scale;   // what one step of q stands for: top / 127 (NaN for a row with a NaN or an infinity)
   float inv;     // 127 / (top pre), 0 where every q is 0
@@ -146,16 +147,35 @@ __device__ inline float quant_exact(float v, float t, const RowScale& s) {
   const float q = k + ((d > 0.f || (d == 0.f && ((int)k & 1))) ? 1.f : 0.f);
   return copysignf(q, v);
 }
-// 8 elements to 8 bytes
-__device__ inline uint2 quant8(const float (&v)[8], const RowScale& s) {
-  uint32_t w[2] = {0u, 0u};
+// 8 elements to 8 bytes.  Adding 1.5 * 2^23 rounds to an integer, whose low
+// byte is the sum's.
+__device__ inline uint2 quant8(const float (&x)[8], const RowScale& s) {
   if (s.inv == 0.f) return make_uint2(0u, 0u);
+  constexpr float kInt = 12582912.f;
+  float v[8], r[8], off[8], worst = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = x[e];
+  if (s.pre != 1.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= s.pre;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float u = v[e] * s.pre, t = u * s.inv;
-    float q = rintf(t);
-    if (fabsf(fabsf(t - q) - 0.5f) < 1e-4f) q = quant_exact(u, t, s);
-    w[e >> 2] |= ((uint32_t)(int)q & 0xffu) << (8 * (e & 3));
+    r[e] = fmaf(v[e], s.inv, kInt);
+    off[e] = fabsf(fmaf(v[e], s.inv, kInt - r[e]));
+    worst = fmaxf(worst, off[e]);
+  }
+  if (worst > 0.4999f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (off[e] > 0.4999f) r[e] = kInt + quant_exact(v[e], v[e] * s.inv, s);
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(r[4 * h + 1]), __float_as_uint(r[4 * h]), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(r[4 * h + 3]), __float_as_uint(r[4 * h + 2]), 0x04000c0cu);
+    w[h] = lo | hi;
   }
   return make_uint2(w[0], w[1]);
 }

@@ -496,6 +496,18 @@ hipError_t by_width(int C, F f) {
   if (C <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
   return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
 }
+// the same for the 8-bit rows, which need few registers: one wave up to 2048
+template <typename F>
+hipError_t by_quant_width(int C, F f) {
+  using std::integral_constant;
+  if (C <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (C <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (C <= 1536) return f(integral_constant<int, 64>{}, integral_constant<int, 3>{});
+  if (C <= 2048) return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+  if (C <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (C <= 8192) return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  return f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+}
 template <typename F>
 hipError_t by_types(int res_bf16, int io_bf16, F f) {
   if (res_bf16) return io_bf16 ? f((__bf16*)0, (__bf16*)0) : f((__bf16*)0, (float*)0);
@@ -570,7 +582,7 @@ hipError_t launch_quant_t(const D* x, int64_t n, int K, int pitch, int8_t* q, fl
     return hipGetLastError();
   }
   const bool vec = (K * (int)sizeof(D)) % 16 == 0 && K % 8 == 0;
-  return by_width(pitch, [&](auto nt, auto ch) {
+  return by_quant_width(pitch, [&](auto nt, auto ch) {
     constexpr int NT = decltype(nt)::value, CH = decltype(ch)::value, WG = wg_of(NT);
     const dim3 grid(row_grid(n, WG / NT, 2048 / WG));
     if (vec) hipLaunchKernelGGL((quant_rows_kernel<D, NT, CH, true>), grid, dim3(WG), 0, st, x, n, K, pitch, q, scale);
