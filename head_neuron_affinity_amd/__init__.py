@@ -14,7 +14,7 @@ from ._binding import (HnaError, HNA_BF16, HNA_F32, HNA_ACCUMULATE, hna_dims, hn
                        affinity_loo, static_scratch_bytes, affinity_up_static,
                        mfma_rate_probe, hna_norm_dims, block_norm, block_norm_quant,
                        block_norm_backward, block_norm_workspace_bytes, quant_pitch, quant_rows,
-                       quant_matmul)
+                       quant_matmul, quant_matmul_pair)
 from .pipeline import (AffinityPass, StackPass, FfnInputs, pass_for_layer, affinity_layer,
                        ffn_inputs)
 
@@ -28,5 +28,5 @@ __all__ = [
     "neuron_step", "head_step", "layout_search", "DUAL_ITERS", "loo_workspace_bytes",
     "affinity_loo", "static_scratch_bytes", "affinity_up_static", "mfma_rate_probe",
     "hna_norm_dims", "block_norm", "block_norm_quant", "block_norm_backward",
-    "block_norm_workspace_bytes", "quant_pitch", "quant_rows", "quant_matmul", "FfnInputs", "ffn_inputs",
+    "block_norm_workspace_bytes", "quant_pitch", "quant_rows", "quant_matmul", "quant_matmul_pair", "FfnInputs", "ffn_inputs",
 ]

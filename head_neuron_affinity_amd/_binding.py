@@ -45,7 +45,7 @@ EXPORTED = [
     "hna_affinity_loo", "hna_static_scratch_bytes", "hna_affinity_up_static",
     "hna_mfma_rate_probe", "hna_block_norm", "hna_block_norm_quant",
     "hna_block_norm_workspace_bytes", "hna_block_norm_backward", "hna_quant_pitch",
-    "hna_quant_rows", "hna_quant_matmul",
+    "hna_quant_rows", "hna_quant_matmul", "hna_quant_matmul_pair",
 ]
 
 
@@ -123,6 +123,7 @@ def lib() -> ctypes.CDLL:
         "hna_quant_pitch": (i32, [i32]),
         "hna_quant_rows": (ctypes.c_int, [i64, i32, i32, vp, vp, vp, vp]),
         "hna_quant_matmul": (ctypes.c_int, [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp]),
+        "hna_quant_matmul_pair": (ctypes.c_int, [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         "hna_mfma_rate_probe": (ctypes.c_int, [i32, i32, i32, vp, vp, vp]),
         "hna_layout_search": (ctypes.c_int, [i32, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp,
                                               ctypes.POINTER(ctypes.c_double), ip, vp, sz, vp]),
@@ -824,3 +825,34 @@ def quant_matmul(q, q_scale, w, w_scale, out=None, dtype: torch.dtype = torch.bf
         _check(lib().hna_quant_matmul(T, N, K, code, _at(q), _at(q_scale), _at(w), _at(w_scale), _at(out), stream),
                "hna_quant_matmul")
     return out
+
+
+def quant_matmul_pair(q, q_scale, w0, w0_scale, w1, w1_scale, out0=None, out1=None,
+                      dtype: torch.dtype = torch.bfloat16):
+    """quant_matmul of q with two weight matrices of one shape (an FFN's gate and up) in one launch
+    (hna_quant_matmul_pair): returns (out0, out1)."""
+    if q.dim() != 2 or w0.dim() != 2:
+        raise ValueError("q and w0 must be [T, K] and [N, K]")
+    T, K = q.shape
+    N = w0.shape[0]
+    _is(q, "q", (T, K), torch.int8)
+    _is(w0, "w0", (N, K), torch.int8)
+    _is(w1, "w1", (N, K), torch.int8)
+    _is(q_scale, "q_scale", (T,), torch.float32)
+    _is(w0_scale, "w0_scale", (N,), torch.float32)
+    _is(w1_scale, "w1_scale", (N,), torch.float32)
+    if out0 is not None:
+        dtype = out0.dtype
+    elif out1 is not None:
+        dtype = out1.dtype
+    _is(out0, "out0", (T, N), dtype)
+    _is(out1, "out1", (T, N), dtype)
+    code = _code(dtype)
+    with _on(q, q_scale, w0, w0_scale, w1, w1_scale, out0, out1) as stream:
+        if out0 is None:
+            out0 = torch.empty((T, N), dtype=dtype, device=q.device)
+        if out1 is None:
+            out1 = torch.empty_like(out0)
+        _check(lib().hna_quant_matmul_pair(T, N, K, code, _at(q), _at(q_scale), _at(w0), _at(w0_scale), _at(w1),
+                                           _at(w1_scale), _at(out0), _at(out1), stream), "hna_quant_matmul_pair")
+    return out0, out1

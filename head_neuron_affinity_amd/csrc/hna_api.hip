@@ -230,6 +230,19 @@ int block_norm(const char* fn, bool quant, const hna_norm_dims* dm, const void* 
   return finish(launch_block_norm(p, dm->res_dtype == HNA_BF16, dm->dtype == HNA_BF16, st), st, fn);
 }
 
+int check_quant_matmul(const char* fn, int64_t T, int32_t N, int32_t K, int32_t out_dtype) {
+  const int rc = check_dtype(fn, out_dtype);
+  if (rc) return rc;
+  if (T < 0 || N < 1 || K < 1)
+    return fail(HNA_ERR_INVALID_ARG, "%s: T=%lld, N=%d, K=%d", fn, (long long)T, N, K);
+  if (K % 16 != 0 || K > kMaxQuantK)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: K=%d must be a multiple of 16 and <= %d", fn, K, kMaxQuantK);
+  if (T > kMaxQuantTokens || N > (1 << 22) || T * N > kMaxQuantOut)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: T=%lld, N=%d: more than 2^30 tokens, 2^22 channels or 2^36 outputs",
+                fn, (long long)T, N);
+  return HNA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1248,15 +1261,8 @@ int hna_quant_matmul(int64_t T, int32_t N, int32_t K, int32_t out_dtype, const i
                      const float* q_scale, const int8_t* w, const float* w_scale, void* out,
                      void* stream) {
   const char* fn = "hna_quant_matmul";
-  int rc = check_dtype(fn, out_dtype);
+  const int rc = check_quant_matmul(fn, T, N, K, out_dtype);
   if (rc) return rc;
-  if (T < 0 || N < 1 || K < 1)
-    return fail(HNA_ERR_INVALID_ARG, "%s: T=%lld, N=%d, K=%d", fn, (long long)T, N, K);
-  if (K % 16 != 0 || K > kMaxQuantK)
-    return fail(HNA_ERR_UNSUPPORTED, "%s: K=%d must be a multiple of 16 and <= %d", fn, K, kMaxQuantK);
-  if (T > kMaxQuantTokens || N > (1 << 22) || T * N > kMaxQuantOut)
-    return fail(HNA_ERR_UNSUPPORTED, "%s: T=%lld, N=%d: more than 2^30 tokens, 2^22 channels or 2^36 outputs",
-                fn, (long long)T, N);
   if (T > 0) {
     REQUIRE_PTR(q);
     REQUIRE_PTR(q_scale);
@@ -1264,16 +1270,29 @@ int hna_quant_matmul(int64_t T, int32_t N, int32_t K, int32_t out_dtype, const i
     REQUIRE_PTR(w_scale);
     REQUIRE_PTR(out);
   }
-  IntMmParams p{};
-  p.q = q;
-  p.w = w;
-  p.q_scale = q_scale;
-  p.w_scale = w_scale;
-  p.out = out;
-  p.T = T;
-  p.N = N;
-  p.K = K;
-  p.out_bf16 = out_dtype == HNA_BF16;
+  const IntMmParams p{q, q_scale, {w, nullptr}, {w_scale, nullptr}, {out, nullptr}, T, N, K, out_dtype == HNA_BF16, 1};
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_mm_int(p, st), st, fn);
+}
+
+int hna_quant_matmul_pair(int64_t T, int32_t N, int32_t K, int32_t out_dtype, const int8_t* q,
+                          const float* q_scale, const int8_t* w0, const float* w0_scale,
+                          const int8_t* w1, const float* w1_scale, void* out0, void* out1,
+                          void* stream) {
+  const char* fn = "hna_quant_matmul_pair";
+  const int rc = check_quant_matmul(fn, T, N, K, out_dtype);
+  if (rc) return rc;
+  if (T > 0) {
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(q_scale);
+    REQUIRE_PTR(w0);
+    REQUIRE_PTR(w0_scale);
+    REQUIRE_PTR(w1);
+    REQUIRE_PTR(w1_scale);
+    REQUIRE_PTR(out0);
+    REQUIRE_PTR(out1);
+  }
+  const IntMmParams p{q, q_scale, {w0, w1}, {w0_scale, w1_scale}, {out0, out1}, T, N, K, out_dtype == HNA_BF16, 2};
   hipStream_t st = static_cast<hipStream_t>(stream);
   return finish(launch_mm_int(p, st), st, fn);
 }

@@ -325,13 +325,16 @@ hipError_t launch_quant_rows(const void* x, int64_t n, int K, int pitch, int x_b
                              hipStream_t st);
 
 // ------------------------------------------------ 8-bit product (k_mm_int.hip)
-// out[t][n] = (sum_k q[t][k] w[n][k]) q_scale[t] w_scale[n], rows of K bytes, K a multiple of 16
+// out[z][t][n] = (sum_k q[t][k] w[z][n][k]) q_scale[t] w_scale[z][n], rows of K bytes, K a
+// multiple of 16, for one or two weight matrices of the same shape
 struct IntMmParams {
-  const int8_t *q, *w;
-  const float *q_scale, *w_scale;
-  void* out;
+  const int8_t* q;
+  const float* q_scale;
+  const int8_t* w[2];
+  const float* w_scale[2];
+  void* out[2];
   int64_t T;
-  int N, K, out_bf16;
+  int N, K, out_bf16, mats;
 };
 hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st);
 

@@ -1,5 +1,6 @@
 // 8-bit integer product on the matrix cores:
 //   out[t, n] = (sum_k q[t, k] w[n, k]) q_scale[t] w_scale[n]
+// for one weight matrix or two of one shape (an FFN's gate and up) in one launch;
 // q [T, K] and w [N, K] row-major with k contiguous, sums in int32 (exact for
 // K < 2^17), the scales applied in fp32, one rounding to the output type.
 // The channels are the MFMA rows and the tokens its columns, so a lane ends up
@@ -24,23 +25,25 @@ __device__ inline void mma_int(i32x16& c, const uint4& a, const uint4& b) {
 }
 
 // 4 consecutive channels n .. n + 3 of token t
-__device__ inline void put4(const IntMmParams& p, int64_t t, int n, const int (&v)[4], float st) {
+__device__ inline void put4(const IntMmParams& p, int z, int64_t t, int n, const int (&v)[4], float st) {
+  const float* w_scale = z ? p.w_scale[1] : p.w_scale[0];
+  void* out = z ? p.out[1] : p.out[0];
   const int64_t o = t * p.N + n;
   if (n + 4 <= p.N && p.N % 4 == 0) {
-    const float4 sw = *reinterpret_cast<const float4*>(p.w_scale + n);
+    const float4 sw = *reinterpret_cast<const float4*>(w_scale + n);
     const float f[4] = {(float)v[0] * st * sw.x, (float)v[1] * st * sw.y, (float)v[2] * st * sw.z, (float)v[3] * st * sw.w};
     if (p.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
     else
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = make_float4(f[0], f[1], f[2], f[3]);
     return;
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if (n + e >= p.N) break;
-    const float f = (float)v[e] * st * p.w_scale[n + e];
-    if (p.out_bf16) static_cast<uint16_t*>(p.out)[o + e] = (uint16_t)pack_bf16x2(f, 0.f);
-    else static_cast<float*>(p.out)[o + e] = f;
+    const float f = (float)v[e] * st * w_scale[n + e];
+    if (p.out_bf16) static_cast<uint16_t*>(out)[o + e] = (uint16_t)pack_bf16x2(f, 0.f);
+    else static_cast<float*>(out)[o + e] = f;
   }
 }
 
@@ -67,6 +70,10 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void mm_int_kernel(const IntMm
   const int grp = wg / NW, w = wg % NW;
   const int wm = w / WGN, wn = w % WGN;
 
+  const int z = blockIdx.y;
+  const float* w_scale = z ? p.w_scale[1] : p.w_scale[0];
+  void* out = z ? p.out[1] : p.out[0];
+
   // tile of this workgroup: XCD by XCD, in groups of 4 tile rows
   const int ntm = (p.N + BM - 1) / BM;
   const int64_t ntn = (p.T + BN - 1) / BN, ntiles = ntm * ntn;
@@ -81,7 +88,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void mm_int_kernel(const IntMm
   const int64_t t0 = tg / gm * BN;
 
   const int64_t xb = (int64_t)(p.N - n0) * p.K, yb = (p.T - t0) * p.K;
-  const u32x4 rx = uniform_rsrc(p.w + (int64_t)n0 * p.K, xb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)xb);
+  const u32x4 rx = uniform_rsrc((z ? p.w[1] : p.w[0]) + (int64_t)n0 * p.K, xb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)xb);
   const u32x4 ry = uniform_rsrc(p.q + t0 * p.K, yb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)yb);
 
   i32x16 acc[TM][TN];
@@ -174,30 +181,30 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void mm_int_kernel(const IntMm
       const int r = x / BM, c = x % BM, n = n0 + c;
       if (r >= rows || n >= p.N) continue;
       const int4 a = *reinterpret_cast<const int4*>(sums + r * PITCH + c), b = *reinterpret_cast<const int4*>(sums + r * PITCH + c + 4);
-      const float4 s = *reinterpret_cast<const float4*>(p.w_scale + n), u = *reinterpret_cast<const float4*>(p.w_scale + n + 4);
+      const float4 s = *reinterpret_cast<const float4*>(w_scale + n), u = *reinterpret_cast<const float4*>(w_scale + n + 4);
       const float st = p.q_scale[t0 + r];
       const int64_t o = (t0 + r) * p.N + n;
       const float4 v = make_float4((float)a.x * st * s.x, (float)a.y * st * s.y, (float)a.z * st * s.z, (float)a.w * st * s.w);
       const float4 y = make_float4((float)b.x * st * u.x, (float)b.y * st * u.y, (float)b.z * st * u.z, (float)b.w * st * u.w);
       if (p.out_bf16) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o) =
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) =
             make_uint4(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
       } else {
-        reinterpret_cast<float4*>(static_cast<float*>(p.out) + o)[0] = v;
-        reinterpret_cast<float4*>(static_cast<float*>(p.out) + o)[1] = y;
+        reinterpret_cast<float4*>(static_cast<float*>(out) + o)[0] = v;
+        reinterpret_cast<float4*>(static_cast<float*>(out) + o)[1] = y;
       }
     }
   } else if (!p.out_bf16) {
     for (int x = tid; x < BM * BN; x += NT) {
       const int r = x / BM, c = x % BM, n = n0 + c;
       if (r >= rows || n >= p.N) continue;
-      static_cast<float*>(p.out)[(t0 + r) * p.N + n] = (float)sums[r * PITCH + c] * p.q_scale[t0 + r] * p.w_scale[n];
+      static_cast<float*>(out)[(t0 + r) * p.N + n] = (float)sums[r * PITCH + c] * p.q_scale[t0 + r] * w_scale[n];
     }
   } else {
     // rows that start on any element: pairs that lie on 4 bytes, and the elements left at both ends
-    uint16_t* o = static_cast<uint16_t*>(p.out);
+    uint16_t* o = static_cast<uint16_t*>(out);
     const int m = min(BM, p.N - n0);
-    auto value = [&](int r, int c) { return (float)sums[r * PITCH + c] * p.q_scale[t0 + r] * p.w_scale[n0 + c]; };
+    auto value = [&](int r, int c) { return (float)sums[r * PITCH + c] * p.q_scale[t0 + r] * w_scale[n0 + c]; };
     for (int x = tid; x < BM / 2 * BN; x += NT) {
       const int r = x / (BM / 2), odd = (int)((t0 + r) & p.N & 1), c = 2 * (x % (BM / 2)) + odd;
       if (r >= rows || c + 1 >= m) continue;
@@ -233,22 +240,24 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void mm_int_kernel(const IntMm
 // them everywhere: reads past the end of an operand return zeros and stores
 // past the end of out are dropped by the buffer's range.
 struct IntTiles {
-  int ntm, gsize, ntiles, last, slots;
+  int ntm1, ntm, gsize, ntiles, last, slots;
 };
 // where a tile lies, and its operands from its first row on
 struct IntPanels {
   u32x4 w, q;
-  int n0, ni, ti;   // first channel; position in its group of 4 x (tokens) tiles
+  int z, n0, ni, ti;   // matrix, first channel; position in its group of 4 x (tokens) tiles
   __device__ inline void set(const IntMmParams& p, const IntTiles& g, int t) {
     const int grp = t / g.gsize, tg = t - grp * g.gsize;
     const int gm = min(4, g.ntm - grp * 4);
     ti = tg / max(gm, 1);
     ni = tg - ti * gm;
-    n0 = (grp * 4 + ni) * 256;
+    const int tn = grp * 4 + ni;                          // both matrices' tiles in a row
+    z = tn >= g.ntm1 ? 1 : 0;
+    n0 = (tn - z * g.ntm1) * 256;
     const bool none = t >= g.ntiles;
     const int64_t t0 = (int64_t)ti * 256;
     const int64_t xb = none ? 0 : (int64_t)(p.N - n0) * p.K, yb = none ? 0 : (p.T - t0) * p.K;
-    w = uniform_rsrc(p.w + (none ? 0 : (int64_t)n0 * p.K), xb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)xb);
+    w = uniform_rsrc((z ? p.w[1] : p.w[0]) + (none ? 0 : (int64_t)n0 * p.K), xb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)xb);
     q = uniform_rsrc(p.q + (none ? 0 : t0 * p.K), yb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)yb);
   }
 };
@@ -283,7 +292,8 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
   const int wm = w >> 1, wn = w & 1;
 
   IntTiles g;
-  g.ntm = (p.N + 255) / 256;
+  g.ntm1 = (p.N + 255) / 256;
+  g.ntm = p.mats * g.ntm1;
   const int ntn = (int)((p.T + 255) / 256);
   g.ntiles = g.ntm * ntn;
   g.gsize = 4 * ntn;
@@ -317,7 +327,7 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
     const bool none = cp_tile >= g.ntiles;
     const int64_t sb = none ? 0 : (int64_t)(p.N - cp.n0) * 4, qb = none ? 0 : (p.T - (int64_t)cp.ti * 256) * 4;
     const uint32_t m0 = lds_addr(scales[cp_par]) + (uint32_t)w * 256u;
-    dma4s(uniform_rsrc(p.w_scale + (none ? 0 : cp.n0), sb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)sb),
+    dma4s(uniform_rsrc((cp.z ? p.w_scale[1] : p.w_scale[0]) + (none ? 0 : cp.n0), sb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)sb),
           (uint32_t)tid * 4, 0u, m0);
     dma4s(uniform_rsrc(p.q_scale + (none ? 0 : (int64_t)cp.ti * 256), qb > kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)qb),
           (uint32_t)tid * 4, 0u, m0 + 4 * BM);
@@ -456,7 +466,7 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
       const int64_t tj = t0 + j * 32;
       const float st = sq[j * 32 + (le & 31)];
       const int64_t rows = min<int64_t>(32, p.T - tj), ob = rows > 0 ? rows * p.N * E : 0;
-      const __amdgpu_buffer_rsrc_t ro = buffer_rsrc(static_cast<unsigned char*>(p.out) + (rows > 0 ? tj * p.N * E : 0), (uint32_t)ob);
+      const __amdgpu_buffer_rsrc_t ro = buffer_rsrc(static_cast<unsigned char*>(here.z ? p.out[1] : p.out[0]) + (rows > 0 ? tj * p.N * E : 0), (uint32_t)ob);
 #pragma unroll
       for (int i0 = 0; i0 < 4; i0 += CH) {
 #pragma unroll
@@ -523,7 +533,7 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
 template <int BM, int BN, int WGM, int WGN, int KG, int NST>
 hipError_t launch_t(const IntMmParams& p, hipStream_t st) {
   const int64_t ntiles = (int64_t)((p.N + BM - 1) / BM) * ((p.T + BN - 1) / BN);
-  const dim3 grid((unsigned)(8 * ((ntiles + 7) / 8)));
+  const dim3 grid((unsigned)(8 * ((ntiles + 7) / 8)), p.mats);
   hipLaunchKernelGGL((mm_int_kernel<BM, BN, WGM, WGN, KG, NST>), grid, dim3(64 * WGM * WGN * KG), 0, st, p);
   return hipGetLastError();
 }
@@ -539,7 +549,7 @@ __global__ __launch_bounds__(64 * W) void mm_int_few_kernel(const IntMmParams p)
   __shared__ int part[W][4][64];
   const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
   const int n0 = blockIdx.x * 16, kl = 16 * (l >> 4);
-  const int8_t* pa = p.w + (int64_t)min(n0 + (l & 15), p.N - 1) * p.K;
+  const int8_t* pa = (blockIdx.y ? p.w[1] : p.w[0]) + (int64_t)min(n0 + (l & 15), p.N - 1) * p.K;
   const int8_t* pb = p.q + (int64_t)min(l & 15, (int)p.T - 1) * p.K;
   i32x4 acc = {};
   const int steps = (p.K + 63) / 64, per = (steps + W - 1) / W;
@@ -571,15 +581,16 @@ __global__ __launch_bounds__(64 * W) void mm_int_few_kernel(const IntMmParams p)
     for (int x = 1; x < W; ++x) v[e] += part[x][e][l];
   }
   const int t = l & 15, n = n0 + 4 * (l >> 4);
-  if (t < p.T && n < p.N) put4(p, t, n, v, p.q_scale[t]);
+  if (t < p.T && n < p.N) put4(p, blockIdx.y, t, n, v, p.q_scale[t]);
 }
 
 // W waves a workgroup: enough for 16 on each CU, with 256 bytes of k each
 hipError_t launch_few(const IntMmParams& p, hipStream_t st) {
-  const int wgs = (p.N + 15) / 16;
-  if (wgs * 4 >= 4096 || p.K <= 1024) hipLaunchKernelGGL(mm_int_few_kernel<4>, dim3(wgs), dim3(256), 0, st, p);
-  else if (wgs * 8 >= 4096 || p.K <= 2048) hipLaunchKernelGGL(mm_int_few_kernel<8>, dim3(wgs), dim3(512), 0, st, p);
-  else hipLaunchKernelGGL(mm_int_few_kernel<16>, dim3(wgs), dim3(1024), 0, st, p);
+  const dim3 grid((p.N + 15) / 16, p.mats);
+  const int wgs = grid.x * p.mats;
+  if (wgs * 4 >= 4096 || p.K <= 1024) hipLaunchKernelGGL(mm_int_few_kernel<4>, grid, dim3(256), 0, st, p);
+  else if (wgs * 8 >= 4096 || p.K <= 2048) hipLaunchKernelGGL(mm_int_few_kernel<8>, grid, dim3(512), 0, st, p);
+  else hipLaunchKernelGGL(mm_int_few_kernel<16>, grid, dim3(1024), 0, st, p);
   return hipGetLastError();
 }
 
@@ -587,9 +598,9 @@ hipError_t launch_few(const IntMmParams& p, hipStream_t st) {
 
 hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
-  // Variants, by the tiles they make of T x N on 256 CUs; times in us of both
+  // Variants, by the tiles they make of the outputs (T x N, or twice that) on 256 CUs; times in us of both
   // sides of each border.
-  auto tiles = [&](int m, int n) { return (int64_t)((p.N + m - 1) / m) * ((p.T + n - 1) / n); };
+  auto tiles = [&](int m, int n) { return p.mats * (int64_t)((p.N + m - 1) / m) * ((p.T + n - 1) / n); };
   // 256 x 256 from 160 tiles on.  T x N x K 4096 x 2531 x 1008 (160 tiles): 27
   // against 34 with 128 x 128; 2048 x 4096 x 1024 (128 tiles): 20 against 17.
   // Two steps a tile at least: its scales are in before the tile before it ends.

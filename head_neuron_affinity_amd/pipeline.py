@@ -129,8 +129,8 @@ def ffn_inputs(x, gamma, w_gate, w_up, y=None, gamma_post=None, gate=None, gate_
     x_in, q, scale, r, _ = B.block_norm_quant(x, y, gamma, gamma_post=gamma_post, gate=gate,
                                               gate_tokens=gate_tokens, res_scale=res_scale,
                                               block_scale=block_scale, eps=eps)
-    return {"x_in": x_in, "r": r, "scale": scale, "g": B.quant_matmul(q, scale, *w_gate),
-            "u": B.quant_matmul(q, scale, *w_up)}
+    g, u = B.quant_matmul_pair(q, scale, *w_gate, *w_up)
+    return {"x_in": x_in, "r": r, "scale": scale, "g": g, "u": u}
 
 
 class FfnInputs:

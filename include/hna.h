@@ -500,6 +500,13 @@ int hna_quant_matmul(int64_t T, int32_t N, int32_t K, int32_t out_dtype, const i
                      const float* q_scale, const int8_t* w, const float* w_scale, void* out,
                      void* stream);
 
+/* hna_quant_matmul of the same q with two weight matrices of one shape, an FFN's gate and up
+ * projections: out0 [T, N] from w0 and out1 [T, N] from w1, in one launch. */
+int hna_quant_matmul_pair(int64_t T, int32_t N, int32_t K, int32_t out_dtype, const int8_t* q,
+                          const float* q_scale, const int8_t* w0, const float* w0_scale,
+                          const int8_t* w1, const float* w1_scale, void* out0, void* out1,
+                          void* stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /*

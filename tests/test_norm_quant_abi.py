@@ -135,6 +135,17 @@ def test_quant_matmul_refusals(hna, kw, status):
     assert matmul(hna, **kw) == status and hna.last_error() != ""
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), -1), (dict(N=0), -1), (dict(K=40), -2), (dict(dtype=2), -1), (dict(T=2 ** 20, N=2 ** 17), -2)] + [
+    ({k: v}, s) for k in ("q", "qs", "w0", "s0", "w1", "s1", "out0", "out1") for v, s in ((0, -1), (MIS, -3))])
+def test_quant_matmul_pair_refusals(hna, kw, status):
+    a = dict(T=4, N=32, K=64, dtype=1, q=FAKE, qs=FAKE, w0=FAKE, s0=FAKE, w1=FAKE, s1=FAKE, out0=FAKE, out1=FAKE)
+    a.update(kw)
+    rc = hna.lib().hna_quant_matmul_pair(a["T"], a["N"], a["K"], a["dtype"], *[ptr(a[k]) for k in (
+        "q", "qs", "w0", "s0", "w1", "s1", "out0", "out1")], None)
+    assert rc == status and hna.last_error() != ""
+
+
 def test_no_rows_is_no_work(hna):
     assert norm(hna, dims(hna, T=0), x=0, y=0, x_out=0, r=0) == 0
     assert quant(hna, rows=0, x=0, q=0, scale=0) == 0
@@ -170,6 +181,9 @@ def test_python_refuses_host_tensors_and_bad_shapes(hna):
                  lambda: hna.quant_rows(x[0]), lambda: hna.quant_rows(x, q=i8[:2]),
                  lambda: hna.quant_matmul(i8, torch.ones(4), i8[:, :32], torch.ones(4)),
                  lambda: hna.quant_matmul(i8, torch.ones(3), i8, torch.ones(4)),
+                 lambda: hna.quant_matmul_pair(i8, torch.ones(4), i8, torch.ones(4), i8[:2], torch.ones(4)),
+                 lambda: hna.quant_matmul_pair(i8, torch.ones(4), i8, torch.ones(4), i8, torch.ones(4), out0=torch.ones(4, 4),
+                                               out1=torch.ones(4, 4).bfloat16()),
                  lambda: hna.quant_matmul(i8, torch.ones(4), i8, torch.ones(4), out=x)):
         with pytest.raises(ValueError):
             call()

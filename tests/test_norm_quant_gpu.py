@@ -388,6 +388,24 @@ def test_product_larger(hna, T, N, K):
         check_product(hna, q, s, w, ws, dtype)
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 4096, 1024), (8, 100, 200), (40, 1000, 512), (100, 8000, 2100), (300, 2531, 1008),
+                                   (1100, 1032, 528), (1024, 8192, 272), (20003, 261, 400), (9000, 1284, 130), (5, 33, 90)])
+def test_product_pair(hna, T, N, K):
+    """Two weight matrices in one launch: each output as the single call's, bit for bit (exact sums,
+    the same two products of the scales)."""
+    print(f"pair T={T} N={N} K={K}", flush=True)
+    g = gen(T + N + K)
+    q, s = int_rows(g, T, K)
+    w0, s0 = int_rows(g, N, K)
+    w1, s1 = int_rows(g, N, K)
+    for dtype in (BF, F):
+        a, b = hna.quant_matmul_pair(q, s, w0, s0, w1, s1, dtype=dtype)
+        assert torch.equal(a, check_product(hna, q, s, w0, s0, dtype))
+        assert torch.equal(b, check_product(hna, q, s, w1, s1, dtype))
+    out = torch.empty(T, N, device="cuda")
+    assert hna.quant_matmul_pair(q, s, w0, s0, w1, s1, out1=out)[1] is out and torch.equal(out, b)
+
+
 def test_product_largest_sums(hna):
     """Every entry at the ends of 8 bits, -128 too, at the longest K: sums up to 2^31 - 2^18."""
     K = 131056
