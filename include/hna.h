@@ -425,7 +425,8 @@ int hna_layout_search(int32_t N, int32_t G, int32_t I, int32_t L, const float* S
  * gamma, gamma_post [hidden], r, r_post [T] and their gradients are fp32, as
  * are all sums.  A row whose mean square and eps are both 0 has r = 0 and
  * normalises to zeros.  A row that holds a NaN or an infinity affects itself
- * only (and the sums over tokens).
+ * only (and the sums over tokens).  Outputs overlap neither each other nor
+ * inputs, but for the whole-buffer cases that a call names.
  */
 typedef struct hna_norm_dims {
   int64_t T;

@@ -236,8 +236,59 @@ def test_backward_optional_gradients(hna):
     got = s.backward(hna, x_out, r, r_post, dn=dn, dx_out=dx_out, dx=dx_out, dy=dn)
     for k in full:
         assert torch.equal(got[k], full[k]), k
+    y = s.y.clone()
+    got = s.backward(hna, x_out, r, r_post, y=y, dy=y)
+    for k in full:
+        assert torch.equal(got[k], full[k]), k
     got = s.backward(hna, x_out, r, None, y=None, gamma_post=None, gate=None, gate_tokens=None, want_dy=False)
     assert torch.equal(got["dx"], full["dx"]) and torch.equal(got["dgamma"], full["dgamma"])
+
+
+def test_backward_gate_without_y(hna):
+    """A gate whose gradient is not wanted: dy = block_scale gate d needs no y."""
+    for gate in (1, 7, 50):
+        s = Step(50, 520, F, BF, post=False, gate=gate)
+        x_out, _, r, _ = s.forward(hna.block_norm)
+        full = s.backward(hna, x_out, r, None)
+        got = s.backward(hna, x_out, r, None, y=None)
+        assert got["dgate"] is None
+        for k in ("dx", "dy", "dgamma"):
+            assert got[k].dtype == full[k].dtype
+        s.check_backward({**got, "dgate": full["dgate"]}, x_out, r, None)
+
+
+def test_c_calls_with_outputs_left_out(hna):
+    """Every optional output of the C calls left out by itself: the others as with it, bit for bit."""
+    import ctypes
+    L = hna.lib()
+    s = Step(37, 520, F, BF, gate=8)
+    x_out, n, r, r_post = s.forward(hna.block_norm)
+    _, q, sc, _, _ = s.forward(hna.block_norm_quant)
+    dims = hna.hna_norm_dims(37, 8, 520, 1, 0)
+    st = torch.cuda.current_stream().cuda_stream
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    head = [ctypes.byref(dims), at(s.x), at(s.y), at(s.gate), at(s.gamma), at(s.gamma_post), s.rs, s.bs, s.eps]
+    blank = lambda ts: [torch.full_like(t, 77) for t in ts]  # noqa: E731
+    for ref_out, call, needed in (((x_out, n, r, r_post), L.hna_block_norm, 1),
+                                  ((x_out, q, sc, r, r_post), L.hna_block_norm_quant, 3)):
+        for skip in range(needed, len(ref_out)):
+            out = blank(ref_out)
+            assert call(*head, *[None if i == skip else at(t) for i, t in enumerate(out)], st) == 0, hna.last_error()
+            for i, t in enumerate(out):
+                assert torch.equal(t, ref_out[i]) if i != skip else bool((t == 77).all())
+    full = s.backward(hna, x_out, r, r_post)
+    ws = torch.empty(hna.block_norm_workspace_bytes(dims), dtype=torch.uint8, device="cuda")
+    names = ("dx", "dy", "dgamma", "dgamma_post", "dgate")
+    for only in (False, True):
+        for k in range(5):
+            out = blank([full[x] for x in names])
+            give = [at(t) if (i == k) == only else None for i, t in enumerate(out)]
+            rc = L.hna_block_norm_backward(ctypes.byref(dims), at(s.dn), at(s.dx_out), at(x_out), at(s.y), at(s.gate),
+                                           at(s.gamma), at(s.gamma_post), at(r), at(r_post), s.rs, s.bs, *give,
+                                           at(ws), ws.numel(), st)
+            assert rc == 0, hna.last_error()
+            for i, t in enumerate(out):
+                assert torch.equal(t, full[names[i]]) if give[i] else bool((t == 77).all()), (only, k, i)
 
 
 def test_backward_against_differences(hna):
