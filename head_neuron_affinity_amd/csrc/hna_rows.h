@@ -8,49 +8,113 @@
 namespace hna {
 namespace rows {
 
-// ---- 8 consecutive elements, 16-byte aligned: as loaded, and in fp32 ----
-template <typename T>
+// ---- the elements of a row over its lanes ----
+// NT lanes hold a row in chunks of 8 NT elements, 8 to a lane: in two halves of 4
+// that follow each other, or (SPLIT) lie NT 4 elements apart.  SPLIT is for rows
+// that are fp32 on one side: a load or store of 16 bytes a lane then covers whole
+// lines, where 8 consecutive fp32 elements a lane would take every other 16 bytes.
+template <int NT, bool SPLIT>
+struct Lane {
+  int lane;
+  __device__ inline int at(int c, int h) const {
+    return SPLIT ? c * NT * 8 + h * NT * 4 + lane * 4 : (c * NT + lane) * 8 + h * 4;
+  }
+};
+
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+// NTEMP: past the caches (a stream that they could not hold)
+template <bool NTEMP, typename V>
+__device__ inline V load_v(const void* p) {
+  const V* v = static_cast<const V*>(p);
+  if constexpr (NTEMP) return __builtin_nontemporal_load(v);
+  else return *v;
+}
+template <bool NTEMP, typename V>
+__device__ inline void store_v(void* p, V x) {
+  V* v = static_cast<V*>(p);
+  if constexpr (NTEMP) __builtin_nontemporal_store(x, v);
+  else *v = x;
+}
+
+// A lane's 8 elements of a chunk as they lie in memory; halves from C on are zeros
+template <typename T, bool SPLIT>
 struct Raw8;
-template <>
-struct Raw8<__bf16> {
-  uint4 q;
-  __device__ inline void load(const __bf16* p) { q = *reinterpret_cast<const uint4*>(p); }
-  __device__ inline void zero() { q = make_uint4(0u, 0u, 0u, 0u); }
+template <bool SPLIT>
+struct Raw8<__bf16, SPLIT> {
+  u32x2v q[2];
+  template <bool NTEMP, int NT>
+  __device__ inline void load(const __bf16* row, Lane<NT, SPLIT> l, int c, int C, bool live) {
+    q[0] = q[1] = u32x2v{0u, 0u};
+    if constexpr (SPLIT) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (live && l.at(c, h) < C) q[h] = load_v<NTEMP, u32x2v>(row + l.at(c, h));
+    } else if (live && l.at(c, 0) < C) {
+      const u32x4v v = load_v<NTEMP, u32x4v>(row + l.at(c, 0));
+      q[0] = u32x2v{v.x, v.y};
+      q[1] = u32x2v{v.z, v.w};
+    }
+  }
   __device__ inline void get(float (&v)[8]) const {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      const uint32_t w = i & 1 ? q[i >> 1].y : q[i >> 1].x;
+      v[2 * i] = __uint_as_float(w << 16);
+      v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
     }
   }
 };
-template <>
-struct Raw8<float> {
-  float4 a, b;
-  __device__ inline void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+template <bool SPLIT>
+struct Raw8<float, SPLIT> {
+  f32x4v q[2];
+  template <bool NTEMP, int NT>
+  __device__ inline void load(const float* row, Lane<NT, SPLIT> l, int c, int C, bool live) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      q[h] = f32x4v{0.f, 0.f, 0.f, 0.f};
+      if (live && l.at(c, h) < C) q[h] = load_v<NTEMP, f32x4v>(row + l.at(c, h));
+    }
   }
-  __device__ inline void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ inline void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v[4 * h] = q[h].x;
+      v[4 * h + 1] = q[h].y;
+      v[4 * h + 2] = q[h].z;
+      v[4 * h + 3] = q[h].w;
+    }
   }
 };
-template <typename T>
-__device__ inline void load8(const T* p, float (&v)[8]) {
-  Raw8<T> r;
-  r.load(p);
-  r.get(v);
+template <bool NTEMP, int NT, bool SPLIT>
+__device__ inline void store8(__bf16* row, Lane<NT, SPLIT> l, int c, int C, const float (&v)[8]) {
+  const u32x2v a = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, b = {pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  if constexpr (SPLIT) {
+    if (l.at(c, 0) < C) store_v<NTEMP, u32x2v>(row + l.at(c, 0), a);
+    if (l.at(c, 1) < C) store_v<NTEMP, u32x2v>(row + l.at(c, 1), b);
+  } else {
+    if (l.at(c, 0) < C) store_v<NTEMP, u32x4v>(row + l.at(c, 0), u32x4v{a.x, a.y, b.x, b.y});
+  }
 }
-__device__ inline void store8(__bf16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+template <bool NTEMP, int NT, bool SPLIT>
+__device__ inline void store8(float* row, Lane<NT, SPLIT> l, int c, int C, const float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (l.at(c, h) < C) store_v<NTEMP, f32x4v>(row + l.at(c, h), f32x4v{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]});
 }
-__device__ inline void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+// 8 floats of a gain row, 1 from C on
+template <int NT, bool SPLIT>
+__device__ inline void load_gain(const float* row, Lane<NT, SPLIT> l, int c, int C, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    f32x4v q = {1.f, 1.f, 1.f, 1.f};
+    if (l.at(c, h) < C) q = *reinterpret_cast<const f32x4v*>(row + l.at(c, h));
+    v[4 * h] = q.x;
+    v[4 * h + 1] = q.y;
+    v[4 * h + 2] = q.z;
+    v[4 * h + 3] = q.w;
+  }
 }
 // v as it will be read back from a tensor of type R
 template <typename R>
@@ -178,6 +242,16 @@ __device__ inline uint2 quant8(const float (&x)[8], const RowScale& s) {
     w[h] = lo | hi;
   }
   return make_uint2(w[0], w[1]);
+}
+
+template <int NT, bool SPLIT>
+__device__ inline void store_quant8(int8_t* row, Lane<NT, SPLIT> l, int c, int pitch, uint2 q) {
+  if constexpr (SPLIT) {
+    if (l.at(c, 0) < pitch) *reinterpret_cast<uint32_t*>(row + l.at(c, 0)) = q.x;
+    if (l.at(c, 1) < pitch) *reinterpret_cast<uint32_t*>(row + l.at(c, 1)) = q.y;
+  } else {
+    if (l.at(c, 0) < pitch) *reinterpret_cast<uint2*>(row + l.at(c, 0)) = q;
+  }
 }
 
 }  // namespace rows

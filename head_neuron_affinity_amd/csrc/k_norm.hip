@@ -24,39 +24,41 @@ constexpr int wg_of(int nt) { return nt < 256 ? 256 : nt; }
 // 1 / r, or 0 for a row whose mean square and eps are both 0: it normalises to zeros
 __device__ inline float inv_or_zero(float r) { return r > 0.f ? 1.f / r : (r == 0.f ? 0.f : r); }
 
-template <typename R, typename D, int NT, int CH, bool Q8>
+// S: past the caches (see streams)
+template <typename R, typename D, int NT, int CH, bool Q8, bool S>
 __global__ __launch_bounds__(wg_of(NT)) void block_norm_kernel(const NormParams p) {
   constexpr int WG = wg_of(NT), NR = WG / NT;
+  constexpr bool SPLIT = sizeof(R) == 4 || sizeof(D) == 4;
   __shared__ uint32_t box[2 * (WG / 64)];
   int phase = 0;
-  const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
-  const float inv_c = 1.f / (float)p.C;
+  const Lane<NT, SPLIT> ln{(int)threadIdx.x % NT};
+  const int sub = threadIdx.x / NT, C = p.C;
+  const float inv_c = 1.f / (float)C;
 
   float ga[CH][8], gp[CH][8];
-  bool in[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int j = (c * NT + lane) * 8;
-    in[c] = j < p.C;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ga[c][e] = gp[c][e] = 1.f;
-    if (in[c] && p.gamma) load8(p.gamma + j, ga[c]);
-    if (in[c] && p.gamma_post) load8(p.gamma_post + j, gp[c]);
+    load_gain(p.gamma, ln, c, p.gamma ? C : 0, ga[c]);
+    load_gain(p.gamma_post, ln, c, p.gamma_post ? C : 0, gp[c]);
   }
 
   for (int64_t row0 = (int64_t)blockIdx.x * NR; row0 < p.T; row0 += (int64_t)gridDim.x * NR) {
     const int64_t row = row0 + sub;
     const bool live = row < p.T;
-    const int64_t base = row * p.C;
+    const int64_t base = row * C;
     float h[CH][8], y[CH][8];
+    {
+      Raw8<R, SPLIT> rx[CH];
+      Raw8<D, SPLIT> ry[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int64_t o = base + (c * NT + lane) * 8;
+      for (int c = 0; c < CH; ++c) {
+        rx[c].template load<S>(static_cast<const R*>(p.x) + base, ln, c, C, live);
+        ry[c].template load<S>(static_cast<const D*>(p.y) + base, ln, c, C, live && p.y);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[c][e] = y[c][e] = 0.f;
-      if (live && in[c]) {
-        load8(static_cast<const R*>(p.x) + o, h[c]);
-        if (p.y) load8(static_cast<const D*>(p.y) + o, y[c]);
+      for (int c = 0; c < CH; ++c) {
+        rx[c].get(h[c]);
+        ry[c].get(y[c]);
       }
     }
     if (p.y) {
@@ -68,7 +70,7 @@ __global__ __launch_bounds__(wg_of(NT)) void block_norm_kernel(const NormParams 
 #pragma unroll
           for (int e = 0; e < 8; ++e) s = fmaf(y[c][e], y[c][e], s);
         const float rp = sqrtf(fmaf(row_sum<NT, WG>(s, box, phase), inv_c, p.eps));
-        if (live && lane == 0 && p.r_post) p.r_post[row] = rp;
+        if (live && ln.lane == 0 && p.r_post) p.r_post[row] = rp;
         m *= inv_or_zero(rp);
       }
 #pragma unroll
@@ -76,17 +78,19 @@ __global__ __launch_bounds__(wg_of(NT)) void block_norm_kernel(const NormParams 
         float g[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = gp[c][e];
-        if (p.gate && live && in[c]) {
+        if (p.gate) {
           float v[8];
-          load8(static_cast<const D*>(p.gate) +
-                    (int64_t)((uint32_t)row / (uint32_t)p.gate_tokens) * p.C + (c * NT + lane) * 8, v);
+          Raw8<D, SPLIT> rg;
+          rg.template load<false>(static_cast<const D*>(p.gate) + (live ? (int64_t)((uint32_t)row / (uint32_t)p.gate_tokens) * C : 0),
+                                  ln, c, C, live);
+          rg.get(v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) g[e] *= v[e];
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           h[c][e] = as_stored<R>(fmaf(p.res_scale, h[c][e], y[c][e] * m * g[e]));
-        if (live && in[c]) store8(static_cast<R*>(p.x_out) + base + (c * NT + lane) * 8, h[c]);
+        if (live) store8<S>(static_cast<R*>(p.x_out) + base, ln, c, C, h[c]);
       }
     }
     float s = 0.f;
@@ -95,7 +99,7 @@ __global__ __launch_bounds__(wg_of(NT)) void block_norm_kernel(const NormParams 
 #pragma unroll
       for (int e = 0; e < 8; ++e) s = fmaf(h[c][e], h[c][e], s);
     const float r = sqrtf(fmaf(row_sum<NT, WG>(s, box, phase), inv_c, p.eps));
-    if (live && lane == 0 && p.r) p.r[row] = r;
+    if (live && ln.lane == 0 && p.r) p.r[row] = r;
     const float inv = inv_or_zero(r);
     if constexpr (!Q8) {
       if (!p.n) continue;
@@ -104,7 +108,7 @@ __global__ __launch_bounds__(wg_of(NT)) void block_norm_kernel(const NormParams 
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = h[c][e] * inv * ga[c][e];
-        if (live && in[c]) store8(static_cast<D*>(p.n) + base + (c * NT + lane) * 8, v);
+        if (live) store8<S>(static_cast<D*>(p.n) + base, ln, c, C, v);
       }
     } else {
       uint32_t top = 0;
@@ -112,59 +116,59 @@ __global__ __launch_bounds__(wg_of(NT)) void block_norm_kernel(const NormParams 
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          h[c][e] = h[c][e] * inv * ga[c][e];
-          if (in[c]) top = max_bits(top, __float_as_uint(h[c][e]) & 0x7fffffffu);
+          h[c][e] = ln.at(c, e >> 2) < C ? h[c][e] * inv * ga[c][e] : 0.f;
+          top = max_bits(top, __float_as_uint(h[c][e]) & 0x7fffffffu);
         }
       const RowScale rs = row_scale(row_max_bits<NT, WG>(top, box, phase));
-      if (live && lane == 0) p.q_scale[row] = rs.scale;
+      if (live && ln.lane == 0) p.q_scale[row] = rs.scale;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int j = (c * NT + lane) * 8;   // columns from C up to the pitch get zeros
-        if (live && j < p.pitch)
-          *reinterpret_cast<uint2*>(p.q + row * p.pitch + j) = in[c] ? quant8(h[c], rs) : make_uint2(0u, 0u);
-      }
+      for (int c = 0; c < CH; ++c)
+        if (live) store_quant8(p.q + row * p.pitch, ln, c, p.pitch, quant8(h[c], rs));
     }
   }
 }
 
 // Rows of x as 8-bit integers.  VEC: rows start on 16 bytes.
-template <typename D, int NT, int CH, bool VEC>
+template <typename D, int NT, int CH, bool VEC, bool S>
 __global__ __launch_bounds__(wg_of(NT)) void quant_rows_kernel(const D* __restrict__ x, int64_t n_rows,
                                                                int K, int pitch, int8_t* __restrict__ q,
                                                                float* __restrict__ scale) {
   constexpr int WG = wg_of(NT), NR = WG / NT;
+  constexpr bool SPLIT = sizeof(D) == 4;
   __shared__ uint32_t box[2 * (WG / 64)];
   int phase = 0;
-  const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
+  const Lane<NT, SPLIT> ln{(int)threadIdx.x % NT};
+  const int sub = threadIdx.x / NT;
   for (int64_t row0 = (int64_t)blockIdx.x * NR; row0 < n_rows; row0 += (int64_t)gridDim.x * NR) {
     const int64_t row = row0 + sub;
     const bool live = row < n_rows;
+    const D* xr = x + row * K;
     float v[CH][8];
+    if constexpr (VEC) {
+      Raw8<D, SPLIT> raw[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) raw[c].template load<S>(xr, ln, c, K, live);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) raw[c].get(v[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = ln.at(c, e >> 2) + (e & 3);
+          v[c][e] = live && j < K ? (float)xr[j] : 0.f;
+        }
+    }
     uint32_t top = 0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int j = (c * NT + lane) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
-      if (live && j < K) {
-        if constexpr (VEC) {
-          load8(x + row * K + j, v[c]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (j + e < K) v[c][e] = (float)x[row * K + j + e];
-        }
-      }
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = max_bits(top, __float_as_uint(v[c][e]) & 0x7fffffffu);
-    }
     const RowScale rs = row_scale(row_max_bits<NT, WG>(top, box, phase));
-    if (live && lane == 0) scale[row] = rs.scale;
+    if (live && ln.lane == 0) scale[row] = rs.scale;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int j = (c * NT + lane) * 8;
-      if (live && j < pitch) *reinterpret_cast<uint2*>(q + row * pitch + j) = quant8(v[c], rs);
-    }
+    for (int c = 0; c < CH; ++c)
+      if (live) store_quant8(q + row * pitch, ln, c, pitch, quant8(v[c], rs));
   }
 }
 
@@ -206,28 +210,27 @@ __global__ __launch_bounds__(1024) void quant_long_rows_kernel(const D* __restri
 // Bound by HBM: the next row is loaded before the present one is worked on, as
 // it lies in memory (bf16 stays packed); the gains are read from LDS.
 // Y: y is read (a block norm, or dgate is wanted).
-template <typename R, typename D, int NT, int CH, bool Y>
+template <typename R, typename D, int NT, int CH, bool Y, bool S>
 __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backward_kernel(const NormGradParams p) {
   constexpr int WG = wg_of(NT), NR = WG / NT;
+  constexpr bool SPLIT = sizeof(R) == 4 || sizeof(D) == 4;
   constexpr int CMAX = NT * CH * 8;
   __shared__ __attribute__((aligned(16))) float gains[(Y ? 2 : 1) * CMAX];   // gamma, then gamma_post
   __shared__ uint32_t box[2 * (WG / 64)];
   __shared__ float cols[NR > 1 ? NR * NT * 8 : 1];
   int phase = 0;
-  const int lane = threadIdx.x % NT, sub = threadIdx.x / NT;
-  const float inv_c = 1.f / (float)p.C;
+  const Lane<NT, SPLIT> ln{(int)threadIdx.x % NT};
+  const int sub = threadIdx.x / NT, C = p.C;
+  const float inv_c = 1.f / (float)C;
   const bool post = Y && p.gamma_post != nullptr;
-  bool in[CH];
   float acc_g[CH][8], acc_p[Y ? CH : 1][8], acc_t[Y ? CH : 1][8];   // dgamma, dgamma_post, dgate
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    in[c] = (c * NT + lane) * 8 < p.C;
+  for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       acc_g[c][e] = 0.f;
       if constexpr (Y) acc_p[c][e] = acc_t[c][e] = 0.f;
     }
-  }
 
   // sum of acc over the NR rows a workgroup holds side by side, chunk by chunk;
   // the lanes of sub-row 0 get it and hand it to `put`
@@ -236,51 +239,42 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
     for (int c = 0; c < CH; ++c) {
       if constexpr (NR > 1) {
         __syncthreads();
-        store8(cols + threadIdx.x * 8, acc[c]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cols[e * WG + threadIdx.x] = acc[c][e];
         __syncthreads();
         if (sub == 0) {
 #pragma unroll
-          for (int i = 1; i < NR; ++i) {
-            float v[8];
-            load8(cols + (i * NT + lane) * 8, v);
+          for (int i = 1; i < NR; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[c][e] += v[e];
-          }
+            for (int e = 0; e < 8; ++e) acc[c][e] += cols[e * WG + i * NT + threadIdx.x];
         }
       }
-      if (sub == 0 && in[c]) put((c * NT + lane) * 8, acc[c]);
+      if (sub == 0) put(c, acc[c]);
     }
   };
 
   // a row as it lies in memory
   struct Row {
-    Raw8<R> x[CH], dx[CH];
-    Raw8<D> dn[CH], y[Y ? CH : 1], gate[CH];
+    Raw8<R, SPLIT> x[CH], dx[CH];
+    Raw8<D, SPLIT> dn[CH], y[Y ? CH : 1], gate[CH];
     float r, r_post;
   };
   auto load = [&](Row& a, int64_t row, bool live) __attribute__((always_inline)) {
-    const int64_t base = row * p.C;
-    const int64_t gbase = p.gate && live ? (int64_t)((uint32_t)row / (uint32_t)p.gate_tokens) * p.C : 0;
+    const int64_t base = row * C;
     a.r = live && p.dn ? p.r[row] : 0.f;
     a.r_post = live && post ? p.r_post[row] : 1.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int j = (c * NT + lane) * 8;
-      const bool on = live && in[c];
-      a.x[c].zero();
-      a.dx[c].zero();
-      a.dn[c].zero();
-      a.gate[c].zero();
-      if constexpr (Y) a.y[c].zero();
-      if (on && p.dn) a.x[c].load(static_cast<const R*>(p.x_out) + base + j);
-      if (on && p.dn) a.dn[c].load(static_cast<const D*>(p.dn) + base + j);
-      if (on && p.dx_out) a.dx[c].load(static_cast<const R*>(p.dx_out) + base + j);
-      if constexpr (Y)
-        if (on) a.y[c].load(static_cast<const D*>(p.y) + base + j);
-      if (on && p.gate) a.gate[c].load(static_cast<const D*>(p.gate) + gbase + j);
+      a.x[c].template load<S>(static_cast<const R*>(p.x_out) + base, ln, c, C, live && p.dn);
+      a.dn[c].template load<S>(static_cast<const D*>(p.dn) + base, ln, c, C, live && p.dn);
+      a.dx[c].template load<S>(static_cast<const R*>(p.dx_out) + base, ln, c, C, live && p.dx_out);
+      if constexpr (Y) a.y[c].template load<S>(static_cast<const D*>(p.y) + base, ln, c, C, live);
     }
+    const bool gated = p.gate && live;
+    const int64_t gbase = gated ? (int64_t)((uint32_t)row / (uint32_t)p.gate_tokens) * C : 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) a.gate[c].template load<false>(static_cast<const D*>(p.gate) + gbase, ln, c, C, gated);
   };
-
   // rows of this workgroup: chunk `i` of the gate row group it belongs to
   const int64_t group = blockIdx.x / p.spans, i = blockIdx.x % p.spans;
   const int64_t beg = group * p.group_rows + i * p.chunk;
@@ -289,7 +283,7 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
   Row cur;
   int64_t row0 = beg, seg = beg;                          // segment: the rows up to the next write of dgate
   if (beg < end) load(cur, beg + sub, beg + sub < min(beg + p.flush_rows, end));
-  for (int j = threadIdx.x * 4; j < p.C; j += WG * 4) {
+  for (int j = threadIdx.x * 4; j < C; j += WG * 4) {
     if (p.gamma) *reinterpret_cast<float4*>(gains + j) = *reinterpret_cast<const float4*>(p.gamma + j);
     if constexpr (Y)
       if (post) *reinterpret_cast<float4*>(gains + CMAX + j) = *reinterpret_cast<const float4*>(p.gamma_post + j);
@@ -307,7 +301,7 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
 
     const int64_t row = row0 + sub;
     const bool live = row < seg_end;
-    const int64_t base = row * p.C;
+    const int64_t base = row * C;
     const float inv = p.dn && live ? inv_or_zero(cur.r) : 0.f;
     const float invp = post && live ? inv_or_zero(cur.r_post) : 1.f;
     float d[CH][8];
@@ -318,9 +312,7 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
         float x[8], w[8], g[8];
         cur.x[c].get(x);
         cur.dn[c].get(w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = 1.f;
-        if (p.gamma && in[c]) load8(gains + (c * NT + lane) * 8, g);
+        load_gain(gains, ln, c, p.gamma ? C : 0, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float t = w[e] * (x[e] * inv);
@@ -333,23 +325,20 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
     s = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int j = (c * NT + lane) * 8;
       float v[8];
       cur.dx[c].get(d[c]);
       if (p.dn) {
         float x[8], w[8], g[8];
         cur.x[c].get(x);
         cur.dn[c].get(w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = 1.f;
-        if (p.gamma && in[c]) load8(gains + j, g);
+        load_gain(gains, ln, c, p.gamma ? C : 0, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[c][e] = fmaf(fmaf(-(x[e] * inv), m, w[e] * g[e]), inv, d[c][e]);
       }
       if (p.dx) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = p.res_scale * d[c][e];
-        if (live && in[c]) store8(static_cast<R*>(p.dx) + base + j, v);
+        if (live) store8<S>(static_cast<R*>(p.dx) + base, ln, c, C, v);
       }
       if (!p.block) continue;
       float g[8];
@@ -361,9 +350,7 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
       if constexpr (Y) {
         float y[8], gp[8];
         cur.y[c].get(y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) gp[e] = 1.f;
-        if (post && in[c]) load8(gains + CMAX + j, gp);
+        load_gain(gains + CMAX, ln, c, post ? C : 0, gp);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           y[e] *= invp;
@@ -375,7 +362,7 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
           d[c][e] *= gp[e];
           s = fmaf(d[c][e], y[e], s);
         }
-        if (p.gate_each && live && in[c]) store8(static_cast<D*>(p.dgate) + base + j, v);
+        if (p.gate_each && live) store8<S>(static_cast<D*>(p.dgate) + base, ln, c, C, v);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[c][e] *= p.block_scale * g[e];
@@ -393,14 +380,14 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[c][e] = fmaf(-(y[e] * invp), m, d[c][e]) * invp;
           }
-          if (live && in[c]) store8(static_cast<D*>(p.dy) + base + (c * NT + lane) * 8, d[c]);
+          if (live) store8<S>(static_cast<D*>(p.dy) + base, ln, c, C, d[c]);
         }
       }
     }
     if constexpr (Y) {
       if (next_seg != seg && p.dgate && !p.part_t && !p.gate_each) {
         const int64_t gate_row = seg / p.gate_tokens;
-        fold(acc_t, [&](int j, const float (&v)[8]) { store8(static_cast<D*>(p.dgate) + gate_row * p.C + j, v); });
+        fold(acc_t, [&](int c, const float (&v)[8]) { store8<false>(static_cast<D*>(p.dgate) + gate_row * C, ln, c, C, v); });
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -412,12 +399,12 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
     seg = next_seg;
     cur = ahead;
   }
-  const int64_t part = (int64_t)blockIdx.x * p.C;
+  const int64_t part = (int64_t)blockIdx.x * C;
   if constexpr (Y) {
-    if (p.part_t) fold(acc_t, [&](int j, const float (&v)[8]) { store8(p.part_t + part + j, v); });
-    if (p.part_p) fold(acc_p, [&](int j, const float (&v)[8]) { store8(p.part_p + part + j, v); });
+    if (p.part_t) fold(acc_t, [&](int c, const float (&v)[8]) { store8<false>(p.part_t + part, ln, c, C, v); });
+    if (p.part_p) fold(acc_p, [&](int c, const float (&v)[8]) { store8<false>(p.part_p + part, ln, c, C, v); });
   }
-  if (p.part_g) fold(acc_g, [&](int j, const float (&v)[8]) { store8(p.part_g + part + j, v); });
+  if (p.part_g) fold(acc_g, [&](int c, const float (&v)[8]) { store8<false>(p.part_g + part, ln, c, C, v); });
 }
 
 // Column sums of partial rows, up to three sets in one launch: blockIdx.y 0 is
@@ -463,25 +450,41 @@ __global__ __launch_bounds__(1024) void col_sums_kernel(const ColSums a) {
                                 : static_cast<float*>(a.dgate) + (int64_t)(which - 2) * a.C) + c) = s;
 }
 
+// Whether a call that reads and writes so many bytes passes the caches by: more
+// than the 256 MB behind the L2, so that nothing of it would be found there.
+// 8-bit rows of 65536 x 1536 bf16 (302 MB): 53 us (75 through the caches); a norm
+// step of 75 MB whose inputs were in the cache: 22 us (17 through it).
+bool streams(int64_t bytes) { return bytes > (int64_t)256 << 20; }
+
 // rows of the grid: at most `per_cu` workgroups on each of the 256 CUs
 int row_grid(int64_t T, int nr, int per_cu) {
   const int64_t need = (T + nr - 1) / nr;
   return (int)(need < 256 * per_cu ? need : 256 * per_cu);
 }
 
+template <typename F>
+void by_flags(bool a, bool b, F f) {
+  if (a) b ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  else b ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+}
 template <typename R, typename D, int NT, int CH>
-hipError_t launch_norm_t(const NormParams& p, hipStream_t st) {
+hipError_t launch_norm_t(const NormParams& p, bool stream, hipStream_t st) {
   constexpr int WG = wg_of(NT);
-  const dim3 grid(row_grid(p.T, WG / NT, 2048 / WG));
-  if (p.q) hipLaunchKernelGGL((block_norm_kernel<R, D, NT, CH, true>), grid, dim3(WG), 0, st, p);
-  else hipLaunchKernelGGL((block_norm_kernel<R, D, NT, CH, false>), grid, dim3(WG), 0, st, p);
+  // a stream to two fp tensors runs best with 8 waves a CU: 65536 x 4096 bf16 375 us
+  // (425 with 32, 398 with 12, 542 with 4); 8-bit output and short calls with 32
+  const int per_cu = stream && !p.q ? std::max(1, 512 / WG) : 2048 / WG;
+  by_flags(p.q != nullptr, stream, [&](auto q8, auto s) {
+    hipLaunchKernelGGL((block_norm_kernel<R, D, NT, CH, decltype(q8)::value, decltype(s)::value>),
+                       dim3(row_grid(p.T, WG / NT, per_cu)), dim3(WG), 0, st, p);
+  });
   return hipGetLastError();
 }
 template <typename R, typename D, int NT, int CH>
-hipError_t launch_norm_grad_t(const NormGradParams& p, hipStream_t st) {
-  const dim3 grid((unsigned)p.n_wg), wg(wg_of(NT));
-  if (p.y) hipLaunchKernelGGL((block_norm_backward_kernel<R, D, NT, CH, true>), grid, wg, 0, st, p);
-  else hipLaunchKernelGGL((block_norm_backward_kernel<R, D, NT, CH, false>), grid, wg, 0, st, p);
+hipError_t launch_norm_grad_t(const NormGradParams& p, bool stream, hipStream_t st) {
+  by_flags(p.y != nullptr, stream, [&](auto y, auto s) {
+    hipLaunchKernelGGL((block_norm_backward_kernel<R, D, NT, CH, decltype(y)::value, decltype(s)::value>),
+                       dim3((unsigned)p.n_wg), dim3(wg_of(NT)), 0, st, p);
+  });
   return hipGetLastError();
 }
 
@@ -518,10 +521,12 @@ hipError_t by_types(int res_bf16, int io_bf16, F f) {
 
 hipError_t launch_block_norm(const NormParams& p, int res_bf16, int io_bf16, hipStream_t st) {
   if (p.T == 0) return hipSuccess;
+  const int rs = res_bf16 ? 2 : 4, io = io_bf16 ? 2 : 4;
+  const bool stream = streams(p.T * p.C * (rs + (p.y ? rs + io : 0) + (p.q ? 1 : p.n ? io : 0)));
   return by_types(res_bf16, io_bf16, [&](auto r, auto d) {
     return by_width(p.C, [&](auto nt, auto ch) {
       return launch_norm_t<std::remove_pointer_t<decltype(r)>, std::remove_pointer_t<decltype(d)>,
-                           decltype(nt)::value, decltype(ch)::value>(p, st);
+                           decltype(nt)::value, decltype(ch)::value>(p, stream, st);
     });
   });
 }
@@ -559,10 +564,13 @@ NormGradGeometry norm_grad_geometry(int64_t T, int C, int64_t gate_tokens) {
 
 hipError_t launch_block_norm_backward(const NormGradParams& p, int res_bf16, int io_bf16, float* dgamma,
                                       float* dgamma_post, hipStream_t st) {
+  const int rs = res_bf16 ? 2 : 4, io = io_bf16 ? 2 : 4;
+  const bool stream = streams(p.T * p.C * ((p.dn ? rs + io : 0) + (p.dx_out ? rs : 0) + (p.y ? io : 0) + (p.dx ? rs : 0) +
+                                  (p.dy ? io : 0) + (p.gate_each ? io : 0)));
   hipError_t e = p.n_wg == 0 ? hipSuccess : by_types(res_bf16, io_bf16, [&](auto r, auto d) {
     return by_width(p.C, [&](auto nt, auto ch) {
       return launch_norm_grad_t<std::remove_pointer_t<decltype(r)>, std::remove_pointer_t<decltype(d)>,
-                                decltype(nt)::value, decltype(ch)::value>(p, st);
+                                decltype(nt)::value, decltype(ch)::value>(p, stream, st);
     });
   });
   if (e == hipSuccess && (p.part_g || p.part_p || p.part_t)) {
@@ -581,12 +589,14 @@ hipError_t launch_quant_t(const D* x, int64_t n, int K, int pitch, int8_t* q, fl
     hipLaunchKernelGGL((quant_long_rows_kernel<D>), dim3(row_grid(n, 1, 2)), dim3(1024), 0, st, x, n, K, pitch, q, scale);
     return hipGetLastError();
   }
-  const bool vec = (K * (int)sizeof(D)) % 16 == 0 && K % 8 == 0;
+  const bool vec = K % 8 == 0;
+  const bool stream = vec && streams(n * ((int64_t)K * sizeof(D) + pitch));
   return by_quant_width(pitch, [&](auto nt, auto ch) {
     constexpr int NT = decltype(nt)::value, CH = decltype(ch)::value, WG = wg_of(NT);
     const dim3 grid(row_grid(n, WG / NT, 2048 / WG));
-    if (vec) hipLaunchKernelGGL((quant_rows_kernel<D, NT, CH, true>), grid, dim3(WG), 0, st, x, n, K, pitch, q, scale);
-    else hipLaunchKernelGGL((quant_rows_kernel<D, NT, CH, false>), grid, dim3(WG), 0, st, x, n, K, pitch, q, scale);
+    if (stream) hipLaunchKernelGGL((quant_rows_kernel<D, NT, CH, true, true>), grid, dim3(WG), 0, st, x, n, K, pitch, q, scale);
+    else if (vec) hipLaunchKernelGGL((quant_rows_kernel<D, NT, CH, true, false>), grid, dim3(WG), 0, st, x, n, K, pitch, q, scale);
+    else hipLaunchKernelGGL((quant_rows_kernel<D, NT, CH, false, false>), grid, dim3(WG), 0, st, x, n, K, pitch, q, scale);
     return hipGetLastError();
   });
 }
