@@ -576,35 +576,30 @@ def affinity_up_static(dims: hna_dims, a, g, u, r, r_next, M, wd_sq, group_of_he
 # These calls are made token by token too, where a call's time is the host's, so
 # their checks are written for speed: sizes compared as tuples, devices by index,
 # pointers and streams as plain integers.
-class _on:
-    """The tensors' device as the current one while a call is enqueued, so that
-    launches go to their GPU and its current stream (the context's value)."""
-    __slots__ = ("index", "guard")
+def _index_of(*ts) -> int:
+    """The one GPU that all tensors live on."""
+    index = None
+    for t in ts:
+        if t is not None:
+            i = t.get_device()
+            if i < 0:
+                raise ValueError("all tensors must live on the GPU")
+            if not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous")
+            if index is None:
+                index = i
+            elif i != index:
+                raise ValueError("all tensors must live on the same GPU")
+    return index
 
-    def __init__(self, *ts):
-        index = None
-        for t in ts:
-            if t is not None:
-                i = t.get_device()
-                if i < 0:
-                    raise ValueError("all tensors must live on the GPU")
-                if not t.is_contiguous():
-                    raise ValueError("all tensors must be contiguous")
-                if index is None:
-                    index = i
-                elif i != index:
-                    raise ValueError("all tensors must live on the same GPU")
-        self.index = index
-        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
+def _current() -> int:
+    return torch._C._cuda_getDevice()
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _raw_stream(index: int) -> int:
+    """torch's current stream on GPU `index`, which has to be the current one for a launch."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -670,18 +665,22 @@ def block_norm(x, y=None, gamma=None, *, gamma_post=None, gate=None, gate_tokens
     """
     dims, dt = _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, dtype, x_out, r, r_post)
     _is(n, "n", x.shape, dt)
-    with _on(x, y, gamma, gamma_post, gate, x_out, n, r, r_post) as stream:
-        if x_out is None and y is not None:
-            x_out = torch.empty_like(x)
-        if n is None:
-            n = torch.empty_like(x, dtype=dt)
-        if r is None:
-            r = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-        if r_post is None and gamma_post is not None:
-            r_post = torch.empty_like(r)
-        _check(lib().hna_block_norm(ctypes.byref(dims), _at(x), _at(y), _at(gate), _at(gamma), _at(gamma_post),
-                                    res_scale, block_scale, eps, _at(x_out), _at(n), _at(r), _at(r_post),
-                                    stream), "hna_block_norm")
+    index = _index_of(x, y, gamma, gamma_post, gate, x_out, n, r, r_post)
+    if index != _current():
+        with torch.cuda.device(index):
+            return block_norm(x, y, gamma, gamma_post=gamma_post, gate=gate, gate_tokens=gate_tokens, res_scale=res_scale,
+                              block_scale=block_scale, eps=eps, dtype=dtype, x_out=x_out, n=n, r=r, r_post=r_post)
+    if x_out is None and y is not None:
+        x_out = torch.empty_like(x)
+    if n is None:
+        n = torch.empty_like(x, dtype=dt)
+    if r is None:
+        r = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    if r_post is None and gamma_post is not None:
+        r_post = torch.empty_like(r)
+    _check(lib().hna_block_norm(ctypes.byref(dims), _at(x), _at(y), _at(gate), _at(gamma), _at(gamma_post),
+                                res_scale, block_scale, eps, _at(x_out), _at(n), _at(r), _at(r_post),
+                                _raw_stream(index)), "hna_block_norm")
     return (x if y is None else x_out), n, r, r_post
 
 
@@ -694,20 +693,25 @@ def block_norm_quant(x, y=None, gamma=None, *, gamma_post=None, gate=None, gate_
     pitch = (C + 15) // 16 * 16
     _is(q, "q", (T, pitch), torch.int8)
     _is(q_scale, "q_scale", (T,), torch.float32)
-    with _on(x, y, gamma, gamma_post, gate, x_out, q, q_scale, r, r_post) as stream:
-        if x_out is None and y is not None:
-            x_out = torch.empty_like(x)
-        if q is None:
-            q = torch.empty((T, pitch), dtype=torch.int8, device=x.device)
-        if q_scale is None:
-            q_scale = torch.empty(T, dtype=torch.float32, device=x.device)
-        if r is None:
-            r = torch.empty_like(q_scale)
-        if r_post is None and gamma_post is not None:
-            r_post = torch.empty_like(q_scale)
-        _check(lib().hna_block_norm_quant(ctypes.byref(dims), _at(x), _at(y), _at(gate), _at(gamma),
-                                          _at(gamma_post), res_scale, block_scale, eps, _at(x_out), _at(q),
-                                          _at(q_scale), _at(r), _at(r_post), stream), "hna_block_norm_quant")
+    index = _index_of(x, y, gamma, gamma_post, gate, x_out, q, q_scale, r, r_post)
+    if index != _current():
+        with torch.cuda.device(index):
+            return block_norm_quant(x, y, gamma, gamma_post=gamma_post, gate=gate, gate_tokens=gate_tokens,
+                                    res_scale=res_scale, block_scale=block_scale, eps=eps, x_out=x_out, q=q,
+                                    q_scale=q_scale, r=r, r_post=r_post)
+    if x_out is None and y is not None:
+        x_out = torch.empty_like(x)
+    if q is None:
+        q = torch.empty((T, pitch), dtype=torch.int8, device=x.device)
+    if q_scale is None:
+        q_scale = torch.empty(T, dtype=torch.float32, device=x.device)
+    if r is None:
+        r = torch.empty_like(q_scale)
+    if r_post is None and gamma_post is not None:
+        r_post = torch.empty_like(q_scale)
+    _check(lib().hna_block_norm_quant(ctypes.byref(dims), _at(x), _at(y), _at(gate), _at(gamma),
+                                      _at(gamma_post), res_scale, block_scale, eps, _at(x_out), _at(q),
+                                      _at(q_scale), _at(r), _at(r_post), _raw_stream(index)), "hna_block_norm_quant")
     return (x if y is None else x_out), q, q_scale, r, r_post
 
 
@@ -755,27 +759,33 @@ def block_norm_backward(x_out, r, *, dn=None, dx_out=None, gamma=None, y=None, g
     _is(dgamma_post, "dgamma_post", (C,), f32)
     if dgate is not None:
         _is(dgate, "dgate", gate.shape, dt)
-    with _on(x_out, r, dn, dx_out, gamma, y, gamma_post, r_post, gate, dx, dy, dgamma, dgamma_post, dgate,
-             workspace) as stream:
-        if dx is None:
-            dx = torch.empty_like(x_out)
-        if dy is None and want_dy:
-            dy = torch.empty_like(x_out, dtype=dt)
-        if dgamma is None and gamma is not None and dn is not None:
-            dgamma = torch.empty_like(gamma)
-        if dgamma_post is None and gamma_post is not None:
-            dgamma_post = torch.empty_like(gamma_post)
-        if dgate is None and gate is not None and y is not None:
-            dgate = torch.empty_like(gate)
-        L = lib()
-        if workspace is None:
-            workspace = torch.empty(L.hna_block_norm_workspace_bytes(ctypes.byref(dims)) or 16,
-                                    dtype=torch.uint8, device=x_out.device)
-        _check(L.hna_block_norm_backward(
-            ctypes.byref(dims), _at(dn), _at(dx_out), _at(x_out), _at(y), _at(gate), _at(gamma), _at(gamma_post),
-            _at(r), _at(r_post), res_scale, block_scale, _at(dx), _at(dy), _at(dgamma), _at(dgamma_post),
-            _at(dgate), _at(workspace), workspace.numel() * workspace.element_size(), stream),
-            "hna_block_norm_backward")
+    index = _index_of(x_out, r, dn, dx_out, gamma, y, gamma_post, r_post, gate, dx, dy, dgamma,
+                      dgamma_post, dgate, workspace)
+    if index != _current():
+        with torch.cuda.device(index):
+            return block_norm_backward(x_out, r, dn=dn, dx_out=dx_out, gamma=gamma, y=y, gamma_post=gamma_post,
+                                       r_post=r_post, gate=gate, gate_tokens=gate_tokens, res_scale=res_scale,
+                                       block_scale=block_scale, want_dy=want_dy, dx=dx, dy=dy, dgamma=dgamma,
+                                       dgamma_post=dgamma_post, dgate=dgate, workspace=workspace)
+    if dx is None:
+        dx = torch.empty_like(x_out)
+    if dy is None and want_dy:
+        dy = torch.empty_like(x_out, dtype=dt)
+    if dgamma is None and gamma is not None and dn is not None:
+        dgamma = torch.empty_like(gamma)
+    if dgamma_post is None and gamma_post is not None:
+        dgamma_post = torch.empty_like(gamma_post)
+    if dgate is None and gate is not None and y is not None:
+        dgate = torch.empty_like(gate)
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(L.hna_block_norm_workspace_bytes(ctypes.byref(dims)) or 16,
+                                dtype=torch.uint8, device=x_out.device)
+    _check(L.hna_block_norm_backward(
+        ctypes.byref(dims), _at(dn), _at(dx_out), _at(x_out), _at(y), _at(gate), _at(gamma), _at(gamma_post),
+        _at(r), _at(r_post), res_scale, block_scale, _at(dx), _at(dy), _at(dgamma), _at(dgamma_post),
+        _at(dgate), _at(workspace), workspace.numel() * workspace.element_size(), _raw_stream(index)),
+        "hna_block_norm_backward")
     return {"dx": dx, "dy": dy if want_dy else None, "dgamma": dgamma, "dgamma_post": dgamma_post,
             "dgate": dgate}
 
@@ -795,12 +805,15 @@ def quant_rows(x, q=None, scale=None):
     pitch = (K + 15) // 16 * 16
     _is(q, "q", (rows, pitch), torch.int8)
     _is(scale, "scale", (rows,), torch.float32)
-    with _on(x, q, scale) as stream:
-        if q is None:
-            q = torch.empty((rows, pitch), dtype=torch.int8, device=x.device)
-        if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-        _check(lib().hna_quant_rows(rows, K, code, _at(x), _at(q), _at(scale), stream), "hna_quant_rows")
+    index = _index_of(x, q, scale)
+    if index != _current():
+        with torch.cuda.device(index):
+            return quant_rows(x, q, scale)
+    if q is None:
+        q = torch.empty((rows, pitch), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _check(lib().hna_quant_rows(rows, K, code, _at(x), _at(q), _at(scale), _raw_stream(index)), "hna_quant_rows")
     return q, scale
 
 
@@ -819,11 +832,14 @@ def quant_matmul(q, q_scale, w, w_scale, out=None, dtype: torch.dtype = torch.bf
         dtype = out.dtype
         _is(out, "out", (T, N), dtype)
     code = _code(dtype)
-    with _on(q, q_scale, w, w_scale, out) as stream:
-        if out is None:
-            out = torch.empty((T, N), dtype=dtype, device=q.device)
-        _check(lib().hna_quant_matmul(T, N, K, code, _at(q), _at(q_scale), _at(w), _at(w_scale), _at(out), stream),
-               "hna_quant_matmul")
+    index = _index_of(q, q_scale, w, w_scale, out)
+    if index != _current():
+        with torch.cuda.device(index):
+            return quant_matmul(q, q_scale, w, w_scale, out, dtype)
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype, device=q.device)
+    _check(lib().hna_quant_matmul(T, N, K, code, _at(q), _at(q_scale), _at(w), _at(w_scale), _at(out), _raw_stream(index)),
+           "hna_quant_matmul")
     return out
 
 
@@ -848,11 +864,14 @@ def quant_matmul_pair(q, q_scale, w0, w0_scale, w1, w1_scale, out0=None, out1=No
     _is(out0, "out0", (T, N), dtype)
     _is(out1, "out1", (T, N), dtype)
     code = _code(dtype)
-    with _on(q, q_scale, w0, w0_scale, w1, w1_scale, out0, out1) as stream:
-        if out0 is None:
-            out0 = torch.empty((T, N), dtype=dtype, device=q.device)
-        if out1 is None:
-            out1 = torch.empty_like(out0)
-        _check(lib().hna_quant_matmul_pair(T, N, K, code, _at(q), _at(q_scale), _at(w0), _at(w0_scale), _at(w1),
-                                           _at(w1_scale), _at(out0), _at(out1), stream), "hna_quant_matmul_pair")
+    index = _index_of(q, q_scale, w0, w0_scale, w1, w1_scale, out0, out1)
+    if index != _current():
+        with torch.cuda.device(index):
+            return quant_matmul_pair(q, q_scale, w0, w0_scale, w1, w1_scale, out0, out1, dtype)
+    if out0 is None:
+        out0 = torch.empty((T, N), dtype=dtype, device=q.device)
+    if out1 is None:
+        out1 = torch.empty_like(out0)
+    _check(lib().hna_quant_matmul_pair(T, N, K, code, _at(q), _at(q_scale), _at(w0), _at(w0_scale), _at(w1),
+                                       _at(w1_scale), _at(out0), _at(out1), _raw_stream(index)), "hna_quant_matmul_pair")
     return out0, out1

@@ -191,3 +191,49 @@ def test_python_refuses_host_tensors_and_bad_shapes(hna):
                  lambda: hna.quant_matmul(i8, torch.ones(4), i8, torch.ones(4), dtype=torch.float16)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_calls_run_with_their_tensors_gpu_current(hna, monkeypatch):
+    """Tensors of GPU 1 while GPU 0 is current: the call is made with GPU 1 current, on GPU 1's stream
+    (a stand-in for the library records the calls; nothing is launched)."""
+    import torch
+    from head_neuron_affinity_amd import _binding as B
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+
+    class Lib:
+        def __getattr__(self, name):
+            def call(*args):
+                if name.endswith("workspace_bytes"):
+                    return 256
+                seen.append((name, now[0], args[-1]))
+                return 0
+            return call
+
+    monkeypatch.setattr(B, "_index_of", lambda *ts: 1)
+    monkeypatch.setattr(B, "_current", lambda: now[0])
+    monkeypatch.setattr(B, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(B, "lib", lambda: Lib())
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    x, g, one = torch.zeros(4, 64), torch.ones(64), torch.ones(4)
+    i8 = torch.zeros(4, 64, dtype=torch.int8)
+    hna.block_norm(x, x, g, gamma_post=g, gate=x, gate_tokens=1, res_scale=2.0, block_scale=3.0, eps=0.5)
+    hna.block_norm_quant(x, x, g, gamma_post=g, gate=x, gate_tokens=1, res_scale=2.0, block_scale=3.0, eps=0.5)
+    got = hna.block_norm_backward(x, one, dn=x, dx_out=x, gamma=g, y=x, gamma_post=g, r_post=one, gate=x, gate_tokens=1,
+                                  res_scale=2.0, block_scale=3.0, want_dy=True)
+    hna.quant_rows(x)
+    hna.quant_matmul(i8, one, i8, one, dtype=torch.float32)
+    a, b = hna.quant_matmul_pair(i8, one, i8, one, i8, one, dtype=torch.float32)
+    assert [s[0] for s in seen] == ["hna_block_norm", "hna_block_norm_quant", "hna_block_norm_backward",
+                                    "hna_quant_rows", "hna_quant_matmul", "hna_quant_matmul_pair"]
+    assert all(s[1:] == (1, 1001) for s in seen) and now == [0]
+    assert all(got[k] is not None for k in got) and a.dtype == b.dtype == torch.float32
