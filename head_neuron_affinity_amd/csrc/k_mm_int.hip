@@ -460,39 +460,50 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
     unsigned char* stg = stage_out + w * 32 * PITCH;
     const float* sw = scales[par] + wm * 128;
     const float* sq = scales[par] + BM + wn * 128;
-    constexpr int CH = 128 / E / 32;                      // 32-channel tiles per 128 bytes
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t tj = t0 + j * 32;
+    constexpr int CH = 128 / E / 32, G = 16 / CH;         // 32-channel tiles per 128 bytes; steps of the epilogue
+    typedef std::conditional_t<BF16, uint2, float4> Four; // 4 outputs
+    Four vals[CH * 4];
+    // step s: tokens 32 (s CH / 4) .., channels 32 (s CH % 4) ..
+    auto make = [&](auto sc) __attribute__((always_inline)) {
+      constexpr int s = decltype(sc)::value, j = s * CH / 4, i0 = s * CH % 4;
       const float st = sq[j * 32 + (le & 31)];
+#pragma unroll
+      for (int i = i0; i < i0 + CH; ++i)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const float4 s4 = *reinterpret_cast<const float4*>(sw + i * 32 + 8 * a + 4 * (le >> 5));
+          const float f[4] = {(float)acc[i][j][4 * a] * st * s4.x, (float)acc[i][j][4 * a + 1] * st * s4.y,
+                              (float)acc[i][j][4 * a + 2] * st * s4.z, (float)acc[i][j][4 * a + 3] * st * s4.w};
+          if constexpr (BF16) vals[(i - i0) * 4 + a] = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+          else vals[(i - i0) * 4 + a] = make_float4(f[0], f[1], f[2], f[3]);
+        }
+    };
+    make(std::integral_constant<int, 0>{});
+    static_for<0, G>([&](auto sc) __attribute__((always_inline)) {
+      constexpr int s = decltype(sc)::value, j = s * CH / 4, i0 = s * CH % 4;
+      const int64_t tj = t0 + j * 32;
       const int64_t rows = min<int64_t>(32, p.T - tj), ob = rows > 0 ? rows * p.N * E : 0;
       const __amdgpu_buffer_rsrc_t ro = buffer_rsrc(static_cast<unsigned char*>(here.z ? p.out[1] : p.out[0]) + (rows > 0 ? tj * p.N * E : 0), (uint32_t)ob);
+      const int nb = n0 + i0 * 32;                        // the first of 128 / E channels
 #pragma unroll
-      for (int i0 = 0; i0 < 4; i0 += CH) {
+      for (int x = 0; x < CH * 4; ++x)
+        *reinterpret_cast<Four*>(stg + (le & 31) * PITCH + (8 * x + 4 * (le >> 5)) * E) = vals[x];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (WIDE) {
+        u32x4 v[4];
 #pragma unroll
-        for (int i = i0; i < i0 + CH; ++i)
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const int n = i * 32 + 8 * a + 4 * (le >> 5);
-            const float4 s4 = *reinterpret_cast<const float4*>(sw + n);
-            const float f[4] = {(float)acc[i][j][4 * a] * st * s4.x, (float)acc[i][j][4 * a + 1] * st * s4.y,
-                                (float)acc[i][j][4 * a + 2] * st * s4.z, (float)acc[i][j][4 * a + 3] * st * s4.w};
-            unsigned char* d = stg + (le & 31) * PITCH + (n - i0 * 32) * E;
-            if constexpr (BF16) *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-            else *reinterpret_cast<float4*>(d) = make_float4(f[0], f[1], f[2], f[3]);
-          }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const u32x4*>(stg + (k * 8 + (le >> 3)) * PITCH + (le & 7) * 16);
         __builtin_amdgcn_sched_barrier(0);
-        const int nb = n0 + i0 * 32;                      // the first of 128 / E channels
-        if constexpr (WIDE) {
+        if constexpr (s + 1 < G) make(std::integral_constant<int, s + 1 < G ? s + 1 : 0>{});   // while the reads run
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row = k * 8 + (le >> 3), n = nb + (le & 7) * (16 / E);
-            const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * PITCH + (le & 7) * 16);
-            const uint32_t off = n < p.N ? (uint32_t)(row * p.N + n) * E : 0xfffffff0u;
-            __builtin_amdgcn_raw_buffer_store_b128(v, ro, (int)off, 0, 0);
-          }
-        } else if constexpr (!BF16) {
+        for (int k = 0; k < 4; ++k) {
+          const int row = k * 8 + (le >> 3), n = nb + (le & 7) * (16 / E);
+          const uint32_t off = n < p.N ? (uint32_t)(row * p.N + n) * E : 0xfffffff0u;
+          __builtin_amdgcn_raw_buffer_store_b128(v[k], ro, (int)off, 0, 2);   // non-temporal: the panels stay in L2
+        }
+      } else {
+        if constexpr (!BF16) {
           for (int k = 0; k < 16; ++k) {
             const int row = k * 2 + (le >> 5), n = nb + (le & 31);
             const uint32_t v = *reinterpret_cast<const uint32_t*>(stg + row * PITCH + (le & 31) * 4);
@@ -517,10 +528,11 @@ __global__ __launch_bounds__(256, 1) void mm_int_big_kernel(const IntMmParams p)
             __builtin_amdgcn_raw_buffer_store_b16(v, ro, on ? (int)((uint32_t)(row * p.N + nb + c) * 2u) : (int)0xfffffff0u, 0, 0);
           }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (s + 1 < G) make(std::integral_constant<int, s + 1 < G ? s + 1 : 0>{});
       }
-    }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    });
     if constexpr (WIDE) stored = true;
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // a varying number of stores
     tile = after(tile);
