@@ -236,11 +236,12 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG) void mm_int_kernel(const IntMm
 // an XCD its share of the panels it has in common with its neighbours.
 // (The scales of a tile come with its first step, into the half of their
 // buffer that the tile before the last one had: a tile has two steps at least.)
-// Measured (operations a second): 16384 x 14336 x 4096 0.75 ms, 2.58e15, MFMAs
-// busy 70% of the cycles at 1.76 GHz: the clock that power leaves (zeros: 3.4e15,
-// and 4.1e15 with the copies taken out).  65536 x 1536 x 4096 0.41 ms, 2.0e15: the
-// epilogue's 5 us a tile, not behind MFMAs, against 20 us of steps.  An int32
-// library product reached 2.2 to 2.5e15 on these sizes.
+// Measured (operations a second), T x K x N: 16384 x 14336 x 4096 0.73 to 0.75
+// ms, 2.6e15, MFMAs busy 70% of the cycles at 1.76 GHz: the clock that power
+// leaves (an earlier form: 2.25e15, on zeros 3.4e15).  65536 x 1536 x 4096 0.40 to
+// 0.41 ms, 2.0e15: 5.5 us of a tile's 25.6 pass outside its steps (from K 1024,
+// 2048 and 4096).  The first dozen calls after an idle time take up to 0.87 and
+// 0.53 ms.  An int32 library product: 2.25 to 2.4e15 and 1.7e15.
 // Every wait counts operations in flight, so a step issues the same number of
 // them everywhere: reads past the end of an operand return zeros and stores
 // past the end of out are dropped by the buffer's range.
