@@ -633,6 +633,7 @@ def _norm_dims(like, dtype: torch.dtype, gate, gate_tokens, name) -> hna_norm_di
     if gate_tokens < 1:
         raise ValueError(f"gate_tokens: {gate_tokens} < 1")
     _is(gate, "gate", (-(-T // gate_tokens), hidden), dtype)
+    gate_tokens = min(gate_tokens, max(T, 1))    # T or more is one row for all; larger ints would wrap in the struct
     return hna_norm_dims(T, gate_tokens, hidden, _code(dtype), _code(like.dtype))
 
 

@@ -193,6 +193,15 @@ def test_python_refuses_host_tensors_and_bad_shapes(hna):
             call()
 
 
+@pytest.mark.parametrize("gate_tokens", [None, 4, 5, 2**31, 2**63, 2**64 + 1])
+def test_gate_tokens_of_any_size_reach_the_library_whole(hna, gate_tokens):
+    """One gate row for all tokens stays that, also where gate_tokens does not fit the struct's 64 bits."""
+    import torch
+    from head_neuron_affinity_amd import _binding as B
+    x = torch.zeros(4, 64)
+    assert B._norm_dims(x, torch.float32, x[:1], gate_tokens, "x").gate_tokens == 4
+
+
 def test_calls_run_with_their_tensors_gpu_current(hna, monkeypatch):
     """Tensors of GPU 1 while GPU 0 is current: the call is made with GPU 1 current, on GPU 1's stream
     (a stand-in for the library records the calls; nothing is launched)."""
