@@ -380,10 +380,12 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
           if constexpr (Y) {
-            float y[8];
-            cur.y[c].get(y);
+            if (post) {                                   // else dy does not depend on y, and 0 y would not be 0 for a NaN
+              float y[8];
+              cur.y[c].get(y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[c][e] = fmaf(-(y[e] * invp), m, d[c][e]) * invp;
+              for (int e = 0; e < 8; ++e) d[c][e] = fmaf(-(y[e] * invp), m, d[c][e]) * invp;
+            }
           }
           if (live) store8<S>(static_cast<D*>(p.dy) + base, ln, c, C, d[c]);
         }
