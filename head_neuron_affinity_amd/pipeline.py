@@ -118,35 +118,39 @@ def affinity_layer(layer: Dict[str, torch.Tensor], with_down: bool = True) -> Di
 
 
 def ffn_inputs(x, gamma, w_gate, w_up, y=None, gamma_post=None, gate=None, gate_tokens=None,
-               res_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6) -> Dict[str, torch.Tensor]:
+               res_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6,
+               dtype: torch.dtype = torch.bfloat16) -> Dict[str, torch.Tensor]:
     """What the affinity pass reads of a layer's FFN, from the residual x [T, hidden] before the
     attention output y (or after it, with y None): the norm step, its result as 8-bit rows, and the
     products with the 8-bit W_gate and W_up, each a (rows, scales) pair of quant_rows.
 
-    Returns x_in (the residual entering the FFN pre-norm, x's type), r [T] fp32, g and u [T, I]
-    bf16, under the names a layer dict of AffinityPass has them, and scale, the tokens' 8-bit scales.
+    Returns x_in (the residual entering the FFN pre-norm, x's type), r [T] fp32, g and u [T, I] in
+    dtype, under the names a layer dict of AffinityPass has them, and scale, the tokens' 8-bit scales.
+    AffinityPass takes g and u in the type of the layer's a and weights; its leave-one-out score
+    also reads x_in, in fp32: give it an fp32 x (y may be bf16).
     """
     x_in, q, scale, r, _ = B.block_norm_quant(x, y, gamma, gamma_post=gamma_post, gate=gate,
                                               gate_tokens=gate_tokens, res_scale=res_scale,
                                               block_scale=block_scale, eps=eps)
-    g, u = B.quant_matmul_pair(q, scale, *w_gate, *w_up)
+    g, u = B.quant_matmul_pair(q, scale, *w_gate, *w_up, dtype=dtype)
     return {"x_in": x_in, "r": r, "scale": scale, "g": g, "u": u}
 
 
 class FfnInputs:
     """ffn_inputs with a layer's weights held as 8-bit rows, quantised once per channel:
     `layer.update(FfnInputs(layer).run(layer["x_in"]))` gives an affinity pass the r, g and u of the
-    layer as it runs with 8-bit weights and activations."""
+    layer as it runs with 8-bit weights and activations, g and u in the type of the layer's weights."""
 
     def __init__(self, layer: Dict[str, torch.Tensor], eps: float = 1e-6):
         self.gamma = layer["gamma"]
         self.w_gate = B.quant_rows(layer["W_gate"])
         self.w_up = B.quant_rows(layer["W_up"])
+        self.dtype = layer["W_gate"].dtype
         self.eps = eps
 
     def run(self, x: torch.Tensor, y: Optional[torch.Tensor] = None, **step) -> Dict[str, torch.Tensor]:
         """x, y and `step` (gamma_post, gate, gate_tokens, res_scale, block_scale) as for ffn_inputs."""
-        return ffn_inputs(x, self.gamma, self.w_gate, self.w_up, y=y, eps=self.eps, **step)
+        return ffn_inputs(x, self.gamma, self.w_gate, self.w_up, y=y, eps=self.eps, dtype=self.dtype, **step)
 
 
 class StackPass:

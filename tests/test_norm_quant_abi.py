@@ -246,3 +246,29 @@ def test_calls_run_with_their_tensors_gpu_current(hna, monkeypatch):
                                     "hna_quant_rows", "hna_quant_matmul", "hna_quant_matmul_pair"]
     assert all(s[1:] == (1, 1001) for s in seen) and now == [0]
     assert all(got[k] is not None for k in got) and a.dtype == b.dtype == torch.float32
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_layer_inputs_ask_for_the_layers_type(hna, monkeypatch, kind):
+    """FfnInputs asks for g and u in the type of the layer's weights, ffn_inputs for bf16 unless told
+    (the calls of the library are recorded, none is made)."""
+    import torch
+    from head_neuron_affinity_amd import _binding as B
+    dtype = torch.float32 if kind == "fp32" else torch.bfloat16
+    asked = []
+
+    def pair(q, s, w0, s0, w1, s1, out0=None, out1=None, dtype=torch.bfloat16):
+        asked.append(dtype)
+        return torch.empty(4, 8, dtype=dtype), torch.empty(4, 8, dtype=dtype)
+
+    monkeypatch.setattr(B, "quant_rows", lambda w: (torch.zeros(8, 64, dtype=torch.int8), torch.ones(8)))
+    monkeypatch.setattr(B, "block_norm_quant", lambda x, y, gamma, **kw: (x, None, None, torch.ones(4), None))
+    monkeypatch.setattr(B, "quant_matmul_pair", pair)
+    layer = {"gamma": torch.ones(64), "W_gate": torch.zeros(8, 64, dtype=dtype), "W_up": torch.zeros(8, 64, dtype=dtype)}
+    x = torch.zeros(4, 64)
+    got = hna.FfnInputs(layer).run(x)
+    assert got["g"].dtype == got["u"].dtype == dtype
+    w = B.quant_rows(None)
+    hna.ffn_inputs(x, layer["gamma"], w, w)
+    hna.ffn_inputs(x, layer["gamma"], w, w, dtype=torch.float32)
+    assert asked == [dtype, torch.bfloat16, torch.float32]
