@@ -88,3 +88,96 @@ def test_layer_inputs_take_a_type(hna):
         assert same, k
     with pytest.raises(TypeError):
         hna.ffn_inputs(s.x, s.gamma, *w, dtype=torch.float16, **kw)
+
+
+# ------------------------------------------------------------------------- large calls
+# widths of every lane count a row is spread over: 64 lanes (8 and 16 elements each), 128, .. 1024
+WIDTHS = [504, 1000, 2040, 4088, 8184, 16376]
+PAST_CACHES = 256 << 20                            # calls that move more go past the caches, on another grid
+
+
+def lanes(C):
+    return 64 if C <= 1024 else 128 if C <= 2048 else 256 if C <= 4096 else 512 if C <= 8192 else 1024
+
+
+def check_step(hna, s):
+    """Forward, 8-bit forward and backward (with and without y) of one large step against 64 bits, again in
+    place bit for bit."""
+    x_out, n, r, r_post = s.forward(hna.block_norm)
+    want = s.check_join(x_out, r, r_post)
+    ref.assert_within(n, want, want.abs(), s.io, "n")
+    xq, q, scale, rq, rpq = s.forward(hna.block_norm_quant)
+    same = [torch.equal(a, b) for a, b in ((xq, x_out), (rq, r), (rpq, r_post))]
+    assert all(same), same
+    top = want.abs().amax(1)
+    ref.assert_within(scale, top / 127, top / 127, F, "scale")
+    want.mul_((127 / top)[:, None])
+    off = float((q[:, :s.C].double() - want).abs().max())   # as in test_norm_quant
+    assert off <= 0.501 and not bool(q[:, s.C:].any()), off
+    del xq, q, want
+    # terms with ROUNDINGS each, then additions: one lane's rows (a workgroup's T / n_wg over the rows it has
+    # side by side), those rows' 4 sums, and the partial rows' 16 in a lane and a tree of 8
+    side, wgs = max(1, 256 // lanes(s.C)), 512 if lanes(s.C) <= 256 else 256
+    sums = ref.ROUNDINGS + -(-s.T // (side * wgs)) + side + 32
+    for keep_y in (True, False):
+        kw = {} if keep_y else dict(y=None, gamma_post=None)
+        y, gp, rp = (s.y, s.gamma_post, r_post) if keep_y else (None, None, None)
+        got = s.backward(hna, x_out, r, rp, **kw)
+        w = ref.gradients(wide(x_out), wide(r), wide(s.dn), wide(s.dx_out), wide(s.gamma), wide(y), wide(gp), wide(rp),
+                          wide(s.gate), s.gate_tokens, s.rs, s.bs)
+        for k, dtype in (("dx", s.res), ("dy", s.io), ("dgamma", F), ("dgamma_post", F), ("dgate", s.io)):
+            if k in w:
+                ref.assert_within(got[k], *w.pop(k), dtype, k, sums if k.startswith("dg") else ref.ROUNDINGS)
+        dn, dx_out = s.dn.clone(), s.dx_out.clone()
+        again = s.backward(hna, x_out, r, rp, dn=dn, dx_out=dx_out, dx=dx_out, dy=dn, **kw)
+        same = {k: got[k] is None or torch.equal(got[k], again[k]) for k in got}
+        assert all(same.values()), same
+    x, y = s.x, s.y
+    s.x, s.y = x.clone(), y.clone()
+    s.forward(hna.block_norm, x_out=s.x, n=s.y)
+    same = torch.equal(s.x, x_out) and torch.equal(s.y, n)
+    assert same
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("res,io", [(BF, BF), (F, BF), (F, F), (BF, F)])
+def test_norm_calls_past_the_caches(hna, C, res, io):
+    """Each of the four kinds of call moves more than 256 MB, on a number of rows that nothing divides."""
+    size = lambda t: 2 if t == BF else 4  # noqa: E731
+    T = PAST_CACHES // (C * (2 * size(res) + size(io) + 1)) + 7      # the 8-bit form moves least
+    T += 1 - T % 2
+    print(f"past the caches T={T} C={C} {res} {io}", flush=True)
+    check_step(hna, Step(T, C, res, io, gate=T // 3))
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("res,io", [(BF, BF), (F, BF)])
+def test_norm_calls_of_many_rows_a_workgroup(hna, C, res, io):
+    """Below that size: every workgroup of a full grid (2048 lanes on each of 256 CUs) goes on to a second
+    row, some to a third."""
+    T = 256 * 2048 // lanes(C) * 2 + 3
+    assert T * C * (12 if res == F else 8) < PAST_CACHES
+    print(f"rows a workgroup T={T} C={C} {res} {io}", flush=True)
+    check_step(hna, Step(T, C, res, io, gate=5))
+
+
+@pytest.mark.parametrize("K", [504, 1000, 1528, 2040, 4088, 8184, 16376])
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("large", [False, True])
+def test_quant_rows_of_many_rows_a_workgroup(hna, K, dtype, large):
+    """8-bit rows, exactly, where workgroups go on to further rows: within the caches and past them, and
+    (K off 8) element by element."""
+    for k in (K, K - 3):
+        if large:
+            rows = PAST_CACHES // (k * (2 if dtype == BF else 4) + k) + 7
+        else:
+            rows = 2 * 8192 + 3 if K <= 2048 else 3 * 2048 + 3 if K <= 8192 else 2 * 1024 + 3
+            assert rows * k * 5 < PAST_CACHES
+        print(f"8-bit rows {rows} x {k} {dtype}", flush=True)
+        x = torch.randn(rows, k, generator=torch.Generator(device="cuda").manual_seed(k), device="cuda").to(dtype)
+        x[rows - 2] = 0
+        q, scale = hna.quant_rows(x)
+        want, s = ref.quant(x.double())
+        same = torch.equal(q[:, :k].double(), want) and not bool(q[:, k:].any())
+        assert same
+        ref.assert_within(scale, s, s, F, "scale", 0)
