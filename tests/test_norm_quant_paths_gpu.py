@@ -181,3 +181,57 @@ def test_quant_rows_of_many_rows_a_workgroup(hna, K, dtype, large):
         same = torch.equal(q[:, :k].double(), want) and not bool(q[:, k:].any())
         assert same
         ref.assert_within(scale, s, s, F, "scale", 0)
+
+
+# ------------------------------------------------------- behind work on another stream
+def behind_work(tensors, call):
+    """`call` on a side stream whose queue is busy, with `tensors` holding other values until just before
+    it on that stream: its outputs.  A launch or a copy made on another stream runs at once and reads the
+    other values."""
+    real = [t.clone() for t in tensors]
+    big = torch.randn(4096, 4096, device="cuda")
+    for t in tensors:
+        t.fill_(NAN) if t.dtype.is_floating_point else t.zero_()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(8):                         # some ms; the host is done with all below before that
+            big = big @ big * 1e-3
+        for t, v in zip(tensors, real):
+            t.copy_(v)
+        got = call()
+        assert not side.query()
+    torch.cuda.synchronize()
+    return got
+
+
+def streams_case(hna, name):
+    """(inputs, call) of one entry point; call() returns its outputs."""
+    s = Step(200, 1024, BF, BF, gate=50)
+    if name in ("block_norm", "block_norm_quant"):
+        return [s.x, s.y, s.gamma, s.gamma_post, s.gate], lambda: s.forward(getattr(hna, name))
+    if name == "block_norm_backward":
+        x_out, _, r, r_post = s.forward(hna.block_norm)
+        return ([s.dn, s.dx_out, x_out, r, r_post, s.y, s.gamma, s.gamma_post, s.gate],
+                lambda: tuple(s.backward(hna, x_out, r, r_post).values()))
+    if name == "quant_rows":
+        return [s.x], lambda: hna.quant_rows(s.x)
+    w = [t for k in (1, 2) for t in hna.quant_rows(torch.randn(264, 1024, device="cuda"))]
+    if name == "ffn_inputs":
+        return ([s.x, s.y, s.gamma, *w],
+                lambda: tuple(hna.ffn_inputs(s.x, s.gamma, w[:2], w[2:], y=s.y).values()))
+    q, scale = hna.quant_rows(s.x)
+    if name == "quant_matmul":
+        return [q, scale, *w[:2]], lambda: (hna.quant_matmul(q, scale, *w[:2]),)
+    return [q, scale, *w], lambda: hna.quant_matmul_pair(q, scale, *w)
+
+
+@pytest.mark.parametrize("name", ["block_norm", "block_norm_quant", "block_norm_backward", "quant_rows", "quant_matmul",
+                                  "quant_matmul_pair", "ffn_inputs"])
+def test_calls_run_in_their_streams_order(hna, name):
+    tensors, call = streams_case(hna, name)
+    want = call()
+    torch.cuda.synchronize()
+    got = behind_work(tensors, call)
+    same = [torch.equal(a, b) for a, b in zip(got, want)]
+    assert len(same) == len(want) and all(same), same
