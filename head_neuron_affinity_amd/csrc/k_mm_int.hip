@@ -619,6 +619,13 @@ hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st) {
   // Variants, by the tiles they make of the outputs (T x N, or twice that) on 256 CUs; times in us of both
   // sides of each border.
   auto tiles = [&](int m, int n) { return p.mats * (int64_t)((p.N + m - 1) / m) * ((p.T + n - 1) / n); };
+  // No LDS for up to 4 tokens, whatever the weights: 1 token, weights read from
+  // HBM, against the best tiles: 4096 x 4096 6.1 (7.5 with 32 x 32), 14336 x 4096
+  // 13.9 (15.1 with 64 x 64), 40960 x 4096 32 (39 with 64 x 64, 58 with 256 x 256),
+  // 65536 x 1024 15.7 (22.6, 23.1); behind where 32 x 32 or 64 x 64 make one round and k is long:
+  // 6144 x 14336 21.7 (18.6), 14336 x 14336 42 (37).  At 4 and 5 tokens 4096 x 4096
+  // 6.3 (7.6) and 6.4 (7.7), 14336 x 4096 15.3 (15.2) and 16.6 (15.0).
+  if (p.T <= 4) return launch_few(p, st);
   // 256 x 256 from 160 tiles on.  T x N x K 4096 x 2531 x 1008 (160 tiles): 27
   // against 34 with 128 x 128; 2048 x 4096 x 1024 (128 tiles): 20 against 17.
   // Two steps a tile at least: its scales are in before the tile before it ends.
@@ -632,16 +639,13 @@ hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st) {
     else go(std::false_type{}, std::false_type{});
     return hipGetLastError();
   }
-  // One round of 64 x 64 tiles, whatever T: 14336 x 4096 weights 11.4 for 1 to 64
-  // tokens (13.0 for one with mm_int_few_kernel, 22 for 64 with 32 x 32 tiles).
-  const int64_t t64 = tiles(64, 64);
-  if (t64 >= 192 && t64 <= 256 && p.K > 2048) return launch_t<64, 64, 2, 2, 2, 4>(p, st);
-  // No LDS for up to 4 tokens, or 16 with short k: 4096 x 4096 weights, 1, 4 and
-  // 16 tokens 5.6, 6.4, 8.2 against 6.2, 6.3, 6.4 with 32 x 32 tiles; 4096 x
-  // 1024, 16 tokens 3.3 against 3.8.
-  if (p.T <= (p.K <= 1024 ? 16 : 4)) return launch_few(p, st);
+  // No LDS for up to 16 with short k either: 16 tokens, 4096 x 1024 4.1 against 4.8
+  // with 32 x 32 tiles (14336 x 1024 8.6 against 6.4 with 64 x 64); 4096 x 2048 4.9 against
+  // 6.0, 14336 x 2048 11.4 against 9.1.
+  if (p.T <= 16 && p.K <= 1024) return launch_few(p, st);
   // 32 x 32 with k in four while they are one round: 4096 x 14336 weights, 64
   // tokens (256 tiles) 15 against 23 with 64 x 64, 128 tokens 27 against 24.
+  const int64_t t64 = tiles(64, 64);
   if (tiles(32, 32) <= 256) return launch_t<32, 32, 1, 1, 4, 4>(p, st);
   // 64 x 64 with k in two up to two rounds, four stages for one round of long k:
   // 4096 x 14336, 128 tokens 24 against 35 with two stages, 512 tokens (two

@@ -7,7 +7,7 @@ import torch
 import norm_reference as ref
 import oracle
 import synth
-from test_norm_quant_gpu import BF, F, NAN, Step, hna, wide  # noqa: F401
+from test_norm_quant_gpu import BF, F, NAN, Step, check_product, gen, hna, int_rows, wide  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -235,3 +235,19 @@ def test_calls_run_in_their_streams_order(hna, name):
     got = behind_work(tensors, call)
     same = [torch.equal(a, b) for a, b in zip(got, want)]
     assert len(same) == len(want) and all(same), same
+
+
+# -------------------------------------------------------- few tokens, many channels
+@pytest.mark.parametrize("T,N,K", [(1, 41000, 272), (4, 50003, 130), (2, 65536, 1024), (3, 12800, 4096), (5, 41000, 272)])
+def test_product_of_few_tokens_with_many_channels(hna, T, N, K):
+    print(f"few tokens T={T} N={N} K={K}", flush=True)
+    g = gen(T + N + K)
+    q, s = int_rows(g, T, K)
+    w, ws = int_rows(g, N, K)
+    for dtype in (BF, F):
+        check_product(hna, q, s, w, ws, dtype)
+    w1, s1 = int_rows(g, N // 2, K)
+    for got, (m, c) in zip(hna.quant_matmul_pair(q, s, w[:N // 2], ws[:N // 2].clone(), w1, s1),
+                           ((w[:N // 2], ws[:N // 2].clone()), (w1, s1))):
+        same = torch.equal(got, hna.quant_matmul(q, s, m, c))
+        assert same
