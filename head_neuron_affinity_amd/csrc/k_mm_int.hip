@@ -602,13 +602,15 @@ __global__ __launch_bounds__(64 * W) void mm_int_few_kernel(const IntMmParams p)
   if (t < p.T && n < p.N) put4(p, blockIdx.y, t, n, v, p.q_scale[t]);
 }
 
-// W waves a workgroup: enough for 16 on each CU, with 256 bytes of k each
+// 8 waves a workgroup where there is at most one workgroup a CU and k is long,
+// else 4.  One token, weights read from HBM, us with 4 and 8 (and 16) waves:
+// 4096 x 4096 6.4, 6.1 (6.8), 4096 x 14336 16.8, 14.2 (14.4); 4096 x 2048 4.1,
+// 4.6 (5.1); 5120 x 4096 8.3, 8.3 (10.0), 6144 x 14336 21.7, 23.3 (23.9), 28672 x 4096
+// 22.2, 22.7 (30.5).
 hipError_t launch_few(const IntMmParams& p, hipStream_t st) {
   const dim3 grid((p.N + 15) / 16, p.mats);
-  const int wgs = grid.x * p.mats;
-  if (wgs * 4 >= 4096 || p.K <= 1024) hipLaunchKernelGGL(mm_int_few_kernel<4>, grid, dim3(256), 0, st, p);
-  else if (wgs * 8 >= 4096 || p.K <= 2048) hipLaunchKernelGGL(mm_int_few_kernel<8>, grid, dim3(512), 0, st, p);
-  else hipLaunchKernelGGL(mm_int_few_kernel<16>, grid, dim3(1024), 0, st, p);
+  if ((int64_t)grid.x * p.mats <= 256 && p.K > 2048) hipLaunchKernelGGL(mm_int_few_kernel<8>, grid, dim3(512), 0, st, p);
+  else hipLaunchKernelGGL(mm_int_few_kernel<4>, grid, dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
