@@ -649,11 +649,12 @@ hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st) {
   // tokens (256 tiles) 15 against 23 with 64 x 64, 128 tokens 27 against 24.
   const int64_t t64 = tiles(64, 64);
   if (tiles(32, 32) <= 256) return launch_t<32, 32, 1, 1, 4, 4>(p, st);
-  // 64 x 64 with k in two up to two rounds, four stages for one round of long k:
-  // 4096 x 14336, 128 tokens 24 against 35 with two stages, 512 tokens (two
-  // rounds) 56 against 52; 4096 x 1024, 512 tokens 6.9 against 8.5 with 128 x
-  // 128, 1024 tokens (four rounds) 13.2 against 10.8.
-  if (t64 <= 256 && p.K > 2048) return launch_t<64, 64, 2, 2, 2, 4>(p, st);
+  // 64 x 64 with k in two up to two rounds, four stages for one round of long k: T x N
+  // x K 128 x 4096 x 14336 37 against 50 with two stages; 300 x 2531 (200 tiles) x 2048
+  // 8.7 against 10.5, x 1024 6.1 against 6.2, x 784 6.8 against 6.5, x 272 5.5 against
+  // 5.2; 512 x 4096 x 14336 (two rounds) 56 against 52.  512 x 4096 x 1024 6.9 against
+  // 8.5 with 128 x 128, 1024 tokens (four rounds) 13.2 against 10.8.
+  if (t64 <= 256 && p.K >= 1024) return launch_t<64, 64, 2, 2, 2, 4>(p, st);
   if (t64 <= 512) return launch_t<64, 64, 2, 2, 2, 2>(p, st);
   // 128 x 128, k in two for one round: 4096 x 14336, 1024 tokens (256 tiles) 69
   // to 83 against 79 to 95, 1500 tokens (384 tiles) 138 against 109.

@@ -251,3 +251,14 @@ def test_product_of_few_tokens_with_many_channels(hna, T, N, K):
                            ((w[:N // 2], ws[:N // 2].clone()), (w1, s1))):
         same = torch.equal(got, hna.quant_matmul(q, s, m, c))
         assert same
+
+
+@pytest.mark.parametrize("T,N,K", [(300, 2531, 1008), (300, 2531, 1024), (190, 4096, 1030), (64, 12290, 2048), (20, 14336, 1500)])
+def test_product_of_one_round_of_tiles(hna, T, N, K):
+    """128 to 256 tiles of 64 x 64, k at both sides of the border between its two forms."""
+    print(f"one round T={T} N={N} K={K}", flush=True)
+    g = gen(T + N + K)
+    q, s = int_rows(g, T, K)
+    w, ws = int_rows(g, N, K)
+    for dtype in (BF, F):
+        check_product(hna, q, s, w, ws, dtype)
