@@ -424,9 +424,12 @@ int hna_layout_search(int32_t N, int32_t G, int32_t I, int32_t L, const float* S
  *   res_dtype    type of x, x' and their gradients
  * gamma, gamma_post [hidden], r, r_post [T] and their gradients are fp32, as
  * are all sums.  A row whose mean square and eps are both 0 has r = 0 and
- * normalises to zeros.  A row that holds a NaN or an infinity affects itself
- * only (and the sums over tokens).  Outputs overlap neither each other nor
- * inputs, but for the whole-buffer cases that a call names.
+ * normalises to zeros; one whose sum of squares passes fp32's range (values
+ * from 1.8e19 / sqrt(hidden) on) has r = inf and normalises to zeros, and one
+ * whose squares are subnormal (values under 1e-19) is inexact with an eps of 0.
+ * A row that holds a NaN or an infinity affects itself only (and the sums over
+ * tokens).  Outputs overlap neither each other nor inputs, but for the
+ * whole-buffer cases that a call names.
  */
 typedef struct hna_norm_dims {
   int64_t T;
@@ -447,7 +450,8 @@ int hna_block_norm(const hna_norm_dims* dims, const void* x, const void* y, cons
                    const float* gamma, const float* gamma_post, float res_scale, float block_scale,
                    float eps, void* x_out, void* n, float* r, float* r_post, void* stream);
 
-/* The same with n as 8-bit rows for hna_quant_matmul (see hna_quant_rows):
+/* The same with n as 8-bit rows for hna_quant_matmul (see hna_quant_rows), from
+ * n in fp32, not rounded to dtype before:
  * q int8 [T, hna_quant_pitch(hidden)], q_scale fp32 [T]. */
 int hna_block_norm_quant(const hna_norm_dims* dims, const void* x, const void* y, const void* gate,
                          const float* gamma, const float* gamma_post, float res_scale,

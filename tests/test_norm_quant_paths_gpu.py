@@ -262,3 +262,21 @@ def test_product_of_one_round_of_tiles(hna, T, N, K):
     w, ws = int_rows(g, N, K)
     for dtype in (BF, F):
         check_product(hna, q, s, w, ws, dtype)
+
+
+# ------------------------------------------------------------ rows past fp32's squares
+@pytest.mark.parametrize("C", [520, 4096])
+def test_rows_whose_squares_pass_fp32(hna, C):
+    """Finite values whose sum of squares is none: r = inf and n = 0, as the header says, x' right, the rows
+    beside it as without it."""
+    s = Step(5, C, F, F, post=False)
+    clean = s.forward(hna.block_norm)
+    s.x[2, 7] = 1e25
+    x_out, n, r, _ = s.forward(hna.block_norm)
+    _, q, scale, _, _ = s.forward(hna.block_norm_quant)
+    assert float(r[2]) == float("inf") and not bool(n[2].any()) and not bool(q[2].any()) and float(scale[2]) == 0
+    want = s.rs * float(s.x[2, 7])                 # lies halfway between two fp32 values: either is right
+    assert abs(float(x_out[2, 7]) - want) <= 2.0 ** -24 * want
+    others = [0, 1, 3, 4]
+    same = [torch.equal(a[others], b[others]) for a, b in zip((x_out, n, r), clean)]
+    assert all(same), same
