@@ -688,7 +688,7 @@ def block_norm(x, y=None, gamma=None, *, gamma_post=None, gate=None, gate_tokens
 def block_norm_quant(x, y=None, gamma=None, *, gamma_post=None, gate=None, gate_tokens: Optional[int] = None,
                      res_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6, x_out=None,
                      q=None, q_scale=None, r=None, r_post=None):
-    """block_norm with n as 8-bit rows (see quant_rows): returns (x', q, q_scale, r, r_post)."""
+    """block_norm with n as 8-bit rows (see quant_rows), from n in fp32: returns (x', q, q_scale, r, r_post)."""
     dims, _ = _norm_args(x, y, gamma, gamma_post, gate, gate_tokens, res_scale, None, x_out, r, r_post)
     T, C = x.shape
     pitch = (C + 15) // 16 * 16
@@ -729,7 +729,7 @@ def block_norm_backward(x_out, r, *, dn=None, dx_out=None, gamma=None, y=None, g
     x_out, r and r_post are the forward call's outputs, the rest its arguments.  Returns a dict of
     dx, dy (unless want_dy is False; by default if y is given), dgamma (with gamma and dn),
     dgamma_post (with gamma_post), dgate (with gate and y); None for the others.  dx may be dx_out,
-    dy may be dn or y.
+    dy may be dn or y.  dy has the type of y, dn or gate, of x_out if none is given.
     """
     dt = x_out.dtype
     for t in (y, dn, gate, dy):

@@ -131,7 +131,9 @@ __global__ __launch_bounds__(wg_of(NT)) void block_norm_kernel(const NormParams 
 }
 
 // Rows of x as 8-bit integers.  VEC: rows start on 16 bytes.  Bound by HBM: 65536
-// x 1536 bf16 52 us, 5.8 TB/s; 16384 x 14336 114 us, 6.2 TB/s.
+// x 1536 bf16 51 us, 5.9 TB/s; 16384 x 14336 113 us, 6.2 TB/s.  Otherwise by loads
+// of one element a lane: 16384 x 14331 bf16 456 us, 1.5 TB/s, 4096 x 14331 fp32 63
+// us, 4.7 TB/s.
 template <typename D, int NT, int CH, bool VEC, bool S>
 __global__ __launch_bounds__(wg_of(NT)) void quant_rows_kernel(const D* __restrict__ x, int64_t n_rows,
                                                                int K, int pitch, int8_t* __restrict__ q,
@@ -175,7 +177,8 @@ __global__ __launch_bounds__(wg_of(NT)) void quant_rows_kernel(const D* __restri
   }
 }
 
-// Rows too long for registers (K > 16384): read twice, one workgroup per row.
+// Rows too long for registers (K > 16384): read twice, one workgroup per row, an
+// element a lane: 8192 x 28672 bf16 463 us, 1.5 TB/s.
 template <typename D>
 __global__ __launch_bounds__(1024) void quant_long_rows_kernel(const D* __restrict__ x, int64_t n_rows, int K,
                                                                int pitch, int8_t* __restrict__ q,
@@ -213,7 +216,9 @@ __global__ __launch_bounds__(1024) void quant_long_rows_kernel(const D* __restri
 // Bound by HBM: the next row is loaded before the present one is worked on, as
 // it lies in memory (bf16 stays packed); the gains are read from LDS.  32768 x
 // 4096 bf16 with both norms and gates 0.314 ms, 5.1 TB/s (0.553 without the row
-// ahead and with the gains from L2).
+// ahead and with the gains from L2).  1024 lanes (hidden past 8192) have 128
+// registers each: no row ahead, and with y 81 to 166 of them spill: 8192 x 16384
+// bf16 0.627 ms, 2.6 TB/s (without y 0.250 ms, 5.4 TB/s).
 // Y: y is read (a block norm, or dgate is wanted).
 template <typename R, typename D, int NT, int CH, bool Y, bool S>
 __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backward_kernel(const NormGradParams p) {
@@ -302,7 +307,7 @@ __global__ __launch_bounds__(wg_of(NT), NT <= 512 ? 2 : 4) void block_norm_backw
     auto load_ahead = [&]() __attribute__((always_inline)) {
       if (next < end) load(ahead, next + sub, next + sub < min(next_seg + p.flush_rows, end));
     };
-    if constexpr (NT < 1024) load_ahead();                // 1024 lanes have 128 registers each: no room
+    if constexpr (NT < 1024) load_ahead();                // no room in 1024 lanes
 
     const int64_t row = row0 + sub;
     const bool live = row < seg_end;
