@@ -14,7 +14,8 @@ from ._binding import (HnaError, HNA_BF16, HNA_F32, HNA_ACCUMULATE, hna_dims, hn
                        affinity_loo, static_scratch_bytes, affinity_up_static,
                        mfma_rate_probe, hna_norm_dims, block_norm, block_norm_quant,
                        block_norm_backward, block_norm_workspace_bytes, quant_pitch, quant_rows,
-                       quant_matmul, quant_matmul_pair)
+                       quant_matmul, quant_matmul_pair, hna_ffn_dims, gated_ffn,
+                       gated_ffn_backward, gated_ffn_workspace_bytes)
 from .pipeline import (AffinityPass, StackPass, FfnInputs, pass_for_layer, affinity_layer,
                        ffn_inputs)
 
@@ -29,4 +30,5 @@ __all__ = [
     "affinity_loo", "static_scratch_bytes", "affinity_up_static", "mfma_rate_probe",
     "hna_norm_dims", "block_norm", "block_norm_quant", "block_norm_backward",
     "block_norm_workspace_bytes", "quant_pitch", "quant_rows", "quant_matmul", "quant_matmul_pair", "FfnInputs", "ffn_inputs",
+    "hna_ffn_dims", "gated_ffn", "gated_ffn_backward", "gated_ffn_workspace_bytes",
 ]

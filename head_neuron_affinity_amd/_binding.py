@@ -45,7 +45,8 @@ EXPORTED = [
     "hna_affinity_loo", "hna_static_scratch_bytes", "hna_affinity_up_static",
     "hna_mfma_rate_probe", "hna_block_norm", "hna_block_norm_quant",
     "hna_block_norm_workspace_bytes", "hna_block_norm_backward", "hna_quant_pitch",
-    "hna_quant_rows", "hna_quant_matmul", "hna_quant_matmul_pair",
+    "hna_quant_rows", "hna_quant_matmul", "hna_quant_matmul_pair", "hna_gated_ffn",
+    "hna_gated_ffn_workspace_bytes", "hna_gated_ffn_backward",
 ]
 
 
@@ -63,6 +64,11 @@ class hna_down_dims(ctypes.Structure):
 class hna_norm_dims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("gate_tokens", ctypes.c_int64), ("hidden", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32)]
+
+
+class hna_ffn_dims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("hidden", ctypes.c_int32), ("I", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class HnaError(RuntimeError):
@@ -87,6 +93,7 @@ def lib() -> ctypes.CDLL:
     dp = ctypes.POINTER(hna_dims)
     ddp = ctypes.POINTER(hna_down_dims)
     ndp = ctypes.POINTER(hna_norm_dims)
+    fdp = ctypes.POINTER(hna_ffn_dims)
     ip = ctypes.POINTER(ctypes.c_int32)
     sig = {
         "hna_abi_version": (ctypes.c_int, []),
@@ -124,6 +131,9 @@ def lib() -> ctypes.CDLL:
         "hna_quant_rows": (ctypes.c_int, [i64, i32, i32, vp, vp, vp, vp]),
         "hna_quant_matmul": (ctypes.c_int, [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp]),
         "hna_quant_matmul_pair": (ctypes.c_int, [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "hna_gated_ffn": (ctypes.c_int, [fdp, vp, vp, vp, vp, vp, vp, vp]),
+        "hna_gated_ffn_workspace_bytes": (sz, [fdp]),
+        "hna_gated_ffn_backward": (ctypes.c_int, [fdp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "hna_mfma_rate_probe": (ctypes.c_int, [i32, i32, i32, vp, vp, vp]),
         "hna_layout_search": (ctypes.c_int, [i32, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp,
                                               ctypes.POINTER(ctypes.c_double), ip, vp, sz, vp]),
@@ -876,3 +886,88 @@ def quant_matmul_pair(q, q_scale, w0, w0_scale, w1, w1_scale, out0=None, out1=No
     _check(lib().hna_quant_matmul_pair(T, N, K, code, _at(q), _at(q_scale), _at(w0), _at(w0_scale), _at(w1),
                                        _at(w1_scale), _at(out0), _at(out1), _raw_stream(index)), "hna_quant_matmul_pair")
     return out0, out1
+
+
+# ------------------------------------------------------------------ gated FFN
+def _ffn_dims(n_shape, w_gate, w_up, dtype) -> hna_ffn_dims:
+    """dims of a gated FFN over n [T, hidden] with weights [I, hidden] of one type."""
+    T, hidden = n_shape
+    if w_gate.dim() != 2:
+        raise ValueError(f"w_gate: shape {tuple(w_gate.shape)}, expected [I, hidden]")
+    I = w_gate.shape[0]
+    _is(w_gate, "w_gate", (I, hidden), dtype)
+    _is(w_up, "w_up", (I, hidden), dtype)
+    return hna_ffn_dims(T, hidden, I, _code(dtype))
+
+
+def gated_ffn(n, w_gate, w_up, *, want_gu: bool = True, want_h: bool = True, g=None, u=None, h=None):
+    """g = n w_gate^T, u = n w_up^T and h = silu(g) u (hna_gated_ffn), n [T, hidden], weights [I, hidden].
+
+    Returns (g, u, h), each [T, I]; g and u are None without want_gu (serving needs h alone), h without
+    want_h (an affinity pass needs g and u alone).  An output tensor that is given is written whatever
+    is wanted."""
+    if n.dim() != 2:
+        raise ValueError(f"n: shape {tuple(n.shape)}, expected [T, hidden]")
+    dt = n.dtype
+    dims = _ffn_dims(n.shape, w_gate, w_up, dt)
+    shape = (dims.T, dims.I)
+    _is(g, "g", shape, dt)
+    _is(u, "u", shape, dt)
+    _is(h, "h", shape, dt)
+    index = _index_of(n, w_gate, w_up, g, u, h)
+    if index != _current():
+        with torch.cuda.device(index):
+            return gated_ffn(n, w_gate, w_up, want_gu=want_gu, want_h=want_h, g=g, u=u, h=h)
+    if want_gu:
+        if g is None:
+            g = torch.empty(shape, dtype=dt, device=n.device)
+        if u is None:
+            u = torch.empty(shape, dtype=dt, device=n.device)
+    if want_h and h is None:
+        h = torch.empty(shape, dtype=dt, device=n.device)
+    _check(lib().hna_gated_ffn(ctypes.byref(dims), _at(n), _at(w_gate), _at(w_up), _at(g), _at(u), _at(h),
+                               _raw_stream(index)), "hna_gated_ffn")
+    return g, u, h
+
+
+def gated_ffn_workspace_bytes(dims: hna_ffn_dims) -> int:
+    return int(lib().hna_gated_ffn_workspace_bytes(ctypes.byref(dims)))
+
+
+def gated_ffn_backward(dh, n, w_gate, w_up, g, u, *, want_dn: bool = True, want_dw: bool = True, dn=None,
+                       dw_gate=None, dw_up=None, workspace=None):
+    """Gradients of gated_ffn (hna_gated_ffn_backward) from dh, the gradient of h, at the g and u it wrote.
+
+    Returns (dn [T, hidden], dw_gate, dw_up [I, hidden]), None for those not wanted."""
+    if n.dim() != 2:
+        raise ValueError(f"n: shape {tuple(n.shape)}, expected [T, hidden]")
+    dt = n.dtype
+    dims = _ffn_dims(n.shape, w_gate, w_up, dt)
+    shape = (dims.T, dims.I)
+    _is(dh, "dh", shape, dt)
+    _is(g, "g", shape, dt)
+    _is(u, "u", shape, dt)
+    _is(dn, "dn", n.shape, dt)
+    _is(dw_gate, "dw_gate", w_gate.shape, dt)
+    _is(dw_up, "dw_up", w_gate.shape, dt)
+    index = _index_of(dh, n, w_gate, w_up, g, u, dn, dw_gate, dw_up, workspace)
+    if index != _current():
+        with torch.cuda.device(index):
+            return gated_ffn_backward(dh, n, w_gate, w_up, g, u, want_dn=want_dn, want_dw=want_dw, dn=dn,
+                                      dw_gate=dw_gate, dw_up=dw_up, workspace=workspace)
+    if dn is None and want_dn:
+        dn = torch.empty_like(n)
+    if want_dw or dw_gate is not None or dw_up is not None:
+        if dw_gate is None:
+            dw_gate = torch.empty_like(w_gate)
+        if dw_up is None:
+            dw_up = torch.empty_like(w_up)
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(L.hna_gated_ffn_workspace_bytes(ctypes.byref(dims)) or 16, dtype=torch.uint8,
+                                device=n.device)
+    _check(L.hna_gated_ffn_backward(ctypes.byref(dims), _at(dh), _at(n), _at(w_gate), _at(w_up), _at(g), _at(u),
+                                    _at(dn), _at(dw_gate), _at(dw_up), _at(workspace),
+                                    workspace.numel() * workspace.element_size(), _raw_stream(index)),
+           "hna_gated_ffn_backward")
+    return dn, dw_gate, dw_up

@@ -243,6 +243,43 @@ int check_quant_matmul(const char* fn, int64_t T, int32_t N, int32_t K, int32_t 
   return HNA_OK;
 }
 
+// ---- gated FFN ----
+constexpr int32_t kMaxFfnHidden = 65536;
+constexpr int32_t kMaxFfnI = 1 << 20;                 // a tile's rows lie within 31 bits
+constexpr int64_t kMaxFfnOut = (int64_t)1 << 34;      // elements of g: 2^32 threads of 8 at most
+constexpr int64_t kMaxFfnIn = (int64_t)1 << 36;
+
+int check_ffn_dims(const char* fn, const hna_ffn_dims* dm) {
+  if (!dm) return fail(HNA_ERR_INVALID_ARG, "%s: dims is NULL", fn);
+  const int rc = check_dtype(fn, dm->dtype);
+  if (rc) return rc;
+  if (dm->T < 0 || dm->hidden < 1 || dm->I < 1)
+    return fail(HNA_ERR_INVALID_ARG, "%s: T=%lld, hidden=%d, I=%d", fn, (long long)dm->T, dm->hidden, dm->I);
+  if (dm->hidden % 8 != 0 || dm->hidden > kMaxFfnHidden)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: hidden=%d must be a multiple of 8 and <= %d", fn, dm->hidden, kMaxFfnHidden);
+  if (dm->I > kMaxFfnI) return fail(HNA_ERR_UNSUPPORTED, "%s: I=%d > 2^20", fn, dm->I);
+  if (dm->T > (int64_t)INT32_MAX || dm->T * dm->I > kMaxFfnOut || dm->T * dm->hidden > kMaxFfnIn)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: T=%lld with I=%d and hidden=%d: T < 2^31, T I <= 2^34 and T hidden <= 2^36", fn,
+                (long long)dm->T, dm->I, dm->hidden);
+  return HNA_OK;
+}
+
+struct FfnWorkspace {
+  size_t dg, du, part, total;
+  int I8, splits;
+};
+FfnWorkspace ffn_workspace(const hna_ffn_dims* dm) {
+  FfnWorkspace w{};
+  w.I8 = round_up(dm->I, 8);
+  const size_t plane = align256((size_t)dm->T * w.I8 * esize_of(dm->dtype));
+  w.splits = ffn_dn_splits(dm->T, dm->hidden, dm->I);
+  w.dg = 0;
+  w.du = plane;
+  w.part = 2 * plane;
+  w.total = w.part + (w.splits > 1 ? align256((size_t)w.splits * dm->T * dm->hidden * sizeof(float)) : 0);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1295,6 +1332,99 @@ int hna_quant_matmul_pair(int64_t T, int32_t N, int32_t K, int32_t out_dtype, co
   const IntMmParams p{q, q_scale, {w0, w1}, {w0_scale, w1_scale}, {out0, out1}, T, N, K, out_dtype == HNA_BF16, 2};
   hipStream_t st = static_cast<hipStream_t>(stream);
   return finish(launch_mm_int(p, st), st, fn);
+}
+
+// ---- gated FFN ----
+int hna_gated_ffn(const hna_ffn_dims* dm, const void* n, const void* W_gate, const void* W_up, void* g,
+                  void* u, void* h, void* stream) {
+  const char* fn = "hna_gated_ffn";
+  const int rc = check_ffn_dims(fn, dm);
+  if (rc) return rc;
+  if (dm->T > 0) {
+    if (!g && !u && !h) return fail(HNA_ERR_INVALID_ARG, "%s: no output is wanted", fn);
+    REQUIRE_PTR(n);
+    REQUIRE_PTR(W_gate);
+    REQUIRE_PTR(W_up);
+    OPTIONAL_PTR(g);
+    OPTIONAL_PTR(u);
+    OPTIONAL_PTR(h);
+  }
+  FfnMmParams p{};
+  p.a[0] = W_gate;
+  p.a[1] = W_up;
+  p.b[0] = p.b[1] = n;
+  p.out[0] = g;
+  p.out[1] = u;
+  p.out[2] = h;
+  p.lda = p.ldb = p.K = dm->hidden;
+  p.N = dm->T;
+  p.M = dm->I;
+  p.splits = 1;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_ffn_mm(p, kFfnGate, dm->dtype == HNA_BF16, st), st, fn);
+}
+
+size_t hna_gated_ffn_workspace_bytes(const hna_ffn_dims* dm) {
+  if (check_ffn_dims("hna_gated_ffn_workspace_bytes", dm)) return 0;
+  return std::max(ffn_workspace(dm).total, size_t(256));
+}
+
+int hna_gated_ffn_backward(const hna_ffn_dims* dm, const void* dh, const void* n, const void* W_gate,
+                           const void* W_up, const void* g, const void* u, void* dn, void* dW_gate,
+                           void* dW_up, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "hna_gated_ffn_backward";
+  const int rc = check_ffn_dims(fn, dm);
+  if (rc) return rc;
+  if (!dn && !dW_gate && !dW_up && dm->T > 0) return fail(HNA_ERR_INVALID_ARG, "%s: no gradient is wanted", fn);
+  if (!dW_gate != !dW_up) return fail(HNA_ERR_INVALID_ARG, "%s: dW_gate and dW_up are wanted together", fn);
+  OPTIONAL_PTR(dW_gate);
+  OPTIONAL_PTR(dW_up);
+  if (dm->T > 0) {      // without tokens only the sums over them are there to be written
+    REQUIRE_PTR(dh);
+    REQUIRE_PTR(g);
+    REQUIRE_PTR(u);
+    OPTIONAL_PTR(dn);
+    if (dW_gate) REQUIRE_PTR(n);
+    if (dn) {
+      REQUIRE_PTR(W_gate);
+      REQUIRE_PTR(W_up);
+    }
+  }
+  REQUIRE_PTR(workspace);
+  const FfnWorkspace w = ffn_workspace(dm);
+  if (workspace_bytes < w.total)
+    return fail(HNA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, w.total);
+  char* ws = static_cast<char*>(workspace);
+  const int bf16 = dm->dtype == HNA_BF16;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t e = launch_ffn_grad(dh, g, u, dm->T, dm->I, w.I8, ws + w.dg, ws + w.du, bf16, st);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  FfnMmParams p{};
+  p.b[0] = ws + w.dg;
+  p.b[1] = ws + w.du;
+  p.ldb = w.I8;
+  p.lda = p.M = dm->hidden;
+  if (dn) {
+    p.a[0] = W_gate;
+    p.a[1] = W_up;
+    p.out[0] = dn;
+    p.N = dm->T;
+    p.K = dm->I;
+    p.splits = w.splits;
+    p.part = w.splits > 1 ? reinterpret_cast<float*>(ws + w.part) : nullptr;
+    if ((e = launch_ffn_mm(p, kFfnDn, bf16, st)) != hipSuccess) return hip_fail(e, fn);
+  }
+  if (dW_gate) {
+    p.a[0] = p.a[1] = n;
+    p.out[0] = dW_gate;
+    p.out[1] = dW_up;
+    p.N = dm->I;
+    p.K = dm->T;
+    p.splits = 1;
+    p.part = nullptr;
+    if ((e = launch_ffn_mm(p, kFfnDw, bf16, st)) != hipSuccess) return hip_fail(e, fn);
+  }
+  return finish(hipSuccess, st, fn);
 }
 
 }  // extern "C"

@@ -338,4 +338,25 @@ struct IntMmParams {
 };
 hipError_t launch_mm_int(const IntMmParams& p, hipStream_t st);
 
+// ------------------------------------------------ gated FFN (k_ffn.hip)
+// out[c][r] = sum_k A(r, k) B(c, k), M rows r (out's contiguous direction) and N columns c:
+//   gate  a = W_gate, W_up [M][K]; b[0] = n [N][K]; out = g, u, h = silu(g) u [N][M], each or NULL
+//   dn    a = W_gate, W_up [K][M]; b = dg, du [N][ldb]; out[0] = dn [N][M], the sum of both products
+//   dw    a[0] = n [K][M]; b = dg, du [K][ldb]; out = dW_gate, dW_up [N][M]
+// lda, ldb: elements from row to row, multiples of 8
+enum FfnMode { kFfnGate = 0, kFfnDn = 1, kFfnDw = 2 };
+struct FfnMmParams {
+  const void* a[2];
+  const void* b[2];
+  void* out[3];
+  float* part;         // dn with splits > 1: [splits][N][M]
+  int64_t lda, ldb, N, K;
+  int M, splits;
+};
+int ffn_dn_splits(int64_t T, int C, int I);
+hipError_t launch_ffn_mm(const FfnMmParams& p, int mode, int bf16, hipStream_t st);
+// dg = dh u silu'(g), du = dh silu(g) [rows][I8], zeros behind I
+hipError_t launch_ffn_grad(const void* dh, const void* g, const void* u, int64_t rows, int I, int I8, void* dg, void* du, int bf16,
+                           hipStream_t st);
+
 }  // namespace hna

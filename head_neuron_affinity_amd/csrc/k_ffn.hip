@@ -1,0 +1,712 @@
+// The gated FFN's products and their gradients:
+//   forward   g = n W_gate^T, u = n W_up^T, h = silu(g) u       (kGate)
+//   gradients dn = dg W_gate + du W_up                          (kDn)
+//             dW_gate = dg^T n, dW_up = du^T n                  (kDw)
+//             with dg = dh u silu'(g), du = dh silu(g)
+// as one product of rows and columns, out[c][r] = sum_k A(r, k) B(c, k), whose
+// operands lie either way in memory: rows of k, or (k-major) rows along the
+// other dimension.  The rows are the MFMA rows, so that a lane ends up with 4
+// consecutive elements of out's contiguous direction:
+//            rows r             columns c   A             B
+//   kGate    gate, up channels  tokens      W, rows of k  n, rows of k
+//   kDn      hidden             tokens      W, k-major    dg then du, rows of k
+//   kDw      hidden             channels    n, k-major    dg or du, k-major
+// bf16 operands multiply on 32x32x16 MFMAs, fp32 ones on 32x32x2; sums are fp32
+// and are rounded once, on output.  dg and du are rounded to the operands' type
+// before their products (bf16: half a step of 2^-8, below what the sum over
+// channels or tokens of rounded operands carries anyway), which lets their
+// products run at the matrix cores' rate.
+#include <algorithm>
+
+#include "hna_internal.h"
+#include "hna_hot.h"
+#include "hna_mma.h"
+
+namespace hna {
+namespace {
+
+using namespace hot;
+using namespace mm;
+
+template <int MODE> constexpr bool kMajorA = MODE != kFfnGate;
+template <int MODE> constexpr bool kMajorB = MODE == kFfnDw;
+
+// ------------------------------------------------------------------ large products
+// 256 x 256 tiles on 4 waves, one per SIMD, each 128 x 128 (16 accumulators of
+// 32 x 32).  128 bytes of k a step in two stages; a step is four quarters, and
+// the fragments of the next quarter are read while the MFMAs of this one run:
+//   quarters 0 .. 2 of step s, reading quarters 1 .. 3
+//   wait for the reads and for step s + 1's copies; barrier
+//   quarter 3, reading quarter 0 of step s + 1 and copying step s + 2 over step s
+// The barrier says that every wave holds step s in registers (its stage is
+// free) and that every wave's part of step s + 1 is in LDS.  One workgroup a CU
+// walks over its tiles, and the steps of all of them are one stream, so that the
+// copies never drain and stores overlap the next tile's MFMAs.
+// A gate tile's 256 rows are 128 channels of both matrices, 64 + 64 a wave, so
+// that a wave holds g and u of the same channels and tokens.
+struct FfnTiles {
+  int ntm, ntn1, ntn, gsize, ntiles, last, slots;
+};
+
+template <typename T, int MODE>
+struct FfnPanels {
+  static constexpr int E = sizeof(T), BK = 128 / E, RM = MODE == kFfnGate ? 128 : 256;
+  int m0, ti, z;            // first row (channel), column tile, matrix
+  int seg, ks;              // the copies' segment of k and step in it
+  u32x4 a0, a1, b;          // operands from the step's first element on
+  int kbytes;               // bytes of k left from there (rows of k)
+
+  __device__ inline void tile(const FfnMmParams& p, const FfnTiles& g, int t) {
+    const int grp = t / g.gsize, tg = t - grp * g.gsize;
+    const int gm = max(min(4, g.ntm - grp * 4), 1);
+    const int c = tg / gm;
+    m0 = (grp * 4 + tg - c * gm) * RM;
+    z = MODE == kFfnDw && c >= g.ntn1 ? 1 : 0;
+    ti = c - z * g.ntn1;
+    seg = ks = 0;
+    if (t < g.ntiles) {
+      step(p);
+    } else {                // no tile: the copies read zeros
+      a0 = a1 = b = uniform_rsrc(p.b[0], 0);
+      kbytes = 0;
+    }
+  }
+  __device__ inline static uint32_t span(int64_t bytes) {
+    return bytes <= 0 ? 0u : bytes > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)bytes;
+  }
+  __device__ inline void step(const FfnMmParams& p) {
+    const int64_t k0 = (int64_t)ks * BK, kb = k0 * E;
+    kbytes = (int)min<int64_t>(p.K * E - kb, 1 << 20);
+    if constexpr (kMajorA<MODE>) {
+      const char* x = static_cast<const char*>(seg ? p.a[1] : p.a[0]) + (k0 * p.lda + m0) * E;
+      a0 = a1 = uniform_rsrc(x, span(((p.K - k0) * p.lda - m0) * E));
+    } else {
+      const int64_t o = (int64_t)m0 * p.lda * E + kb, left = span((int64_t)(p.M - m0) * p.lda * E - kb);
+      a0 = uniform_rsrc(static_cast<const char*>(p.a[0]) + o, left);
+      a1 = uniform_rsrc(static_cast<const char*>(p.a[1]) + o, left);
+    }
+    const int64_t c0 = (int64_t)ti * 256;
+    if constexpr (kMajorB<MODE>) {
+      const char* x = static_cast<const char*>(z ? p.b[1] : p.b[0]) + (k0 * p.ldb + c0) * E;
+      b = uniform_rsrc(x, span(((p.K - k0) * p.ldb - c0) * E));
+    } else {
+      const char* x = static_cast<const char*>(seg ? p.b[1] : p.b[0]) + c0 * p.ldb * E + kb;
+      b = uniform_rsrc(x, span((p.N - c0) * p.ldb * E - kb));
+    }
+  }
+};
+
+// The lane number, computed anew: values made from it are not kept in registers
+// over the loops
+__device__ inline int lane_id() {
+  int v;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(v));
+  return v;
+}
+
+// WIDE: out's rows start on 16 bytes
+template <typename T, int MODE, bool WIDE>
+__global__ __launch_bounds__(256, 1) void ffn_big_kernel(const FfnMmParams p) {
+  constexpr int BM = 256, STAGE = 2 * BM * 128, E = sizeof(T), BK = 128 / E;
+  constexpr int SEGS = MODE == kFfnDn ? 2 : 1;
+  constexpr int PITCH = 128 + 16;                       // a staged column: 128 bytes of outputs
+  constexpr int KP = BM * E;                            // pitch of a k-major tile
+  __shared__ __attribute__((aligned(16))) unsigned char lds[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) unsigned char stage_out[4 * 32 * PITCH];
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = w >> 1, wn = w & 1;
+
+  typedef FfnPanels<T, MODE> Panels;
+  FfnTiles g;
+  g.ntm = (p.M + Panels::RM - 1) / Panels::RM;
+  g.ntn1 = (int)((p.N + 255) / 256);
+  g.ntn = (MODE == kFfnDw ? 2 : 1) * g.ntn1;
+  g.ntiles = g.ntm * g.ntn;
+  g.gsize = 4 * g.ntn;
+  g.slots = gridDim.x >> 3;
+  // tiles of an XCD (workgroup ids go round the XCDs) are consecutive; its workgroups take them in turn
+  const int per_xcd = (g.ntiles + 7) / 8, first = (int)(blockIdx.x & 7) * per_xcd;
+  g.last = min(first + per_xcd, g.ntiles);
+  int tile = first + (int)(blockIdx.x >> 3);
+  if (tile >= g.last) return;
+  auto after = [&](int t) __attribute__((always_inline)) {
+    return t + g.slots < g.last ? t + g.slots : g.ntiles;   // ntiles: no tile, its copies read zeros
+  };
+  const int nks = (int)((p.K + BK - 1) / BK), nk = SEGS * nks;
+
+  // copy c of 16 of a step, 1 KB a wave of A (c even) or B (c odd), i = c / 2:
+  // rows of k: rows 32 i + 8 w + l / 8, chunk x of row r in slot x ^ swz(r);
+  // k-major: rows of k (1024 / KP) (4 i + w) .. , chunk x of row k in slot x ^ ksw(k)
+  const int rc = 8 * w + (l >> 3);
+  const int kc = 16 * ((l & 7) ^ swz<8>(rc));
+  constexpr int KR = 1024 / KP;                             // rows of k a copy
+  const int kr = KR * w + l / (KP / 16);
+  const uint32_t kx = 16u * (uint32_t)((l % (KP / 16)) ^ ksw<T, KP>(kr));
+  static_assert(4 * KR % 4 == 0, "the copies of a lane share their XOR");
+  const uint32_t va = kMajorA<MODE> ? (uint32_t)((int64_t)kr * p.lda * E) + kx : (uint32_t)((int64_t)rc * p.lda * E) + kc;
+  const uint32_t vb = kMajorB<MODE> ? (uint32_t)((int64_t)kr * p.ldb * E) + kx : (uint32_t)((int64_t)rc * p.ldb * E) + kc;
+  const uint32_t sa = (uint32_t)((kMajorA<MODE> ? 4 * KR : 32) * p.lda * E), sb = (uint32_t)((kMajorB<MODE> ? 4 * KR : 32) * p.ldb * E);
+  const uint32_t lds0 = lds_addr(lds) + (uint32_t)w * 1024u;
+  Panels cp;
+  int cp_tile = tile;
+  cp.tile(p, g, cp_tile);
+  auto issue = [&](int buf, int c) __attribute__((always_inline)) {
+    const int i = c >> 1;
+    const uint32_t to = lds0 + (uint32_t)(buf * STAGE + (c & 1) * BM * 128 + i * 4096);
+    if (c & 1) {
+      const uint32_t v = vb + (uint32_t)i * sb;
+      dma16s(cp.b, kMajorB<MODE> || kc < cp.kbytes ? v : kOutOfRange, 0u, to);
+    } else if (kMajorA<MODE>) {
+      dma16s(cp.a0, va + (uint32_t)i * sa, 0u, to);
+    } else {
+      // channels 32 (i % 2) + 64 (i / 4) of gate (i / 2 even) or up
+      const uint32_t v = va + (uint32_t)((i & 1) + 2 * (i >> 2)) * sa;
+      dma16s((i >> 1) & 1 ? cp.a1 : cp.a0, kc < cp.kbytes ? v : kOutOfRange, 0u, to);
+    }
+  };
+  auto next_copy = [&]() __attribute__((always_inline)) {
+    if (++cp.ks == nks) {
+      cp.ks = 0;
+      if (SEGS == 1 || cp.seg == 1) {
+        cp_tile = after(cp_tile);
+        cp.tile(p, g, cp_tile);
+        return;
+      }
+      cp.seg = 1;
+    }
+    if (cp_tile < g.ntiles) cp.step(p);
+  };
+
+  f32x16 acc[4][4];
+  uint4 fa[2][4], fb[2][4];
+  const int sl = swz<8>(l & 31), up = l >> 5;
+  const int ra = (wm * 128 + (l & 31)) * 128, rb = (BM + wn * 128 + (l & 31)) * 128;
+  const int ka = klane<T, KP>(l);
+  // fragment f of 8 (4 of the rows, 4 of the columns) of quarter h of a stage
+  auto rd = [&](int buf, auto h, int f) __attribute__((always_inline)) {
+    const unsigned char* st = lds + buf * STAGE;
+    if (f < 4) {
+      if constexpr (kMajorA<MODE>) fa[h & 1][f] = kfrag<T, KP>(st + wm * 128 * E, ka, f, h);
+      else fa[h & 1][f] = *reinterpret_cast<const uint4*>(st + (((2 * h + up) ^ sl) << 4) + ra + f * 32 * 128);
+    } else {
+      if constexpr (kMajorB<MODE>) fb[h & 1][f - 4] = kfrag<T, KP>(st + BM * 128 + wn * 128 * E, ka, f - 4, h);
+      else fb[h & 1][f - 4] = *reinterpret_cast<const uint4*>(st + (((2 * h + up) ^ sl) << 4) + rb + (f - 4) * 32 * 128);
+    }
+  };
+  // the 16 products of quarter h, behind(i) right behind the i-th
+  auto mm = [&](auto quarter, auto behind) __attribute__((always_inline)) {
+    constexpr int h = decltype(quarter)::value & 1;
+    static_for<0, 16>([&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      mma16<T>(acc[i / 4][i % 4], fa[h][i / 4], fb[h][i % 4]);
+      behind(ic);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  constexpr std::integral_constant<int, 0> Q0{};
+  constexpr std::integral_constant<int, 1> Q1{};
+  constexpr std::integral_constant<int, 2> Q2{};
+  constexpr std::integral_constant<int, 3> Q3{};
+
+#pragma unroll
+  for (int c = 0; c < 16; ++c) issue(0, c);
+  next_copy();
+#pragma unroll
+  for (int c = 0; c < 16; ++c) issue(1, c);
+  next_copy();
+  __builtin_amdgcn_s_waitcnt(vm_wait(16));                  // the first step is in
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+
+  const int outs = MODE == kFfnGate ? (p.out[0] != nullptr) + (p.out[1] != nullptr) + (p.out[2] != nullptr) : 1;
+  constexpr int STORES = 16 * (MODE == kFfnGate ? 1 : 2) * E / 2;   // of an output of a tile, per thread
+  int buf = 0;
+  bool stored = false;                                      // the previous tile's stores may be in flight
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+#pragma unroll
+    for (int f = 0; f < 8; ++f) rd(buf, Q0, f);             // not kept over the epilogue
+    for (int kt = 0; kt < nk; ++kt) {
+      mm(Q0, [&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < 8) rd(buf, Q1, i);
+      });
+      mm(Q1, [&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < 8) rd(buf, Q2, i);
+      });
+      mm(Q2, [&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < 8) rd(buf, Q3, i);
+      });
+      // step s + 1's copies are older than the stores of the tile before
+      if (kt == 0 && stored) {
+        if (outs == 3) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(3 * STORES > 63 ? 63 : 3 * STORES) : "memory");
+        else if (outs == 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * STORES > 63 ? 63 : 2 * STORES) : "memory");
+        else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(STORES > 63 ? 63 : STORES) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      }
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      mm(Q3, [&](auto i) __attribute__((always_inline)) {
+        if constexpr (i < 8) rd(buf ^ 1, Q0, i);
+        issue(buf, i);
+      });
+      next_copy();
+      buf ^= 1;
+    }
+
+    // lane l holds column (l & 31) and rows 8 a + 4 (l / 32) + e of each 32 x 32
+    // tile: rounded and staged through LDS, 32 columns x 128 bytes at a time, so
+    // that out is written in whole lines
+    const int le = lane_id();
+    Panels here;
+    {
+      const int grp = tile / g.gsize, tg = tile - grp * g.gsize;
+      const int gm = max(min(4, g.ntm - grp * 4), 1), c = tg / gm;
+      here.m0 = (grp * 4 + tg - c * gm) * Panels::RM;
+      here.z = MODE == kFfnDw && c >= g.ntn1 ? 1 : 0;
+      here.ti = c - here.z * g.ntn1;
+    }
+    const int64_t t0 = (int64_t)here.ti * 256 + wn * 128;
+    constexpr int WR = MODE == kFfnGate ? 64 : 128;         // rows of out a wave holds
+    const int n0 = here.m0 + wm * WR;
+    unsigned char* stg = stage_out + w * 32 * PITCH;
+    constexpr int CH = 4 / E, TI = WR / 32;                 // 32-row tiles per 128 bytes, and of a wave
+    typedef typename Four<T>::type F4;
+    static_for<0, 4 * (TI / CH)>([&](auto sc) __attribute__((always_inline)) {
+      constexpr int s = decltype(sc)::value, j = s / (TI / CH), i0 = s % (TI / CH) * CH;
+      static_for<0, MODE == kFfnGate ? 3 : 1>([&](auto oc) __attribute__((always_inline)) {
+        constexpr int o = decltype(oc)::value;
+        void* out = MODE == kFfnDw && here.z ? p.out[1] : p.out[o];
+        if (MODE == kFfnGate && !out) return;
+        // the sums stay in accumulation registers until here
+#pragma unroll
+        for (int i = i0; i < i0 + CH; ++i) {
+          asm volatile("" : "+a"(acc[i][j]));
+          if constexpr (MODE == kFfnGate) asm volatile("" : "+a"(acc[i + 2][j]));
+        }
+#pragma unroll
+        for (int i = i0; i < i0 + CH; ++i)
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (MODE == kFfnGate && o == 1) f[e] = acc[i + 2][j][4 * a + e];
+              else if constexpr (MODE == kFfnGate && o == 2) f[e] = acc[i][j][4 * a + e] * sigmoid(acc[i][j][4 * a + e]) * acc[i + 2][j][4 * a + e];
+              else f[e] = acc[i][j][4 * a + e];
+            }
+            *reinterpret_cast<F4*>(stg + (le & 31) * PITCH + (32 * (i - i0) + 8 * a + 4 * (le >> 5)) * E) = Four<T>::of(f[0], f[1], f[2], f[3]);
+          }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        const int64_t tj = t0 + j * 32;
+        const int64_t rows = min<int64_t>(32, p.N - tj), ob = rows > 0 ? rows * p.M * E : 0;
+        const __amdgpu_buffer_rsrc_t ro = buffer_rsrc(static_cast<unsigned char*>(out) + (rows > 0 ? tj * p.M * E : 0), (uint32_t)ob);
+        const int nb = n0 + i0 * 32;                        // the first of 128 / E rows
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = k * 8 + (le >> 3), n = nb + (le & 7) * (16 / E);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(stg + row * PITCH + (le & 7) * 16);
+            const uint32_t off = n < p.M ? (uint32_t)(row * p.M + n) * E : 0xfffffff0u;
+            __builtin_amdgcn_raw_buffer_store_b128(v, ro, (int)off, 0, 2);   // non-temporal: the panels stay in L2
+          }
+        } else if constexpr (E == 4) {
+          for (int k = 0; k < 16; ++k) {
+            const int row = k * 2 + (le >> 5), n = nb + (le & 31);
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(stg + row * PITCH + (le & 31) * 4);
+            const uint32_t off = n < p.M ? (uint32_t)(row * p.M + n) * 4u : 0xfffffff0u;
+            __builtin_amdgcn_raw_buffer_store_b32(v, ro, (int)off, 0, 0);
+          }
+        } else {
+          // rows that start on any element: pairs that lie on 4 bytes, and the
+          // elements left at both ends
+          const int m = min(64, p.M - nb);
+          for (int k = 0; k < 16; ++k) {
+            const int row = k * 2 + (le >> 5), odd = (int)((tj + row) & p.M & 1), c = 2 * (le & 31) + odd;
+            const uint16_t* x = reinterpret_cast<const uint16_t*>(stg + row * PITCH) + c;
+            const uint32_t v = (uint32_t)x[0] | ((uint32_t)x[1] << 16);
+            const uint32_t off = c + 1 < m ? (uint32_t)(row * p.M + nb + c) * 2u : 0xfffffff0u;
+            __builtin_amdgcn_raw_buffer_store_b32(v, ro, (int)off, 0, 0);
+          }
+          const int row = le & 31, odd = (int)((tj + row) & p.M & 1), c = le < 32 ? 0 : m - 1;
+          if (m > 0) {
+            const uint16_t v = reinterpret_cast<const uint16_t*>(stg + row * PITCH)[c];
+            const bool on = le < 32 ? odd : (m - odd) & 1;
+            __builtin_amdgcn_raw_buffer_store_b16(v, ro, on ? (int)((uint32_t)(row * p.M + nb + c) * 2u) : (int)0xfffffff0u, 0, 0);
+          }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    if constexpr (WIDE) stored = true;
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // a varying number of stores
+    tile = after(tile);
+    if (tile >= g.ntiles) break;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// ------------------------------------------------------------------ smaller products
+// Tiles of BM x BN: KG groups of WGM x WGN waves, each group with a part of k of
+// its own (128 bytes of a step of KG 128), the steps in a ring of NST stages.
+// Several groups shorten the chain of steps where there are few tiles.  The
+// groups' sums meet in LDS.  Where even that leaves CUs idle, k is split among
+// p.splits workgroups too (kDn), whose fp32 sums a second kernel adds in order.
+// A gate tile has BM / 2 channels of both matrices, in blocks of 32 by turns.
+template <typename T, int MODE, int BM, int BN, int WGM, int WGN, int KG, int NST>
+__global__ __launch_bounds__(64 * WGM * WGN * KG) void ffn_tile_kernel(const FfnMmParams p) {
+  constexpr int NW = WGM * WGN, NT = 64 * NW * KG, E = sizeof(T), BK = 128 / E;
+  constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
+  constexpr int ROWS = BM + BN, PART = ROWS * 128, STAGE = KG * PART;
+  constexpr int NCP = ROWS / (8 * NW), NCX = BM / (8 * NW);
+  constexpr int PITCH = BM + 4;                          // floats of a column of sums
+  constexpr int KPA = BM * E, KPB = BN * E;
+  constexpr int SEGS = MODE == kFfnDn ? 2 : 1;
+  constexpr bool GATE = MODE == kFfnGate;
+  constexpr int RM = GATE ? BM / 2 : BM;
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "copy rounds cover whole rows");
+  static_assert(!GATE || BM % 64 == 0, "blocks of 32 channels by turns");
+  static_assert((NST - 2) * NCP <= 63, "copies in flight must fit the wait counter");
+  constexpr int SUMS = BN * PITCH * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[NST * STAGE > SUMS ? NST * STAGE : SUMS];
+
+  const int tid = threadIdx.x, l = tid & 63;
+  const int wg = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wg / NW, w = wg % NW;
+  const int wm = w / WGN, wn = w % WGN;
+  const int z = MODE == kFfnDw ? blockIdx.y : 0;
+
+  // tile of this workgroup: XCD by XCD, in groups of 4 tile rows
+  const int ntm = (p.M + RM - 1) / RM;
+  const int64_t ntn = (p.N + BN - 1) / BN, ntiles = ntm * ntn;
+  const int64_t per_xcd = (ntiles + 7) / 8;
+  const int64_t t = (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= per_xcd || t >= ntiles) return;
+  constexpr int GM = 4;
+  const int64_t gsize = GM * ntn;
+  const int g0 = (int)(t / gsize) * GM, gm = min(GM, ntm - g0);
+  const int64_t tg = t - (t / gsize) * gsize;
+  const int n0 = (g0 + (int)(tg % gm)) * RM;
+  const int64_t t0 = tg / gm * BN;
+
+  // steps of KG 128 bytes of k, those of the second segment behind the first's
+  const int64_t nks = (p.K + KG * BK - 1) / (KG * BK), all = SEGS * nks;
+  const int splits = MODE == kFfnDn ? p.splits : 1, mine = MODE == kFfnDn ? blockIdx.y : 0;
+  const int64_t s_begin = all * mine / splits, s_end = all * (mine + 1) / splits;
+
+  // copy i of wave w fills 1 KB of its group's part (A first)
+  uint32_t voff[NCP];
+  int kc[NCP];                                           // byte (rows of k) or row (k-major) of k within the step
+#pragma unroll
+  for (int i = 0; i < NCP; ++i) {
+    const bool is_a = i < NCX;
+    const bool km = is_a ? kMajorA<MODE> : kMajorB<MODE>;
+    if (!km) {
+      const int r = 8 * (NW * (is_a ? i : i - NCX) + w) + (l >> 3);
+      kc[i] = grp * 128 + 16 * ((l & 7) ^ swz<8>(r));
+      // gate tile: 32-row block b is channels 32 (b / 2) .. of matrix b % 2
+      const int64_t row = GATE && is_a ? (r >> 6) * 32 + (r & 31) : r;
+      voff[i] = (uint32_t)(row * (is_a ? p.lda : p.ldb) * E + kc[i]);
+    } else {
+      const int chunks = (is_a ? KPA : KPB) / 16, q = (is_a ? i : i - NCX) * NW + w;
+      const int k = (64 * q + l) / chunks, x = (64 * q + l) % chunks;
+      kc[i] = grp * BK + k;
+      voff[i] = (uint32_t)((int64_t)kc[i] * (is_a ? p.lda : p.ldb) * E) + 16u * (uint32_t)(x ^ (is_a ? ksw<T, KPA>(k) : ksw<T, KPB>(k)));
+    }
+  }
+  const uint32_t lds0 = lds_addr(lds) + (uint32_t)(grp * PART + w * 1024);
+  auto span = [](int64_t bytes) __attribute__((always_inline)) {
+    return bytes <= 0 ? 0u : bytes > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)bytes;
+  };
+  auto issue = [&](int64_t step, int buf) __attribute__((always_inline)) {
+    const int seg = SEGS == 2 && step >= nks;
+    const int64_t k0 = (step - (seg ? nks : 0)) * KG * BK, left = step < s_end ? p.K - k0 : 0;
+    const char* pa = static_cast<const char*>(seg ? p.a[1] : p.a[0]);
+    const char* pb = static_cast<const char*>(seg || z ? p.b[1] : p.b[0]);
+    u32x4 ra[2], rb;
+    if constexpr (kMajorA<MODE>) {
+      ra[0] = ra[1] = uniform_rsrc(left > 0 ? pa + (k0 * p.lda + n0) * E : pa, span(left > 0 ? (left * p.lda - n0) * E : 0));
+    } else {
+      const int64_t o = left > 0 ? ((int64_t)n0 * p.lda + k0) * E : 0, n = left > 0 ? ((int64_t)(p.M - n0) * p.lda - k0) * E : 0;
+      ra[0] = uniform_rsrc(pa + o, span(n));
+      ra[1] = GATE ? uniform_rsrc(static_cast<const char*>(p.a[1]) + o, span(n)) : ra[0];
+    }
+    if constexpr (kMajorB<MODE>) rb = uniform_rsrc(left > 0 ? pb + (k0 * p.ldb + t0) * E : pb, span(left > 0 ? (left * p.ldb - t0) * E : 0));
+    else rb = uniform_rsrc(left > 0 ? pb + (t0 * p.ldb + k0) * E : pb, span(left > 0 ? ((p.N - t0) * p.ldb - k0) * E : 0));
+    const uint32_t base = lds0 + (uint32_t)(buf * STAGE);
+#pragma unroll
+    for (int i = 0; i < NCP; ++i) {
+      const bool is_a = i < NCX;
+      const bool km = is_a ? kMajorA<MODE> : kMajorB<MODE>;
+      const bool out = !km && kc[i] >= left * E;
+      // 1 KB of A is 8 rows: matrix (row / 32) % 2
+      const int block = is_a && GATE ? ((NW * i + w) >> 2) & 1 : 0;
+      dma16s(is_a ? (block ? ra[1] : ra[0]) : rb, out ? kOutOfRange : voff[i], 0u, base + (uint32_t)(i * NW * 1024));
+    }
+  };
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
+  const int la = klane<T, KPA>(l), lb = klane<T, KPB>(l);
+
+#pragma unroll
+  for (int st = 0; st < NST - 1; ++st) issue(s_begin + st, st);
+  int cur = 0;
+  for (int64_t kt = s_begin; kt < s_end; ++kt) {
+    // step kt has landed once at most the copies of the NST - 2 steps after it
+    // are in flight (past the end they read zeros); the barrier shows it to every
+    // wave and ends their reads of step kt - 1, whose stage the next copies take
+    __builtin_amdgcn_s_waitcnt(vm_wait((NST - 2) * NCP));
+    __syncthreads();
+    issue(kt + NST - 1, cur == 0 ? NST - 1 : cur - 1);
+    const unsigned char* sb = lds + cur * STAGE + grp * PART;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int col = 2 * h + (l >> 5);
+      uint4 fa[TM], fb[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int r = wm * WM + i * 32 + (l & 31);
+        if constexpr (kMajorA<MODE>) fa[i] = kfrag<T, KPA>(sb, la, wm * TM + i, h);
+        else fa[i] = *reinterpret_cast<const uint4*>(sb + r * 128 + ((col ^ swz<8>(r)) << 4));
+      }
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int r = wn * WN + j * 32 + (l & 31);
+        if constexpr (kMajorB<MODE>) fb[j] = kfrag<T, KPB>(sb + BM * 128, lb, wn * TN + j, h);
+        else fb[j] = *reinterpret_cast<const uint4*>(sb + BM * 128 + r * 128 + ((col ^ swz<8>(r)) << 4));
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) mma16<T>(acc[i][j], fa[i], fb[j]);
+    }
+    cur = cur + 1 == NST ? 0 : cur + 1;
+  }
+
+  // the sums as columns of BM rows, in the stages: lane l holds column (l & 31)
+  // and rows 8 a + 4 (l / 32) + e of each 32 x 32 tile
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the last copies (zeros) are in
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int x = 0; x < KG; ++x) {
+    if (grp == x) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            float4* d = reinterpret_cast<float4*>(sums + (wn * WN + j * 32 + (l & 31)) * PITCH + wm * WM + i * 32 + 8 * a + 4 * (l >> 5));
+            float4 v = make_float4(acc[i][j][4 * a], acc[i][j][4 * a + 1], acc[i][j][4 * a + 2], acc[i][j][4 * a + 3]);
+            if (x > 0) {
+              const float4 o = *d;
+              v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+            }
+            *d = v;
+          }
+    }
+    __syncthreads();
+  }
+  const int cols = (int)min<int64_t>(BN, p.N - t0);
+  if (MODE == kFfnDn && p.part) {
+    float* out = p.part + (int64_t)mine * p.N * p.M;     // M a multiple of 8
+    for (int x = tid * 4; x < BM * BN; x += NT * 4) {
+      const int c = x / BM, r = x % BM;
+      if (c < cols && n0 + r < p.M)
+        *reinterpret_cast<float4*>(out + (t0 + c) * p.M + n0 + r) = *reinterpret_cast<const float4*>(sums + c * PITCH + r);
+    }
+    return;
+  }
+  // rows r .. r + 3 of column c of output o
+  auto four = [&](int o, int c, int r, float (&f)[4]) __attribute__((always_inline)) {
+    // gate tile: channel r is row 64 (r / 32) + r % 32 for gate, 32 behind that for up
+    const float4 a = *reinterpret_cast<const float4*>(sums + c * PITCH + (GATE ? 64 * (r >> 5) + (r & 31) : r));
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    if constexpr (GATE) {
+      if (o == 0) return;
+      const float4 b = *reinterpret_cast<const float4*>(sums + c * PITCH + 64 * (r >> 5) + 32 + (r & 31));
+      const float y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = o == 1 ? y[e] : f[e] * sigmoid(f[e]) * y[e];
+    }
+  };
+#pragma unroll
+  for (int o = 0; o < (GATE ? 3 : 1); ++o) {
+    T* out = static_cast<T*>(MODE == kFfnDw && z ? p.out[1] : p.out[o]);
+    if (!out) continue;
+    if (p.M % 4 == 0) {
+      for (int x = tid * 4; x < RM * BN; x += NT * 4) {
+        const int c = x / RM, r = x % RM;
+        if (c >= cols || n0 + r >= p.M) continue;
+        float f[4];
+        four(o, c, r, f);
+        *reinterpret_cast<typename Four<T>::type*>(out + (t0 + c) * p.M + n0 + r) = Four<T>::of(f[0], f[1], f[2], f[3]);
+      }
+    } else {
+      for (int x = tid; x < RM * BN; x += NT) {
+        const int c = x / RM, r = x % RM;
+        if (c >= cols || n0 + r >= p.M) continue;
+        float f[4];
+        four(o, c, r & ~3, f);
+        const int e = r & 3;
+        out[(t0 + c) * p.M + n0 + r] = to_type<T>(e == 0 ? f[0] : e == 1 ? f[1] : e == 2 ? f[2] : f[3]);
+      }
+    }
+  }
+}
+
+// out = the splits' sums added in order
+template <typename T>
+__global__ __launch_bounds__(256) void ffn_join_kernel(const float* part, int splits, int64_t n4, T* out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  float4 s = reinterpret_cast<const float4*>(part)[i];
+  for (int x = 1; x < splits; ++x) {
+    const float4 v = reinterpret_cast<const float4*>(part)[x * n4 + i];
+    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+  }
+  reinterpret_cast<typename Four<T>::type*>(out)[i] = Four<T>::of(s.x, s.y, s.z, s.w);
+}
+
+// dg = dh u silu'(g), du = dh silu(g) in rows of I8 = I rounded up to 8 elements,
+// zeros behind I (they are k of dn's product).  A thread has 8 channels of a token.
+template <typename T>
+__global__ __launch_bounds__(256) void ffn_grad_kernel(const T* dh, const T* g, const T* u, int64_t rows, int I, int I8, T* dg, T* du) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i >= rows * I8) return;
+  const int64_t t = i / I8;
+  const int c = (int)(i - t * I8);
+  const int64_t o = t * I + c;
+  T x[3][8];
+  const T* src[3] = {dh, g, u};
+  constexpr int V = 16 / sizeof(T);
+  if (I % 8 == 0) {
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+      for (int v = 0; v < 8 / V; ++v) *reinterpret_cast<uint4*>(&x[s][v * V]) = *reinterpret_cast<const uint4*>(src[s] + o + v * V);
+  } else {
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[s][e] = c + e < I ? src[s][o + e] : (T)0.f;
+  }
+  typename Four<T>::type og[2], ou[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float a[4], b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float d = (float)x[0][4 * h + e], gv = (float)x[1][4 * h + e], uv = (float)x[2][4 * h + e];
+      const float sg = sigmoid(gv), silu = gv * sg;
+      a[e] = d * uv * fmaf(silu, 1.0f - sg, sg);
+      b[e] = d * silu;
+    }
+    og[h] = Four<T>::of(a[0], a[1], a[2], a[3]);
+    ou[h] = Four<T>::of(b[0], b[1], b[2], b[3]);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    reinterpret_cast<typename Four<T>::type*>(dg + i)[h] = og[h];
+    reinterpret_cast<typename Four<T>::type*>(du + i)[h] = ou[h];
+  }
+}
+
+template <typename T, int MODE, int BM, int BN, int WGM, int WGN, int KG, int NST>
+hipError_t launch_tile(const FfnMmParams& p, hipStream_t st) {
+  constexpr int RM = MODE == kFfnGate ? BM / 2 : BM;
+  const int64_t ntiles = (int64_t)((p.M + RM - 1) / RM) * ((p.N + BN - 1) / BN);
+  const dim3 grid((unsigned)(8 * ((ntiles + 7) / 8)), MODE == kFfnDw ? 2 : MODE == kFfnDn ? p.splits : 1);
+  hipLaunchKernelGGL((ffn_tile_kernel<T, MODE, BM, BN, WGM, WGN, KG, NST>), grid, dim3(64 * WGM * WGN * KG), 0, st, p);
+  return hipGetLastError();
+}
+
+// The variant for a product of this shape; splits (kDn) are chosen here too.
+enum { kBig = 0, k128 = 1, k64 = 2, k32 = 3 };
+int choose(int mode, int64_t N, int M) {
+  const int mats = mode == kFfnGate ? 1 : mode == kFfnDw ? 2 : 1;
+  const int64_t rows = mode == kFfnGate ? 2 * (int64_t)M : M;
+  auto tiles = [&](int m, int n) { return mats * ((rows + m - 1) / m) * ((N + n - 1) / n); };
+  if (tiles(256, 256) >= 160) return kBig;
+  if (tiles(128, 128) > 256) return k128;
+  if (mode == kFfnGate || tiles(64, 64) > 128) return k64;
+  return k32;
+}
+
+template <typename T>
+hipError_t launch_ffn_t(const FfnMmParams& p0, int mode, hipStream_t st) {
+  FfnMmParams p = p0;
+  const int v = choose(mode, p.N, p.M);
+  if (mode == kFfnGate) {
+    if (v == kBig) {
+      if ((p.M * sizeof(T)) % 16 == 0) hipLaunchKernelGGL((ffn_big_kernel<T, kFfnGate, true>), dim3(256), dim3(256), 0, st, p);
+      else hipLaunchKernelGGL((ffn_big_kernel<T, kFfnGate, false>), dim3(256), dim3(256), 0, st, p);
+      return hipGetLastError();
+    }
+    if (v == k128) return launch_tile<T, kFfnGate, 128, 128, 2, 2, 1, 2>(p, st);
+    return launch_tile<T, kFfnGate, 64, 64, 2, 2, 2, 2>(p, st);
+  }
+  if (mode == kFfnDw) {
+    if (v == kBig) {
+      hipLaunchKernelGGL((ffn_big_kernel<T, kFfnDw, true>), dim3(256), dim3(256), 0, st, p);
+      return hipGetLastError();
+    }
+    if (v == k128) return launch_tile<T, kFfnDw, 128, 128, 2, 2, 1, 2>(p, st);
+    return launch_tile<T, kFfnDw, 64, 64, 2, 2, 2, 2>(p, st);
+  }
+  if (v == kBig) {
+    hipLaunchKernelGGL((ffn_big_kernel<T, kFfnDn, true>), dim3(256), dim3(256), 0, st, p);
+    return hipGetLastError();
+  }
+  hipError_t e;
+  if (p.splits == 1) p.part = nullptr;
+  if (v == k128) e = launch_tile<T, kFfnDn, 128, 128, 2, 2, 1, 2>(p, st);
+  else if (v == k64) e = launch_tile<T, kFfnDn, 64, 64, 2, 2, 2, 2>(p, st);
+  else e = launch_tile<T, kFfnDn, 32, 32, 1, 1, 4, 4>(p, st);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t n4 = p.N * p.M / 4;
+  hipLaunchKernelGGL(ffn_join_kernel<T>, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st, p.part, p.splits, n4, static_cast<T*>(p.out[0]));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int ffn_dn_splits(int64_t T, int C, int I) {
+  const int v = choose(kFfnDn, T, C);
+  if (v == kBig) return 1;
+  const int b = v == k128 ? 128 : v == k64 ? 64 : 32;
+  const int64_t tiles = (int64_t)((C + b - 1) / b) * ((T + b - 1) / b);
+  const int64_t most = std::min<int64_t>(16, ((int64_t)I + 1023) / 1024);   // 2048 of k a split at least
+  return (int)std::max<int64_t>(1, std::min(most, 256 / std::max<int64_t>(tiles, 1)));
+}
+
+hipError_t launch_ffn_mm(const FfnMmParams& p, int mode, int bf16, hipStream_t st) {
+  if (p.N == 0 || p.M == 0) return hipSuccess;
+  return bf16 ? launch_ffn_t<__bf16>(p, mode, st) : launch_ffn_t<float>(p, mode, st);
+}
+
+hipError_t launch_ffn_grad(const void* dh, const void* g, const void* u, int64_t rows, int I, int I8, void* dg, void* du, int bf16,
+                           hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  const dim3 grid((unsigned)((rows * I8 / 8 + 255) / 256));
+  if (bf16)
+    hipLaunchKernelGGL(ffn_grad_kernel<__bf16>, grid, dim3(256), 0, st, static_cast<const __bf16*>(dh), static_cast<const __bf16*>(g),
+                       static_cast<const __bf16*>(u), rows, I, I8, static_cast<__bf16*>(dg), static_cast<__bf16*>(du));
+  else
+    hipLaunchKernelGGL(ffn_grad_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(dh), static_cast<const float*>(g),
+                       static_cast<const float*>(u), rows, I, I8, static_cast<float*>(dg), static_cast<float*>(du));
+  return hipGetLastError();
+}
+
+}  // namespace hna

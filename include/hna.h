@@ -512,6 +512,48 @@ int hna_quant_matmul_pair(int64_t T, int32_t N, int32_t K, int32_t out_dtype, co
                           const int8_t* w1, const float* w1_scale, void* out0, void* out1,
                           void* stream);
 
+/* ---------------------------------------------------------- gated FFN */
+
+/*
+ * The FFN's pre-activations and their product, and the gradients of both:
+ *   g = n W_gate^T,  u = n W_up^T,  h = silu(g) u          [T, I]
+ *   dg = dh u silu'(g),  du = dh silu(g)
+ *   dn = dg W_gate + du W_up [T, hidden],  dW_gate = dg^T n,  dW_up = du^T n [I, hidden]
+ * n [T, hidden] is the normed FFN input (the norm step's n), W_gate and W_up
+ * [I, hidden].  Every tensor has dims' dtype; sums are fp32 and rounded once; h
+ * comes from the fp32 g and u, not from the stored ones; dg and du, which the
+ * products of the gradients read, are rounded to dtype.
+ *   hidden  a positive multiple of 8, at most 65536;  1 <= I <= 2^20
+ *   T >= 0, T < 2^31;  T I <= 2^34 and T hidden <= 2^36 (HNA_ERR_UNSUPPORTED above)
+ * A NaN or an infinity in a row of n or dh stays in that row of g, u, h and dn.
+ * Outputs overlap neither each other nor inputs.
+ */
+typedef struct hna_ffn_dims {
+  int64_t T;
+  int32_t hidden;
+  int32_t I;
+  int32_t dtype;
+} hna_ffn_dims;
+
+/* g, u, h: each may be NULL, not all (g and u without h: the affinity pass's
+ * inputs; h without g and u: serving; all three: training). */
+int hna_gated_ffn(const hna_ffn_dims* dims, const void* n, const void* W_gate, const void* W_up,
+                  void* g, void* u, void* h, void* stream);
+
+/* Bytes of workspace hna_gated_ffn_backward needs (0 for invalid dims). */
+size_t hna_gated_ffn_workspace_bytes(const hna_ffn_dims* dims);
+
+/*
+ * Gradients from dh at the g and u that hna_gated_ffn wrote.  dn may be NULL, and
+ * dW_gate with dW_up, not all; n is needed with dW_gate, the weights with dn.
+ * The outputs are written, not added to (zeros in dW for T = 0), summed in a
+ * fixed order: no atomics.
+ */
+int hna_gated_ffn_backward(const hna_ffn_dims* dims, const void* dh, const void* n,
+                           const void* W_gate, const void* W_up, const void* g, const void* u,
+                           void* dn, void* dW_gate, void* dW_up, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /*
