@@ -15,7 +15,9 @@ from ._binding import (HnaError, HNA_BF16, HNA_F32, HNA_ACCUMULATE, hna_dims, hn
                        mfma_rate_probe, hna_norm_dims, block_norm, block_norm_quant,
                        block_norm_backward, block_norm_workspace_bytes, quant_pitch, quant_rows,
                        quant_matmul, quant_matmul_pair, hna_ffn_dims, gated_ffn,
-                       gated_ffn_backward, gated_ffn_workspace_bytes)
+                       gated_ffn_backward, gated_ffn_workspace_bytes, hna_attn_dims, hna_step_dims,
+                       attention_rows, attention, attention_backward, attention_workspace_bytes,
+                       attention_step, attention_step_workspace_bytes)
 from .pipeline import (AffinityPass, StackPass, FfnInputs, pass_for_layer, affinity_layer,
                        ffn_inputs)
 
@@ -31,4 +33,6 @@ __all__ = [
     "hna_norm_dims", "block_norm", "block_norm_quant", "block_norm_backward",
     "block_norm_workspace_bytes", "quant_pitch", "quant_rows", "quant_matmul", "quant_matmul_pair", "FfnInputs", "ffn_inputs",
     "hna_ffn_dims", "gated_ffn", "gated_ffn_backward", "gated_ffn_workspace_bytes",
+    "hna_attn_dims", "hna_step_dims", "attention_rows", "attention", "attention_backward",
+    "attention_workspace_bytes", "attention_step", "attention_step_workspace_bytes",
 ]

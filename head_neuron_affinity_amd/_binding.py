@@ -46,7 +46,9 @@ EXPORTED = [
     "hna_mfma_rate_probe", "hna_block_norm", "hna_block_norm_quant",
     "hna_block_norm_workspace_bytes", "hna_block_norm_backward", "hna_quant_pitch",
     "hna_quant_rows", "hna_quant_matmul", "hna_quant_matmul_pair", "hna_gated_ffn",
-    "hna_gated_ffn_workspace_bytes", "hna_gated_ffn_backward",
+    "hna_gated_ffn_workspace_bytes", "hna_gated_ffn_backward", "hna_attention_rows", "hna_attention",
+    "hna_attention_workspace_bytes", "hna_attention_backward", "hna_attention_step_workspace_bytes",
+    "hna_attention_step",
 ]
 
 
@@ -69,6 +71,20 @@ class hna_norm_dims(ctypes.Structure):
 class hna_ffn_dims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("hidden", ctypes.c_int32), ("I", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class hna_attn_dims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64),
+                ("ld_v", ctypes.c_int64), ("H", ctypes.c_int32), ("G", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("cap", ctypes.c_float)]
+
+
+class hna_step_dims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64),
+                ("bs_k", ctypes.c_int64), ("bs_v", ctypes.c_int64), ("S", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("G", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("cap", ctypes.c_float)]
 
 
 class HnaError(RuntimeError):
@@ -94,6 +110,8 @@ def lib() -> ctypes.CDLL:
     ddp = ctypes.POINTER(hna_down_dims)
     ndp = ctypes.POINTER(hna_norm_dims)
     fdp = ctypes.POINTER(hna_ffn_dims)
+    adp = ctypes.POINTER(hna_attn_dims)
+    sdp = ctypes.POINTER(hna_step_dims)
     ip = ctypes.POINTER(ctypes.c_int32)
     sig = {
         "hna_abi_version": (ctypes.c_int, []),
@@ -134,6 +152,13 @@ def lib() -> ctypes.CDLL:
         "hna_gated_ffn": (ctypes.c_int, [fdp, vp, vp, vp, vp, vp, vp, vp]),
         "hna_gated_ffn_workspace_bytes": (sz, [fdp]),
         "hna_gated_ffn_backward": (ctypes.c_int, [fdp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "hna_attention_rows": (ctypes.c_int, [i64, i32, vp, vp, i32, vp, vp]),
+        "hna_attention": (ctypes.c_int, [adp, vp, vp, vp, vp, vp, ip, vp, vp, vp]),
+        "hna_attention_workspace_bytes": (sz, [adp]),
+        "hna_attention_backward": (ctypes.c_int, [adp, vp, vp, vp, vp, vp, vp, vp, vp, ip, vp, vp, vp, vp,
+                                                  sz, vp]),
+        "hna_attention_step_workspace_bytes": (sz, [sdp]),
+        "hna_attention_step": (ctypes.c_int, [sdp, vp, vp, vp, vp, vp, vp, ip, vp, vp, vp, sz, vp]),
         "hna_mfma_rate_probe": (ctypes.c_int, [i32, i32, i32, vp, vp, vp]),
         "hna_layout_search": (ctypes.c_int, [i32, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp,
                                               ctypes.POINTER(ctypes.c_double), ip, vp, sz, vp]),
@@ -971,3 +996,204 @@ def gated_ffn_backward(dh, n, w_gate, w_up, g, u, *, want_dn: bool = True, want_
                                     workspace.numel() * workspace.element_size(), _raw_stream(index)),
            "hna_gated_ffn_backward")
     return dn, dw_gate, dw_up
+
+
+# ------------------------------------------------------------------ attention
+def _gpu_of(index, *ts) -> int:
+    """_index_of for tensors that need not be contiguous, on the GPU `index`."""
+    for t in ts:
+        if t.get_device() != index:
+            raise ValueError("all tensors must live on the same GPU")
+    return index
+
+
+def _heads_ld(t, name: str, shape: tuple, dtype: torch.dtype) -> int:
+    """Elements from token to token of t [tokens, heads, d], whose heads lie next to each other."""
+    _is(t, name, shape, dtype)
+    tokens, heads, d = shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a token's heads must lie next to each other (strides {t.stride()})")
+    return t.stride(0) if tokens > 1 else heads * d
+
+
+_MAPS: dict = {}
+
+
+def _head_map(group_of_head, H: int, G: int):
+    """group_of_head, by default heads in blocks of H / G."""
+    if group_of_head is not None:
+        if len(group_of_head) != H:
+            raise ValueError(f"group_of_head has {len(group_of_head)} entries, expected {H}")
+        return _map(group_of_head)
+    m = _MAPS.get((H, G))
+    if m is None:
+        if G < 1 or H % G:
+            raise ValueError(f"H={H} is not a multiple of G={G}")
+        m = _MAPS[(H, G)] = _map([h * G // H for h in range(H)])
+    return m
+
+
+def attention_rows(T: int, doc_start, prefix=None, causal: bool = True, rows=None):
+    """Which keys each of T tokens' queries sees (hna_attention_rows): int32 [T, 4] for attention.
+
+    doc_start int32 [documents + 1]: document i is tokens doc_start[i] .. doc_start[i + 1] - 1.  causal:
+    a query sees its document up to itself and the document's first prefix[i] tokens (int32
+    [documents], optional); otherwise all of its document.  Made once for a batch."""
+    if doc_start.dim() != 1 or doc_start.shape[0] < 2:
+        raise ValueError(f"doc_start: shape {tuple(doc_start.shape)}, expected [documents + 1]")
+    n = doc_start.shape[0] - 1
+    T = int(T)
+    _is(doc_start, "doc_start", (n + 1,), torch.int32)
+    _is(prefix, "prefix", (n,), torch.int32)
+    _is(rows, "rows", (T, 4), torch.int32)
+    index = _index_of(doc_start, prefix, rows)
+    if index != _current():
+        with torch.cuda.device(index):
+            return attention_rows(T, doc_start, prefix, causal, rows)
+    if rows is None:
+        rows = torch.empty((T, 4), dtype=torch.int32, device=doc_start.device)
+    _check(lib().hna_attention_rows(T, n, _at(doc_start), _at(prefix), int(bool(causal)), _at(rows),
+                                    _raw_stream(index)), "hna_attention_rows")
+    return rows
+
+
+def _attn_args(q, k, v, rows, slopes, causal, scale, cap):
+    """Checks what forward and backward share; (dims, index of the GPU)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [T, heads, d]")
+    T, H, d = q.shape
+    G = k.shape[1]
+    dt = q.dtype
+    dims = hna_attn_dims(T, _heads_ld(q, "q", (T, H, d), dt), _heads_ld(k, "k", (T, G, d), dt),
+                         _heads_ld(v, "v", (T, G, d), dt), H, G, d, _code(dt), int(bool(causal)),
+                         d ** -0.5 if scale is None else scale, cap)
+    _is(rows, "rows", (T, 4), torch.int32)
+    _is(slopes, "slopes", (H,), torch.float32)
+    index = q.get_device()
+    if index < 0:
+        raise ValueError("all tensors must live on the GPU")
+    _gpu_of(index, k, v)
+    return dims, index
+
+
+def _same_gpu(index: int, *ts):
+    """Contiguous tensors, if any, on the GPU `index`."""
+    other = _index_of(*ts)
+    if other is not None and other != index:
+        raise ValueError("all tensors must live on the same GPU")
+
+
+def attention(q, k, v, rows=None, *, causal: bool = True, scale: Optional[float] = None, cap: float = 0.0,
+              slopes=None, group_of_head: Optional[Sequence[int]] = None, out=None, lse=None):
+    """Attention of tokens in a row (hna_attention): (a [T, H, d], lse [T, H] fp32).
+
+    q [T, H, d], k, v [T, G, d], a token's heads next to each other, tokens any distance apart.  rows: who
+    sees whom, from attention_rows; without it one document, causal or not.  scale: of the scores, default
+    d^-0.5; cap > 0: scores become cap tanh(score / cap); slopes fp32 [H]: minus slopes[h] |i - j|."""
+    dims, index = _attn_args(q, k, v, rows, slopes, causal, scale, cap)
+    T, H, d = q.shape
+    _is(out, "out", (T, H, d), q.dtype)
+    _is(lse, "lse", (T, H), torch.float32)
+    _same_gpu(index, rows, slopes, out, lse)
+    if index != _current():
+        with torch.cuda.device(index):
+            return attention(q, k, v, rows, causal=causal, scale=scale, cap=cap, slopes=slopes,
+                             group_of_head=group_of_head, out=out, lse=lse)
+    if out is None:
+        out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    _check(lib().hna_attention(ctypes.byref(dims), _at(q), _at(k), _at(v), _at(rows), _at(slopes),
+                               _head_map(group_of_head, H, dims.G), _at(out), _at(lse), _raw_stream(index)),
+           "hna_attention")
+    return out, lse
+
+
+def attention_workspace_bytes(dims: hna_attn_dims) -> int:
+    return int(lib().hna_attention_workspace_bytes(ctypes.byref(dims)))
+
+
+def attention_backward(da, q, k, v, a, lse, rows=None, *, causal: bool = True, scale: Optional[float] = None,
+                       cap: float = 0.0, slopes=None, group_of_head: Optional[Sequence[int]] = None, dq=None,
+                       dk=None, dv=None, workspace=None):
+    """Gradients of attention (hna_attention_backward) from da, that of a, at the a and lse it returned;
+    the other arguments as for attention.  Returns (dq [T, H, d], dk, dv [T, G, d])."""
+    dims, index = _attn_args(q, k, v, rows, slopes, causal, scale, cap)
+    (T, H, d), G, dt = q.shape, dims.G, q.dtype
+    _is(da, "da", (T, H, d), dt)
+    _is(a, "a", (T, H, d), dt)
+    _is(lse, "lse", (T, H), torch.float32)
+    _is(dq, "dq", (T, H, d), dt)
+    _is(dk, "dk", (T, G, d), dt)
+    _is(dv, "dv", (T, G, d), dt)
+    _same_gpu(index, da, a, lse, rows, slopes, dq, dk, dv, workspace)
+    if index != _current():
+        with torch.cuda.device(index):
+            return attention_backward(da, q, k, v, a, lse, rows, causal=causal, scale=scale, cap=cap,
+                                      slopes=slopes, group_of_head=group_of_head, dq=dq, dk=dk, dv=dv,
+                                      workspace=workspace)
+    if dq is None:
+        dq = torch.empty((T, H, d), dtype=dt, device=q.device)
+    if dk is None:
+        dk = torch.empty((T, G, d), dtype=dt, device=q.device)
+    if dv is None:
+        dv = torch.empty_like(dk)
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(L.hna_attention_workspace_bytes(ctypes.byref(dims)) or 16, dtype=torch.uint8,
+                                device=q.device)
+    _check(L.hna_attention_backward(ctypes.byref(dims), _at(da), _at(q), _at(k), _at(v), _at(a), _at(lse),
+                                    _at(rows), _at(slopes), _head_map(group_of_head, H, G), _at(dq), _at(dk),
+                                    _at(dv), _at(workspace), workspace.numel() * workspace.element_size(),
+                                    _raw_stream(index)), "hna_attention_backward")
+    return dq, dk, dv
+
+
+def attention_step_workspace_bytes(dims: hna_step_dims) -> int:
+    return int(lib().hna_attention_step_workspace_bytes(ctypes.byref(dims)))
+
+
+def attention_step(q, k, v, lengths, starts=None, *, scale: Optional[float] = None, cap: float = 0.0, slopes=None,
+                   group_of_head: Optional[Sequence[int]] = None, out=None, lse=None, workspace=None):
+    """Attention of one new token for each of B sequences over a cache (hna_attention_step):
+    (a [B, H, d], lse [B, H] fp32).
+
+    q [B, H, d]; k, v [B, S, G, d], the heads of a key next to each other; lengths int32 [B]: the query
+    stands at lengths[b] - 1 and sees keys starts[b] (int32 [B], default 0) .. lengths[b] - 1.  scale, cap
+    and slopes as for attention."""
+    if q.dim() != 3 or k.dim() != 4:
+        raise ValueError("q must be [B, H, d], k and v [B, S, G, d]")
+    B, H, d = q.shape
+    S, G = k.shape[1:3]
+    dt = q.dtype
+    _is(k, "k", (B, S, G, d), dt)
+    _is(v, "v", (B, S, G, d), dt)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.numel() and (t.stride(3) != 1 or (G > 1 and t.stride(2) != d)):
+            raise ValueError(f"{name}: a key's heads must lie next to each other (strides {t.stride()})")
+    ld = [t.stride(1) if S > 1 else G * d for t in (k, v)]
+    bs = [t.stride(0) if B > 1 else 0 for t in (k, v)]
+    dims = hna_step_dims(B, *ld, *bs, S, H, G, d, _code(dt), d ** -0.5 if scale is None else scale, cap)
+    _is(lengths, "lengths", (B,), torch.int32)
+    _is(starts, "starts", (B,), torch.int32)
+    _is(slopes, "slopes", (H,), torch.float32)
+    _is(out, "out", (B, H, d), dt)
+    _is(lse, "lse", (B, H), torch.float32)
+    index = _gpu_of(_index_of(q, lengths, starts, slopes, out, lse, workspace), k, v)
+    if index != _current():
+        with torch.cuda.device(index):
+            return attention_step(q, k, v, lengths, starts, scale=scale, cap=cap, slopes=slopes,
+                                  group_of_head=group_of_head, out=out, lse=lse, workspace=workspace)
+    if out is None:
+        out = torch.empty((B, H, d), dtype=dt, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(L.hna_attention_step_workspace_bytes(ctypes.byref(dims)) or 16, dtype=torch.uint8,
+                                device=q.device)
+    _check(L.hna_attention_step(ctypes.byref(dims), _at(q), _at(k), _at(v), _at(lengths), _at(starts), _at(slopes),
+                                _head_map(group_of_head, H, G), _at(out), _at(lse), _at(workspace),
+                                workspace.numel() * workspace.element_size(), _raw_stream(index)),
+           "hna_attention_step")
+    return out, lse

@@ -13,7 +13,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 
 SOURCES = ["hna_api.hip", "k_affinity.hip", "k_gram.hip", "k_gemm.hip", "k_mm.hip",
            "k_small.hip", "k_objective.hip", "k_layout.hip", "k_loo.hip", "k_probe.hip",
-           "k_norm.hip", "k_mm_int.hip", "k_ffn.hip"]
+           "k_norm.hip", "k_mm_int.hip", "k_ffn.hip",
+           "k_attn.hip", "k_attn_grad.hip", "k_attn_step.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -52,7 +53,7 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
         objs.append(obj)
         jobs.append([HIPCC, *FLAGS, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj])
-    with ThreadPoolExecutor(max_workers=min(4, len(jobs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
         for msg in ex.map(_run, jobs):
             if verbose and msg.strip():
                 print(msg, file=sys.stderr)

@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -241,6 +242,110 @@ int check_quant_matmul(const char* fn, int64_t T, int32_t N, int32_t K, int32_t 
     return fail(HNA_ERR_UNSUPPORTED, "%s: T=%lld, N=%d: more than 2^30 tokens, 2^22 channels or 2^36 outputs",
                 fn, (long long)T, N);
   return HNA_OK;
+}
+
+// ---- attention ----
+constexpr int64_t kMaxAttnLd = 1 << 20;               // a tile's rows lie within 31 bits
+constexpr int64_t kMaxAttnRows = (int64_t)1 << 30;    // T H: at most 2^23 workgroups
+constexpr int64_t kMaxStepRows = (int64_t)1 << 22;    // B H
+constexpr int32_t kMaxStepKeys = 1 << 30;
+
+int check_attn_heads(const char* fn, int dtype, int H, int G, int d, float scale, float cap) {
+  const int rc = check_dtype(fn, dtype);
+  if (rc) return rc;
+  const int rh = check_heads(fn, 8, H, G, d);
+  if (rh) return rh;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(HNA_ERR_INVALID_ARG, "%s: scale=%g must be finite and > 0", fn, scale);
+  if (!(cap >= 0.f) || !std::isfinite(cap)) return fail(HNA_ERR_INVALID_ARG, "%s: cap=%g must be finite and >= 0", fn, cap);
+  return HNA_OK;
+}
+
+int check_ld(const char* fn, const char* name, int64_t ld, int64_t least) {
+  if (ld < least) return fail(HNA_ERR_INVALID_ARG, "%s: %s=%lld < %lld", fn, name, (long long)ld, (long long)least);
+  if (ld % 8 != 0 || ld > kMaxAttnLd)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: %s=%lld must be a multiple of 8 and <= %lld", fn, name, (long long)ld, (long long)kMaxAttnLd);
+  return HNA_OK;
+}
+
+int check_attn_dims(const char* fn, const hna_attn_dims* dm) {
+  if (!dm) return fail(HNA_ERR_INVALID_ARG, "%s: dims is NULL", fn);
+  int rc = check_attn_heads(fn, dm->dtype, dm->H, dm->G, dm->d, dm->scale, dm->cap);
+  if (rc) return rc;
+  if (dm->T < 0) return fail(HNA_ERR_INVALID_ARG, "%s: T=%lld < 0", fn, (long long)dm->T);
+  if ((rc = check_ld(fn, "ld_q", dm->ld_q, (int64_t)dm->H * dm->d))) return rc;
+  if ((rc = check_ld(fn, "ld_k", dm->ld_k, (int64_t)dm->G * dm->d))) return rc;
+  if ((rc = check_ld(fn, "ld_v", dm->ld_v, (int64_t)dm->G * dm->d))) return rc;
+  if (dm->T > kMaxAttnRows || dm->T * dm->H > kMaxAttnRows)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: T=%lld with H=%d: T H > 2^30", fn, (long long)dm->T, dm->H);
+  return HNA_OK;
+}
+
+int check_step_dims(const char* fn, const hna_step_dims* dm) {
+  if (!dm) return fail(HNA_ERR_INVALID_ARG, "%s: dims is NULL", fn);
+  int rc = check_attn_heads(fn, dm->dtype, dm->H, dm->G, dm->d, dm->scale, dm->cap);
+  if (rc) return rc;
+  if (dm->B < 0 || dm->S < 0) return fail(HNA_ERR_INVALID_ARG, "%s: B=%lld, S=%d", fn, (long long)dm->B, dm->S);
+  if ((rc = check_ld(fn, "ld_k", dm->ld_k, (int64_t)dm->G * dm->d))) return rc;
+  if ((rc = check_ld(fn, "ld_v", dm->ld_v, (int64_t)dm->G * dm->d))) return rc;
+  if (dm->bs_k < 0 || dm->bs_v < 0) return fail(HNA_ERR_INVALID_ARG, "%s: bs_k=%lld, bs_v=%lld", fn, (long long)dm->bs_k, (long long)dm->bs_v);
+  if (dm->bs_k % 8 != 0 || dm->bs_v % 8 != 0)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: bs_k=%lld and bs_v=%lld must be multiples of 8", fn, (long long)dm->bs_k, (long long)dm->bs_v);
+  if (dm->B > kMaxStepRows || dm->B * dm->H > kMaxStepRows || dm->S > kMaxStepKeys)
+    return fail(HNA_ERR_UNSUPPORTED, "%s: B=%lld with H=%d, S=%d: B H > 2^22 or S > 2^30", fn, (long long)dm->B, dm->H, dm->S);
+  return HNA_OK;
+}
+
+// heads sorted by group (stable), and where each group's begin; returns the largest group's heads
+int sort_heads(const int32_t* map, int H, int G, int8_t* order, int8_t* group, int16_t* start) {
+  int n = 0, most = 0;
+  for (int g = 0; g < G; ++g) {
+    start[g] = (int16_t)n;
+    for (int h = 0; h < H; ++h)
+      if (map[h] == g) order[n++] = (int8_t)h;
+    most = std::max(most, n - start[g]);
+  }
+  start[G] = (int16_t)n;
+  if (group)
+    for (int h = 0; h < H; ++h) group[h] = (int8_t)map[h];
+  return most;
+}
+
+AttnParams attn_params(const hna_attn_dims* dm, const void* q, const void* k, const void* v, const int32_t* rows,
+                       const float* slopes, const int32_t* map) {
+  AttnParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.rows = reinterpret_cast<const int4*>(rows);
+  p.slopes = slopes;
+  p.T = dm->T;
+  p.ld_q = dm->ld_q;
+  p.ld_k = dm->ld_k;
+  p.ld_v = dm->ld_v;
+  p.H = dm->H;
+  p.G = dm->G;
+  p.d = dm->d;
+  p.causal = dm->causal != 0;
+  p.scale = dm->scale;
+  p.cap = dm->cap;
+  sort_heads(map, dm->H, dm->G, p.head_order, p.head_group, p.group_start);
+  return p;
+}
+
+size_t attn_stat_bytes(const hna_attn_dims* dm) { return align256((size_t)2 * dm->H * dm->T * sizeof(float)); }
+
+struct StepWorkspace {
+  size_t ms, total;
+  int splits;
+};
+StepWorkspace step_workspace(const hna_step_dims* dm) {
+  StepWorkspace w{};
+  w.splits = attention_step_splits(dm->B, dm->G, dm->S);
+  if (w.splits == 1) return w;
+  const size_t rows = (size_t)dm->B * dm->H * w.splits;
+  w.ms = align256(rows * dm->d * sizeof(float));
+  w.total = w.ms + align256(rows * 2 * sizeof(float));
+  return w;
 }
 
 // ---- gated FFN ----
@@ -1425,6 +1530,141 @@ int hna_gated_ffn_backward(const hna_ffn_dims* dm, const void* dh, const void* n
     if ((e = launch_ffn_mm(p, kFfnDw, bf16, st)) != hipSuccess) return hip_fail(e, fn);
   }
   return finish(hipSuccess, st, fn);
+}
+
+// ---- attention ----
+int hna_attention_rows(int64_t T, int32_t n_docs, const int32_t* doc_start, const int32_t* prefix,
+                       int32_t causal, int32_t* rows, void* stream) {
+  const char* fn = "hna_attention_rows";
+  if (T < 0 || n_docs < 1) return fail(HNA_ERR_INVALID_ARG, "%s: T=%lld, n_docs=%d", fn, (long long)T, n_docs);
+  if (T > kMaxAttnRows) return fail(HNA_ERR_UNSUPPORTED, "%s: T=%lld > 2^30", fn, (long long)T);
+  if (T > 0) {
+    REQUIRE_PTR(doc_start);
+    OPTIONAL_PTR(prefix);
+    REQUIRE_PTR(rows);
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_attention_rows(T, n_docs, doc_start, prefix, causal != 0, rows, st), st, fn);
+}
+
+int hna_attention(const hna_attn_dims* dm, const void* q, const void* k, const void* v, const int32_t* rows,
+                  const float* slopes, const int32_t* group_of_head, void* a, float* lse, void* stream) {
+  const char* fn = "hna_attention";
+  int rc = check_attn_dims(fn, dm);
+  if (rc) return rc;
+  if ((rc = check_map(fn, group_of_head, dm->H, dm->G))) return rc;
+  if (dm->T > 0) {
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(v);
+    OPTIONAL_PTR(rows);
+    OPTIONAL_PTR(slopes);
+    REQUIRE_PTR(a);
+    OPTIONAL_PTR(lse);
+  }
+  AttnParams p = attn_params(dm, q, k, v, rows, slopes, group_of_head);
+  p.a = a;
+  p.lse = lse;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_attention(p, dm->dtype == HNA_BF16, st), st, fn);
+}
+
+size_t hna_attention_workspace_bytes(const hna_attn_dims* dm) {
+  if (check_attn_dims("hna_attention_workspace_bytes", dm)) return 0;
+  return std::max(attn_stat_bytes(dm), size_t(256));
+}
+
+int hna_attention_backward(const hna_attn_dims* dm, const void* da, const void* q, const void* k, const void* v,
+                           const void* a, const float* lse, const int32_t* rows, const float* slopes,
+                           const int32_t* group_of_head, void* dq, void* dk, void* dv, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const char* fn = "hna_attention_backward";
+  int rc = check_attn_dims(fn, dm);
+  if (rc) return rc;
+  if ((rc = check_map(fn, group_of_head, dm->H, dm->G))) return rc;
+  if (dm->T > 0) {
+    REQUIRE_PTR(da);
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(v);
+    REQUIRE_PTR(a);
+    REQUIRE_PTR(lse);
+    OPTIONAL_PTR(rows);
+    OPTIONAL_PTR(slopes);
+    REQUIRE_PTR(dq);
+    REQUIRE_PTR(dk);
+    REQUIRE_PTR(dv);
+  }
+  REQUIRE_PTR(workspace);
+  const size_t need = attn_stat_bytes(dm);
+  if (workspace_bytes < need)
+    return fail(HNA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, need);
+  AttnParams p = attn_params(dm, q, k, v, rows, slopes, group_of_head);
+  p.da = da;
+  p.a = const_cast<void*>(a);
+  p.lse = const_cast<float*>(lse);
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  p.stat = static_cast<float*>(workspace);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_attention_backward(p, dm->dtype == HNA_BF16, st), st, fn);
+}
+
+size_t hna_attention_step_workspace_bytes(const hna_step_dims* dm) {
+  if (check_step_dims("hna_attention_step_workspace_bytes", dm)) return 0;
+  return std::max(step_workspace(dm).total, size_t(256));
+}
+
+int hna_attention_step(const hna_step_dims* dm, const void* q, const void* k, const void* v, const int32_t* lengths,
+                       const int32_t* starts, const float* slopes, const int32_t* group_of_head, void* a,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "hna_attention_step";
+  int rc = check_step_dims(fn, dm);
+  if (rc) return rc;
+  if ((rc = check_map(fn, group_of_head, dm->H, dm->G))) return rc;
+  if (dm->B > 0) {
+    REQUIRE_PTR(q);
+    if (dm->S > 0) {
+      REQUIRE_PTR(k);
+      REQUIRE_PTR(v);
+    }
+    REQUIRE_PTR(lengths);
+    OPTIONAL_PTR(starts);
+    OPTIONAL_PTR(slopes);
+    REQUIRE_PTR(a);
+    OPTIONAL_PTR(lse);
+  }
+  REQUIRE_PTR(workspace);
+  const StepWorkspace w = step_workspace(dm);
+  if (workspace_bytes < w.total)
+    return fail(HNA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, w.total);
+  StepParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.lengths = lengths;
+  p.starts = starts;
+  p.slopes = slopes;
+  p.a = a;
+  p.lse = lse;
+  p.part = static_cast<float*>(workspace);
+  p.part_ms = reinterpret_cast<float2*>(static_cast<char*>(workspace) + w.ms);
+  p.B = dm->B;
+  p.ld_k = dm->ld_k;
+  p.ld_v = dm->ld_v;
+  p.bs_k = dm->bs_k;
+  p.bs_v = dm->bs_v;
+  p.S = dm->S;
+  p.H = dm->H;
+  p.G = dm->G;
+  p.d = dm->d;
+  p.splits = w.splits;
+  p.column_blocks = (sort_heads(group_of_head, dm->H, dm->G, p.head_order, nullptr, p.group_start) + 31) / 32;
+  p.scale = dm->scale;
+  p.cap = dm->cap;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return finish(launch_attention_step(p, dm->dtype == HNA_BF16, st), st, fn);
 }
 
 }  // extern "C"

@@ -1,0 +1,230 @@
+// Device helpers of the attention kernels (gfx950): tiles of 64 rows (keys or
+// queries of one head) in LDS that are read both ways, as rows of the head
+// dimension and along the rows, the scores' arithmetic, and the rows of a tile
+// that hold a NaN or an infinity.
+#pragma once
+
+#include "hna_hot.h"
+#include "hna_mma.h"
+
+namespace hna {
+namespace attn {
+
+using namespace hot;
+using namespace mm;
+
+// 64 rows of d elements (d a multiple of 16, at most 32 DT) in LDS; 16-byte chunk
+// c of row r lies in slot c ^ f(r).  f is distinct over 16 rows of one chunk (a
+// fragment of rows), and puts the four rows that a transposed read takes at once
+// (64 bytes of each) in different banks.  Chunks from d on are zeros.
+template <typename T, int DT>
+struct Tile {
+  static constexpr int E = sizeof(T), F = E / 2;         // F: 16-byte pieces of a lane's 8 elements
+  static constexpr int DP = DT == 3 ? 128 : 32 * DT, PITCH = DP * E, CPR = PITCH / 16, BYTES = 64 * PITCH;
+  static constexpr int RPC = 64 / CPR;                   // rows of a 1 KB copy
+  static constexpr int COPIES = BYTES / 4096;            // of each of 4 waves
+  typedef uint4 Frag[F];
+
+  __device__ static inline int f(int r) {
+    if constexpr (CPR == 4) return (r >> 2) & 3;
+    else if constexpr (CPR == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    else return ((r & 3) << 2) | ((r >> 2) & 3);
+  }
+  // byte offsets of a lane's copies from their first row: copy i of wave w is rows
+  // (4 i + w) RPC .. of the tile, and f repeats every 16 rows
+  static constexpr int PERIOD = 16 / (4 * RPC) > 1 ? 16 / (4 * RPC) : 1;
+  __device__ static inline void offsets(uint32_t (&voff)[PERIOD], int w, int l, int64_t ld, int d) {
+#pragma unroll
+    for (int i = 0; i < PERIOD; ++i) {
+      const int r = (4 * i + w) * RPC + l / CPR, c = (l % CPR) ^ f(r);
+      voff[i] = 16 * c < d * E ? (uint32_t)(r * ld * E) + 16u * (uint32_t)c : kOutOfRange;
+    }
+  }
+  // copies of rows first .. of x, rows from `end` on are zeros
+  __device__ static inline void copy(const void* x, int64_t ld, int d, int64_t first, int64_t end, const uint32_t (&voff)[PERIOD],
+                                     uint32_t lds, int w) {
+#pragma unroll
+    for (int i = 0; i < COPIES; i += PERIOD) {
+      const int64_t from = first + 4 * i * RPC, n = ((end - 1 - from) * ld + d) * E;
+      const u32x4 rs = uniform_rsrc(static_cast<const char*>(x) + from * ld * E,
+                                    end <= from ? 0u : n > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)n);
+#pragma unroll
+      for (int j = 0; j < PERIOD; ++j) dma16s(rs, voff[j], 0u, lds + (uint32_t)((4 * (i + j) + w) * 1024));
+    }
+  }
+  // rows r0 + (l & 31), elements 16 s + 8 (l / 32) .. + 7
+  __device__ static inline void rows(Frag& a, const unsigned char* t, int r0, int s, int l) {
+    const int r = r0 + (l & 31), up = l >> 5;
+#pragma unroll
+    for (int x = 0; x < F; ++x) a[x] = *reinterpret_cast<const uint4*>(t + r * PITCH + (((F * (2 * s + up) + x) ^ f(r)) << 4));
+  }
+  // columns 32 dt + (l & 31), rows r0 + 8 j + 4 (l / 32) + e for element 4 j + e, j < 2: r0 a multiple of 16
+  __device__ static inline void cols(Frag& a, const unsigned char* t, int r0, int dt, int l) {
+    const int up = l >> 5;
+    if constexpr (E == 2) {
+      const int r = (l & 15) >> 2, c = 4 * dt + 2 * ((l >> 4) & 1) + ((l & 3) >> 1);
+      uint2 v[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = r0 + 8 * j + 4 * up + r;
+        v[j] = read_tr16(t + row * PITCH + ((c ^ f(row)) << 4) + 8 * (l & 1));
+      }
+      a[0] = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
+    } else {
+      uint32_t v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int row = r0 + 8 * (x >> 2) + 4 * up + (x & 3), c = 8 * dt + ((l & 31) >> 2);
+        v[x] = *reinterpret_cast<const uint32_t*>(t + row * PITCH + ((c ^ f(row)) << 4) + 4 * (l & 3));
+      }
+      a[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      a[F - 1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+  }
+  // a 32 x 32 result's rows 16 s + 8 j + 4 (l / 32) + e, as the operand that meets cols()
+  __device__ static inline void pack(Frag& b, const f32x16& x, int s) {
+    if constexpr (E == 2) {
+      b[0] = make_uint4(pack_bf16x2(x[8 * s], x[8 * s + 1]), pack_bf16x2(x[8 * s + 2], x[8 * s + 3]),
+                        pack_bf16x2(x[8 * s + 4], x[8 * s + 5]), pack_bf16x2(x[8 * s + 6], x[8 * s + 7]));
+    } else {
+      b[0] = make_uint4(__float_as_uint(x[8 * s]), __float_as_uint(x[8 * s + 1]), __float_as_uint(x[8 * s + 2]), __float_as_uint(x[8 * s + 3]));
+      b[F - 1] = make_uint4(__float_as_uint(x[8 * s + 4]), __float_as_uint(x[8 * s + 5]), __float_as_uint(x[8 * s + 6]), __float_as_uint(x[8 * s + 7]));
+    }
+  }
+  // the same elements of a row in memory (elements from d on are zeros)
+  __device__ static inline void load(Frag& a, const T* row, int s, int d, int l) {
+    const int c = 16 * s + 8 * (l >> 5);
+#pragma unroll
+    for (int x = 0; x < F; ++x) a[x] = c < d ? *reinterpret_cast<const uint4*>(row + c + x * (16 / E)) : make_uint4(0, 0, 0, 0);
+  }
+
+  // ---- rows that hold a NaN or an infinity ----
+  __device__ static inline bool bad(const uint4& v) {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) any |= E == 2 ? ((x[i] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u : ((x[i] & 0x7fffffffu) + 0x00800000u) & 0x80000000u;
+    return any != 0;
+  }
+  // Bits of the bad rows into words[2] (zero before; a barrier makes them whole)
+  __device__ static inline void find_bad(const unsigned char* t, int tid, uint32_t* words) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 4096; ++i) {
+      const int x = tid + 256 * i;
+      if (bad(*reinterpret_cast<const uint4*>(t + 16 * x))) {
+        const int r = x / CPR;
+        atomicOr(&words[r >> 5], 1u << (r & 31));
+      }
+    }
+  }
+  // zeros in the place of NaNs and infinities
+  __device__ static inline void clean(Frag& a) {
+#pragma unroll
+    for (int x = 0; x < F; ++x) {
+      uint32_t v[4] = {a[x].x, a[x].y, a[x].z, a[x].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (E == 2) v[i] &= ~(((((v[i] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u) >> 15) * 0xffffu);
+        else v[i] = (v[i] & 0x7f800000u) == 0x7f800000u ? 0u : v[i];
+      }
+      a[x] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  // acc += cols(rows r0 .. r0 + 31 of the tile) x: 32 DT elements of the head dimension, 32 columns
+  template <bool CLEAN>
+  __device__ static inline void along(f32x16 (&acc)[DT], const unsigned char* t, int r0, const f32x16& x, int l) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      Frag b;
+      pack(b, x, s);
+#pragma unroll
+      for (int j = 0; j < DT; ++j) {
+        Frag a;
+        cols(a, t, r0 + 16 * s, j, l);
+        if constexpr (CLEAN) clean(a);
+        mma(acc[j], a, b);
+      }
+    }
+  }
+};
+
+// What along<CLEAN> left out: acc += w[r][column] x[r] at the NaNs and infinities of
+// the bad rows r of a block of 32, only where the column sees the row (so that 0
+// times a NaN stays out).  row(r): x's row in memory.  A tile has few such rows, if any.
+template <typename T, int DT, typename Row, typename Seen>
+__device__ inline __attribute__((always_inline)) void add_bad_rows(f32x16 (&acc)[DT], const f32x16& w, uint32_t words, int d, int l, Row row, Seen seen) {
+  for (int x = 0; x < 32; ++x) {
+    if (!((words >> x) & 1)) continue;
+    const int v = 4 * (x >> 3) + (x & 3), half = (x >> 2) & 1;
+    float mine = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mine = i == v ? w[i] : mine;
+    const float weight = __shfl(mine, (l & 31) + 32 * half);
+    const bool on = seen(x);
+    const T* src = row(x);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int e = 32 * dt + 8 * (i >> 2) + 4 * (l >> 5) + (i & 3);
+        const float y = on && e < d ? (float)src[e] : 0.f;
+        if (!__builtin_isfinite(y)) acc[dt][i] += weight * y;
+        asm volatile("" ::: "memory");      // one load at a time: this path must not cost the others registers
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  }
+}
+
+// joined over the two lanes that hold a column's rows
+__device__ inline float swap_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float swap_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The capped score's tanh(x / 2 log2(e) ...): t = tanh(z) from y = 2 log2(e) z.
+// 1 - 2 / (1 + exp(2 z)) is off by up to 2^-24 of 1, which for bf16 inputs is below
+// the score's own rounding; fp32 takes the series where that would cost digits.
+template <typename T>
+__device__ inline float tanh_of(float y) {
+  const float t = fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(y)), 1.0f);
+  if constexpr (sizeof(T) == 2) {
+    return t;
+  } else {
+    const float z = y * (0.5f * kLn2), q = z * z;
+    // z - z^3/3 + 2 z^5/15 - 17 z^7/315 + 62 z^9/2835 - 1382 z^11/155925: within 2^-24 of z below 0.35
+    const float s = z + z * q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1382.f / 155925.f, 62.f / 2835.f), -17.f / 315.f), 2.f / 15.f), -1.f / 3.f);
+    return fabsf(z) < 0.35f ? s : t;
+  }
+}
+
+// asynchronous 4-byte copy of 64 lanes to 256 bytes of LDS
+__device__ inline void dma4s(u32x4 rs, uint32_t voff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" :: "s"(m0), "v"(voff), "s"(rs) : "memory");
+}
+
+// the keys that query t sees, and whether its row is there to be written
+struct Span {
+  int lo, hi;
+  bool live;
+  __device__ static inline Span of(const int4* rows, int causal, int64_t T, int64_t t) {
+    Span s{0, 0, false};
+    if (t >= T) return s;
+    if (rows) {
+      const int2 v = *reinterpret_cast<const int2*>(rows + t);
+      s.live = v.x >= 0;
+      s.lo = max(v.x, 0);
+      s.hi = s.live ? (int)min<int64_t>(max(v.y, 0), T) : 0;
+    } else {
+      s.live = true;
+      s.hi = (int)(causal ? t + 1 : T);
+    }
+    return s;
+  }
+};
+
+}  // namespace attn
+}  // namespace hna

@@ -359,4 +359,44 @@ hipError_t launch_ffn_mm(const FfnMmParams& p, int mode, int bf16, hipStream_t s
 hipError_t launch_ffn_grad(const void* dh, const void* g, const void* u, int64_t rows, int I, int I8, void* dg, void* du, int bf16,
                            hipStream_t st);
 
+// ------------------------------------------------ attention (k_attn*.hip)
+struct AttnParams {
+  const void *q, *k, *v;    // token t's heads at t * ld, d elements each
+  const int4* rows;         // [T] keys [x, y) that query t sees, queries [z, w) that see key t; or NULL
+  const float* slopes;      // [H] or NULL
+  void* a;                  // [T][H][d]
+  float* lse;               // [T][H] or NULL
+  // gradients
+  const void* da;           // [T][H][d]
+  void *dq, *dk, *dv;       // [T][H][d], [T][G][d], or NULL
+  float* stat;              // [2][H][T]: lse in powers of two, then sum_e da a
+  int64_t T, ld_q, ld_k, ld_v;
+  int H, G, d, causal;
+  float scale, cap;         // cap 0: none
+  int8_t head_order[kMaxHeads];        // heads sorted by KV group (stable)
+  int8_t head_group[kMaxHeads];        // group of head h
+  int16_t group_start[kMaxHeads + 1];  // group g owns head_order[group_start[g] .. group_start[g + 1])
+};
+hipError_t launch_attention(const AttnParams& p, int bf16, hipStream_t st);
+hipError_t launch_attention_rows(int64_t T, int docs, const int32_t* start, const int32_t* prefix, int causal, void* rows, hipStream_t st);
+hipError_t launch_attention_backward(const AttnParams& p, int bf16, hipStream_t st);
+
+struct StepParams {
+  const void *q, *k, *v;    // q [B][H][d]; key j of sequence b at b * bs + j * ld, G heads of d elements
+  const int32_t* lengths;   // [B]: keys [start, length) are seen, and length - 1 is the query's place
+  const int32_t* starts;    // [B] or NULL (0)
+  const float* slopes;      // [H] or NULL
+  void* a;                  // [B][H][d]
+  float* lse;               // [B][H] or NULL
+  float* part;              // [B][H][splits][d] sums, and their (reference, total)
+  float2* part_ms;
+  int64_t B, ld_k, ld_v, bs_k, bs_v;
+  int S, H, G, d, splits, column_blocks;   // column_blocks: of 32 heads of the largest group
+  float scale, cap;
+  int8_t head_order[kMaxHeads];
+  int16_t group_start[kMaxHeads + 1];
+};
+int attention_step_splits(int64_t B, int G, int S);
+hipError_t launch_attention_step(const StepParams& p, int bf16, hipStream_t st);
+
 }  // namespace hna

@@ -1,0 +1,267 @@
+// Attention over tokens of several documents in a row:
+//   s_ij = scale q_i . k_j,  capped: s = c tanh(s / c),  biased: s -= slope_h |i - j|
+//   a_i = sum_j exp(s_ij - lse_i) v_j,  lse_i = log sum_j exp(s_ij),
+// j over the keys rows[i] says that query i sees.  One pass over the keys with
+// a running reference m and sum of exp(s - m), in powers of two.
+//
+// A workgroup has 128 queries of a head, 32 a wave, and walks over tiles of 64
+// keys whose copies run one tile ahead.  The products are formed transposed,
+// S^T = K Q^T and O^T = V^T P^T, so that a lane holds one query: the maximum and
+// the sum are in-lane but for one exchange with the lane that has the other half
+// of the keys, rescaling is by a value of the lane's own, and the exponentials go
+// into the second product as they lie (its sum over keys is taken in the order
+// that the first one's result has; V is read along the keys by transposed reads).
+// P is rounded to the inputs' type, as an operand of a product in that type.
+// m moves only where a tile's maximum passes it by 8 powers of two: sums stay in
+// fp32's range, and the accumulators are seldom rescaled.
+#include "hna_internal.h"
+#include "hna_attn.h"
+
+namespace hna {
+namespace {
+
+using namespace attn;
+
+template <typename T, int DT, bool CAP, bool BIAS>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const AttnParams p) {
+  typedef Tile<T, DT> L;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[4 * L::BYTES];   // K, V of two tiles
+  __shared__ int span[4][4];
+  __shared__ uint32_t bad[2];
+  const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // blocks of an XCD are consecutive: the heads of a group next to each other, then
+  // the queries from the last on (the longest rows first), then the groups
+  const int nq = (int)((p.T + 127) / 128), r = p.H / p.G, total = nq * p.H;
+  const int per_xcd = (total + 7) / 8, slot = (int)(blockIdx.x >> 3), n = (int)(blockIdx.x & 7) * per_xcd + slot;
+  if (slot >= per_xcd || n >= total) return;
+  const int gi = n / (nq * r), rem = n - gi * nq * r, qt = nq - 1 - rem / r;
+  const int h = p.head_order[gi * r + rem % r], g = p.head_group[h];
+
+  const int64_t q0 = (int64_t)qt * 128, t = q0 + 32 * w + (l & 31);
+  const Span mine = Span::of(p.rows, p.causal, p.T, t);
+  const int lo = mine.lo, hi = mine.hi;
+  {
+    // the keys that any query of the workgroup sees, and those that all of them see
+    int a = mine.live && lo < hi ? lo : INT32_MAX, b = mine.live && lo < hi ? hi : 0;
+    int c = mine.live ? lo : 0, e = mine.live ? hi : INT32_MAX;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      a = min(a, __shfl_xor(a, o));
+      b = max(b, __shfl_xor(b, o));
+      c = max(c, __shfl_xor(c, o));
+      e = min(e, __shfl_xor(e, o));
+    }
+    if (l == 0) {
+      span[w][0] = a;
+      span[w][1] = b;
+      span[w][2] = c;
+      span[w][3] = e;
+    }
+    if (tid < 2) bad[tid] = 0;
+  }
+  __syncthreads();
+  const int first = __builtin_amdgcn_readfirstlane(min(min(span[0][0], span[1][0]), min(span[2][0], span[3][0])));
+  const int end = __builtin_amdgcn_readfirstlane(max(max(span[0][1], span[1][1]), max(span[2][1], span[3][1])));
+  const int all_lo = __builtin_amdgcn_readfirstlane(max(max(span[0][2], span[1][2]), max(span[2][2], span[3][2])));
+  const int all_hi = __builtin_amdgcn_readfirstlane(min(min(span[0][3], span[1][3]), min(span[2][3], span[3][3])));
+
+  const T* K = static_cast<const T*>(p.k) + (int64_t)g * p.d;
+  const T* V = static_cast<const T*>(p.v) + (int64_t)g * p.d;
+  uint32_t ko[L::PERIOD], vo[L::PERIOD];
+  L::offsets(ko, w, l, p.ld_k, p.d);
+  L::offsets(vo, w, l, p.ld_v, p.d);
+  const uint32_t base = lds_addr(lds);
+  auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
+    L::copy(K, p.ld_k, p.d, kb, end, ko, base + (uint32_t)(buf * 2 * L::BYTES), w);
+    L::copy(V, p.ld_v, p.d, kb, end, vo, base + (uint32_t)(buf * 2 * L::BYTES + L::BYTES), w);
+  };
+
+  typename L::Frag qf[2 * DT];
+  const T* qrow = static_cast<const T*>(p.q) + min<int64_t>(t, p.T - 1) * p.ld_q + (int64_t)h * p.d;
+#pragma unroll
+  for (int s = 0; s < 2 * DT; ++s) L::load(qf[s], qrow, s, p.d, l);
+
+  f32x16 o[DT];
+  float m, sum;
+  const float c1 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+  const float cap = kLog2e * p.cap;
+  const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
+
+  // The walk over the keys.  A value that some queries of a tile do not see must not
+  // reach them as 0 times a NaN: where such a tile holds a NaN or an infinity, the
+  // walk ends (false) and is made again with those elements apart (CAREFUL).
+  auto walk = [&](auto careful) __attribute__((always_inline)) {
+    constexpr bool CAREFUL = decltype(careful)::value;
+    int buf = 0;
+    m = -__builtin_inff();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] = f32x16{};
+    if (first < end) issue(first, 0);
+    for (int kb = first; kb < end; kb += 64, buf ^= 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // this tile's copies
+      __syncthreads();                                        // all waves' copies, and the other tile is read
+      if (kb + 64 < end) issue(kb + 64, buf ^ 1);
+      const unsigned char* kt = lds + buf * 2 * L::BYTES;
+      const unsigned char* vt = lds + buf * 2 * L::BYTES + L::BYTES;
+      uint32_t bad0 = 0, bad1 = 0;
+      if (kb < all_lo || kb + 64 > all_hi) {
+        L::find_bad(vt, tid, bad);
+        __syncthreads();
+        bad0 = __builtin_amdgcn_readfirstlane(bad[0]);
+        bad1 = __builtin_amdgcn_readfirstlane(bad[1]);
+        if (bad0 | bad1) {
+          __syncthreads();
+          if (tid < 2) bad[tid] = 0;
+          if constexpr (!CAREFUL) return false;
+        }
+      }
+      if (!__any(mine.live && lo < kb + 64 && hi > kb)) continue;
+
+      f32x16 s[2];
+      s[0] = s[1] = f32x16{};
+#pragma unroll
+      for (int x = 0; x < 2 * DT; ++x)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          typename L::Frag a;
+          L::rows(a, kt, 32 * i, x, l);
+          mma(s[i], a, qf[x]);
+        }
+      // scores in powers of two
+      if constexpr (CAP || BIAS) {
+        const float at = (float)((int)t - kb - 4 * up);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            float x = s[i][v] * c1;
+            if constexpr (CAP) x = cap * tanh_of<T>(x);
+            if constexpr (BIAS) x = fmaf(-slope, fabsf(at - (float)(32 * i + 8 * (v >> 2) + (v & 3))), x);
+            s[i][v] = x;
+          }
+      }
+      if (!__all(!mine.live || (lo <= kb && hi >= kb + 64))) {
+        const uint32_t from = (uint32_t)(lo - kb - 4 * up), len = (uint32_t)max(hi - lo, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v)
+            s[i][v] = (uint32_t)(32 * i + 8 * (v >> 2) + (v & 3)) - from < len ? s[i][v] : -__builtin_inff();
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) top = fmaxf(top, s[i][v]);
+      top = swap_max(top);
+      if constexpr (!(CAP || BIAS)) top *= c1;                // scale > 0
+      if (__any(top > m + 8.f)) {
+        const float to = top > m + 8.f ? top : m;
+        const float f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        sum *= f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) o[i][v] *= f;
+      }
+      const float ref = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          s[i][v] = __builtin_amdgcn_exp2f(CAP || BIAS ? s[i][v] - ref : fmaf(s[i][v], c1, -ref));
+          sum += s[i][v];
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        L::template along<CAREFUL>(o, vt, 32 * i, s[i], l);
+        if constexpr (CAREFUL)
+          add_bad_rows<T, DT>(o, s[i], i ? bad1 : bad0, p.d, l, [&](int x) { return V + (int64_t)(kb + 32 * i + x) * p.ld_v; },
+                              [&](int x) { return kb + 32 * i + x >= lo && kb + 32 * i + x < hi; });
+      }
+    }
+    return true;
+  };
+  if (!walk(std::false_type{})) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // the next tile's copies
+    __syncthreads();
+    walk(std::true_type{});
+  }
+
+  sum = swap_sum(sum);
+  if (!mine.live) return;
+  if (p.lse && up == 0) p.lse[t * p.H + h] = sum == 0.f ? -__builtin_inff() : kLn2 * (m + __builtin_amdgcn_logf(sum));
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  T* out = static_cast<T*>(p.a) + (t * p.H + h) * p.d;
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int e = 32 * i + 8 * a + 4 * up;
+      if (e < p.d)
+        *reinterpret_cast<typename Four<T>::type*>(out + e) = Four<T>::of(o[i][4 * a] * inv, o[i][4 * a + 1] * inv, o[i][4 * a + 2] * inv, o[i][4 * a + 3] * inv);
+    }
+}
+
+// rows[t]: the document of t by bisection of its starts, then the interval of keys
+// that its query sees and of queries that see its key
+__global__ __launch_bounds__(256) void attn_rows_kernel(int T, int docs, const int* start, const int* prefix, int causal, int4* rows) {
+  const int t = (int)(blockIdx.x * 256 + threadIdx.x);
+  if (t >= T) return;
+  // the last document that starts at or before t (documents of no tokens share a start)
+  int a = 0, b = docs;                                      // start[a] <= t < start[b], if t has a document
+  while (b - a > 1) {
+    const int c = (a + b) >> 1;
+    if (start[c] <= t) a = c;
+    else b = c;
+  }
+  const int s = max(start[a], 0), e = min(start[a + 1], T);
+  int4 v = make_int4(-1, -1, -1, -1);
+  if (t >= s && t < e) {
+    v = make_int4(s, e, s, e);
+    if (causal) {
+      const int known = s + (prefix ? min(max(prefix[a], 0), e - s) : 0);
+      v.y = max(t + 1, known);
+      v.z = t < known ? s : t;
+    }
+  }
+  rows[t] = v;
+}
+
+template <typename T, int DT, bool CAP, bool BIAS>
+hipError_t launch_one(const AttnParams& p, hipStream_t st) {
+  const int64_t total = (p.T + 127) / 128 * p.H;
+  hipLaunchKernelGGL((attn_kernel<T, DT, CAP, BIAS>), dim3((unsigned)(8 * ((total + 7) / 8))), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+template <typename T, int DT>
+hipError_t launch_dt(const AttnParams& p, hipStream_t st) {
+  if (p.cap > 0.f) return p.slopes ? launch_one<T, DT, true, true>(p, st) : launch_one<T, DT, true, false>(p, st);
+  return p.slopes ? launch_one<T, DT, false, true>(p, st) : launch_one<T, DT, false, false>(p, st);
+}
+template <typename T>
+hipError_t launch_t(const AttnParams& p, hipStream_t st) {
+  if (p.d <= 32) return launch_dt<T, 1>(p, st);
+  if (p.d <= 64) return launch_dt<T, 2>(p, st);
+  if (p.d <= 96) return launch_dt<T, 3>(p, st);
+  return launch_dt<T, 4>(p, st);
+}
+
+}  // namespace
+
+hipError_t launch_attention(const AttnParams& p, int bf16, hipStream_t st) {
+  if (p.T == 0) return hipSuccess;
+  return bf16 ? launch_t<__bf16>(p, st) : launch_t<float>(p, st);
+}
+
+hipError_t launch_attention_rows(int64_t T, int docs, const int32_t* start, const int32_t* prefix, int causal, void* rows, hipStream_t st) {
+  if (T == 0) return hipSuccess;
+  hipLaunchKernelGGL(attn_rows_kernel, dim3((unsigned)((T + 255) / 256)), dim3(256), 0, st, (int)T, docs, start, prefix, causal, static_cast<int4*>(rows));
+  return hipGetLastError();
+}
+
+}  // namespace hna

@@ -1,0 +1,231 @@
+// Attention of one new token per sequence over a cache of keys and values: the
+// query is the last key's, and sees keys [start, length) of its sequence.
+//   s_j = scale q . k_j, capped and biased by its distance to the last key as in
+//   k_attn.hip;  a = sum_j exp(s_j - lse) v_j
+// Bound by the cache's bytes.  A workgroup has one group of one sequence (the up to
+// 32 heads that read the same keys are the columns of its products) and a part of
+// the keys; each wave walks over 32 keys at a time in two stages of its own, with
+// no barrier, so that a CU has 64 KB and more of copies in flight.  The waves'
+// sums meet in LDS and, where the keys are split among workgroups too (few
+// sequences), a second kernel joins the parts in order.
+#include <algorithm>
+
+#include "hna_internal.h"
+#include "hna_attn.h"
+
+namespace hna {
+namespace {
+
+using namespace attn;
+
+template <typename T, int DT> constexpr int kStepWaves = Tile<T, DT>::BYTES * 8 <= 128 * 1024 ? 4 : 2;
+
+template <typename T, int DT, bool CAP, bool BIAS>
+__global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(const StepParams p) {
+  typedef Tile<T, DT> L;
+  constexpr int NW = kStepWaves<T, DT>, HALF = L::BYTES / 2, REGION = 4 * HALF;   // K, V of 32 keys, two stages
+  constexpr int CP = HALF / 1024, PERIOD = 16 / L::RPC > 1 ? 16 / L::RPC : 1;
+  constexpr int OP = 32 * DT + 4;                           // floats of a column of sums
+  static_assert(32 * OP * 4 <= REGION, "the sums fit a wave's stages");
+  __shared__ __attribute__((aligned(16))) unsigned char lds[NW * REGION];
+  __shared__ float ms[2][NW][32];
+  const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // the parts of a sequence's group are next to each other, then the groups' columns, groups and sequences
+  const int64_t n = blockIdx.x;
+  const int part = (int)(n % p.splits);
+  const int cb = (int)(n / p.splits % p.column_blocks), g = (int)(n / p.splits / p.column_blocks % p.G);
+  const int64_t b = n / p.splits / p.column_blocks / p.G;
+  const int heads0 = p.group_start[g] + 32 * cb, heads = min(32, p.group_start[g + 1] - heads0);
+  if (heads <= 0) return;
+
+  const int length = min(max(p.lengths[b], 0), p.S), start = p.starts ? min(max(p.starts[b], 0), length) : 0;
+  const int per = ((length - start + p.splits - 1) / p.splits + 31) & ~31;
+  const int first = __builtin_amdgcn_readfirstlane((int)min<int64_t>(start + (int64_t)part * per, length));
+  const int end = __builtin_amdgcn_readfirstlane((int)min<int64_t>(first + (int64_t)per, length));
+
+  const T* K = static_cast<const T*>(p.k) + b * p.bs_k + (int64_t)g * p.d;
+  const T* V = static_cast<const T*>(p.v) + b * p.bs_v + (int64_t)g * p.d;
+  // copy i of 32 rows: rows RPC i .., f repeats every 16 rows
+  uint32_t ko[PERIOD], vo[PERIOD];
+#pragma unroll
+  for (int i = 0; i < PERIOD; ++i) {
+    const int r = i * L::RPC + l / L::CPR, c = (l % L::CPR) ^ L::f(r);
+    const bool on = 16 * c < p.d * L::E;
+    ko[i] = on ? (uint32_t)(r * p.ld_k * L::E) + 16u * (uint32_t)c : kOutOfRange;
+    vo[i] = on ? (uint32_t)(r * p.ld_v * L::E) + 16u * (uint32_t)c : kOutOfRange;
+  }
+  const uint32_t base = lds_addr(lds) + (uint32_t)(w * REGION);
+  auto one = [&](const T* x, int64_t ld, const uint32_t (&voff)[PERIOD], int kb, uint32_t to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < CP; i += PERIOD) {
+      const int64_t from = kb + i * L::RPC, bytes = ((end - 1 - from) * ld + p.d) * L::E;
+      const u32x4 rs = uniform_rsrc(x + (end > from ? from * ld : 0), end <= from ? 0u : bytes > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)bytes);
+#pragma unroll
+      for (int j = 0; j < PERIOD; ++j) dma16s(rs, voff[j], 0u, to + (uint32_t)((i + j) * 1024));
+    }
+  };
+  auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
+    one(K, p.ld_k, ko, kb, base + (uint32_t)(buf * 2 * HALF));
+    one(V, p.ld_v, vo, kb, base + (uint32_t)(buf * 2 * HALF + HALF));
+  };
+  const int mine = first + 32 * w;
+  issue(mine, 0);
+  issue(mine + 32 * NW, 1);
+
+  const int col = l & 31;
+  const int h = p.head_order[heads0 + min(col, heads - 1)];
+  typename L::Frag qf[2 * DT];
+  const T* qrow = static_cast<const T*>(p.q) + (b * p.H + h) * p.d;
+#pragma unroll
+  for (int s = 0; s < 2 * DT; ++s) L::load(qf[s], qrow, s, p.d, l);
+  const float c1 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+  const float cap = kLog2e * p.cap;
+  const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i) o[i] = f32x16{};
+  float m = -__builtin_inff(), sum = 0.f;
+  int buf = 0;
+  for (int kb = mine; kb < end; kb += 32 * NW, buf ^= 1) {
+    // this stage's copies; the other's (as many, zeros past the end) may be in flight
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * CP) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const unsigned char* kt = lds + w * REGION + buf * 2 * HALF;
+    const unsigned char* vt = kt + HALF;
+    f32x16 s = {};
+#pragma unroll
+    for (int x = 0; x < 2 * DT; ++x) {
+      typename L::Frag a;
+      L::rows(a, kt, 0, x, l);
+      mma(s, a, qf[x]);
+    }
+    const float at = (float)(length - 1 - kb - 4 * up);
+    const int left = end - kb - 4 * up;
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int off = 8 * (v >> 2) + (v & 3);
+      float x = s[v] * c1;
+      if constexpr (CAP) x = cap * tanh_of<T>(x);
+      if constexpr (BIAS) x = fmaf(-slope, at - (float)off, x);
+      x = off < left ? x : -__builtin_inff();
+      s[v] = x;
+      top = fmaxf(top, x);
+    }
+    top = swap_max(top);
+    if (__any(top > m + 8.f)) {
+      const float to = top > m + 8.f ? top : m;
+      const float f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      sum *= f;
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) o[i][v] *= f;
+    }
+    const float ref = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      s[v] = __builtin_amdgcn_exp2f(s[v] - ref);
+      sum += s[v];
+    }
+    L::template along<false>(o, vt, 0, s, l);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the stage is read
+    __builtin_amdgcn_sched_barrier(0);
+    issue(kb + 64 * NW, buf);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // the last copies (zeros) are in
+  sum = swap_sum(sum);
+  float* mine_o = reinterpret_cast<float*>(lds + w * REGION);
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      *reinterpret_cast<float4*>(mine_o + col * OP + 32 * i + 8 * a + 4 * up) = make_float4(o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]);
+  if (up == 0) {
+    ms[0][w][col] = m;
+    ms[1][w][col] = sum;
+  }
+  __syncthreads();
+  for (int x = tid; x < heads * p.d; x += 64 * NW) {
+    const int c = x / p.d, e = x - c * p.d, hc = p.head_order[heads0 + c];
+    float M = ms[0][0][c];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) M = fmaxf(M, ms[0][i][c]);
+    const float ref = M == -__builtin_inff() ? 0.f : M;
+    float total = 0.f, y = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const float f = __builtin_amdgcn_exp2f(ms[0][i][c] - ref);
+      total = fmaf(f, ms[1][i][c], total);
+      y = fmaf(f, reinterpret_cast<const float*>(lds + i * REGION)[c * OP + e], y);
+    }
+    const int64_t row = b * p.H + hc;
+    if (p.splits == 1) {
+      static_cast<T*>(p.a)[row * p.d + e] = to_type<T>(total == 0.f ? 0.f : y / total);
+      if (e == 0 && p.lse) p.lse[row] = total == 0.f ? -__builtin_inff() : kLn2 * (M + __builtin_amdgcn_logf(total));
+    } else {
+      p.part[(row * p.splits + part) * p.d + e] = y;
+      if (e == 0) p.part_ms[row * p.splits + part] = make_float2(M, total);
+    }
+  }
+}
+
+// the parts of a row joined: a workgroup a row (sequence and head)
+template <typename T>
+__global__ __launch_bounds__(128) void attn_join_kernel(const StepParams p) {
+  const int64_t row = blockIdx.x;
+  const float2* ms = p.part_ms + row * p.splits;
+  float M = -__builtin_inff();
+  for (int i = 0; i < p.splits; ++i) M = fmaxf(M, ms[i].x);
+  const float ref = M == -__builtin_inff() ? 0.f : M;
+  const int e = threadIdx.x;
+  float total = 0.f, y = 0.f;
+  for (int i = 0; i < p.splits; ++i) {
+    const float2 v = ms[i];
+    const float f = __builtin_amdgcn_exp2f(v.x - ref);
+    total = fmaf(f, v.y, total);
+    if (e < p.d) y = fmaf(f, p.part[(row * p.splits + i) * p.d + e], y);
+  }
+  if (e < p.d) static_cast<T*>(p.a)[row * p.d + e] = to_type<T>(total == 0.f ? 0.f : y / total);
+  if (e == 0 && p.lse) p.lse[row] = total == 0.f ? -__builtin_inff() : kLn2 * (M + __builtin_amdgcn_logf(total));
+}
+
+template <typename T, int DT, bool CAP, bool BIAS>
+hipError_t launch_one(const StepParams& p, hipStream_t st) {
+  const int64_t grid = p.B * p.G * p.column_blocks * p.splits;
+  hipLaunchKernelGGL((attn_step_kernel<T, DT, CAP, BIAS>), dim3((unsigned)grid), dim3(64 * kStepWaves<T, DT>), 0, st, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(attn_join_kernel<T>, dim3((unsigned)(p.B * p.H)), dim3(128), 0, st, p);
+  return hipGetLastError();
+}
+template <typename T, int DT>
+hipError_t launch_dt(const StepParams& p, hipStream_t st) {
+  if (p.cap > 0.f) return p.slopes ? launch_one<T, DT, true, true>(p, st) : launch_one<T, DT, true, false>(p, st);
+  return p.slopes ? launch_one<T, DT, false, true>(p, st) : launch_one<T, DT, false, false>(p, st);
+}
+template <typename T>
+hipError_t launch_t(const StepParams& p, hipStream_t st) {
+  if (p.d <= 32) return launch_dt<T, 1>(p, st);
+  if (p.d <= 64) return launch_dt<T, 2>(p, st);
+  if (p.d <= 96) return launch_dt<T, 3>(p, st);
+  return launch_dt<T, 4>(p, st);
+}
+
+}  // namespace
+
+int attention_step_splits(int64_t B, int G, int S) {
+  const int64_t rows = std::max<int64_t>(B * G, 1);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(1024 + rows - 1) / rows, ((int64_t)S + 127) / 128, 64}));
+}
+
+hipError_t launch_attention_step(const StepParams& p, int bf16, hipStream_t st) {
+  if (p.B == 0) return hipSuccess;
+  return bf16 ? launch_t<__bf16>(p, st) : launch_t<float>(p, st);
+}
+
+}  // namespace hna

@@ -554,6 +554,97 @@ int hna_gated_ffn_backward(const hna_ffn_dims* dims, const void* dh, const void*
                            void* dn, void* dW_gate, void* dW_up, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------ attention */
+
+/*
+ * Attention of tokens in a row, which may be those of several documents: what a
+ * calibration forward runs to give the pass its a [T, H, d], its gradients, and
+ * one new token per sequence over a cache.  Head h reads the keys and values of
+ * group g = group_of_head[h]:
+ *   s_ij = scale q_i . k_j;  with a cap c > 0: s = c tanh(s / c);
+ *   with slopes: s -= slopes[h] |i - j|
+ *   lse_i = log sum_j exp(s_ij),  a_i = sum_j exp(s_ij - lse_i) v_j
+ * over the keys j that query i sees.  A query that sees no key has a = 0 and
+ * lse = -inf, and gradients of 0.
+ *
+ * rows int32 [T, 4], device memory, 16 bytes a token, says who sees whom: query t
+ * sees keys rows[t][0] <= j < rows[t][1], and key t is seen by queries within
+ * rows[t][2] <= i < rows[t][3] (the gradients of k and v look at no others; the
+ * first pair decides which of these see it).  rows[t][0] < 0: token t belongs to no
+ * document; its rows of a, lse, dq, dk and dv are left as they are, and no other
+ * token may see it.  Ends past T count as T.  rows is made once for a batch, by
+ * hna_attention_rows or by the caller; NULL: one document, dims' causal says
+ * whether query i sees keys up to i or all.
+ *
+ * q [T, H, d], k, v [T, G, d] with the heads of a token next to each other and
+ * tokens ld_q, ld_k, ld_v elements apart (parts of one projection's output, say);
+ * a, da, dq [T, H, d] and dk, dv [T, G, d] are contiguous, lse [T, H] and slopes
+ * [H] fp32.  Sums, maxima and lse are fp32; exp(s - m) (m a running reference),
+ * and in the gradients p and ds, are rounded to dtype as operands of products.
+ *   H, G, d, group_of_head   as for the pass (head dims 16, 32 .. 128)
+ *   ld_*         multiples of 8, at least H d (q) or G d (k, v), at most 2^20
+ *   T H          at most 2^30
+ *   scale        finite and > 0;  cap  finite, 0 for none
+ * A NaN or an infinity in a key or value (in the gradients: in any row) reaches
+ * only the tokens that see it or are seen by it.  Slopes are constants: no
+ * gradient of theirs is formed.  Outputs overlap neither each other nor inputs.
+ */
+typedef struct hna_attn_dims {
+  int64_t T;
+  int64_t ld_q, ld_k, ld_v;
+  int32_t H, G, d, dtype;
+  int32_t causal;            /* without rows */
+  float scale, cap;
+} hna_attn_dims;
+
+/* rows of T tokens in n_docs documents: document i is tokens doc_start[i] ..
+ * doc_start[i + 1] - 1 (doc_start [n_docs + 1], non-decreasing, int32 device
+ * memory; documents may be empty, tokens outside all of them belong to none).
+ * causal: a query sees its document's keys up to its own, and the document's first
+ * prefix[i] tokens (prefix [n_docs] or NULL); else all of its document. */
+int hna_attention_rows(int64_t T, int32_t n_docs, const int32_t* doc_start, const int32_t* prefix,
+                       int32_t causal, int32_t* rows, void* stream);
+
+/* a, and lse unless NULL (the gradients need it) */
+int hna_attention(const hna_attn_dims* dims, const void* q, const void* k, const void* v,
+                  const int32_t* rows, const float* slopes, const int32_t* group_of_head, void* a,
+                  float* lse, void* stream);
+
+/* Bytes of workspace hna_attention_backward needs (0 for invalid dims). */
+size_t hna_attention_workspace_bytes(const hna_attn_dims* dims);
+
+/* dq, dk, dv from da, at the a and lse that hna_attention wrote; summed over the
+ * heads of a group and over tokens in a fixed order: no atomics. */
+int hna_attention_backward(const hna_attn_dims* dims, const void* da, const void* q, const void* k,
+                           const void* v, const void* a, const float* lse, const int32_t* rows,
+                           const float* slopes, const int32_t* group_of_head, void* dq, void* dk,
+                           void* dv, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One new token for each of B sequences over a cache: the query stands at
+ * lengths[b] - 1, the place of its own key (already written), and sees keys
+ * starts[b] <= j < lengths[b] (starts NULL: from 0).  lengths, starts int32 [B]
+ * device memory; they count as clamped to 0 .. S and 0 .. length.
+ *   q, a [B, H, d]; lse [B, H] or NULL
+ *   k, v  key j of sequence b at b bs + j ld elements, G heads of d there; S keys
+ *         a sequence; ld_k, ld_v as above, bs_k, bs_v multiples of 8
+ *   B H at most 2^22, S at most 2^30
+ * What the cache holds outside a sequence's keys is not read into any result.
+ */
+typedef struct hna_step_dims {
+  int64_t B;
+  int64_t ld_k, ld_v, bs_k, bs_v;
+  int32_t S, H, G, d, dtype;
+  float scale, cap;
+} hna_step_dims;
+
+/* Bytes of workspace hna_attention_step needs (0 for invalid dims). */
+size_t hna_attention_step_workspace_bytes(const hna_step_dims* dims);
+int hna_attention_step(const hna_step_dims* dims, const void* q, const void* k, const void* v,
+                       const int32_t* lengths, const int32_t* starts, const float* slopes,
+                       const int32_t* group_of_head, void* a, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /*
