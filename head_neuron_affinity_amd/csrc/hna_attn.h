@@ -52,30 +52,57 @@ struct Tile {
       for (int j = 0; j < PERIOD; ++j) dma16s(rs, voff[j], 0u, lds + (uint32_t)((4 * (i + j) + w) * 1024));
     }
   }
-  // rows r0 + (l & 31), elements 16 s + 8 (l / 32) .. + 7
-  __device__ static inline void rows(Frag& a, const unsigned char* t, int r0, int s, int l) {
-    const int r = r0 + (l & 31), up = l >> 5;
+  // A lane's addresses in a tile at LDS address `at` (a multiple of 512): of row
+  // l & 31's elements 8 (l / 32) .., and (bf16) of the transposed reads of rows 8 j + 4 (l / 32) + ..
+  struct At {
+    uint32_t row[F], col[2];
+  };
+  __device__ static inline At lane(uint32_t at, int l) {
+    const int up = l >> 5, r = (l & 15) >> 2, b = 2 * ((l >> 4) & 1) + ((l & 3) >> 1);
+    At x;
 #pragma unroll
-    for (int x = 0; x < F; ++x) a[x] = *reinterpret_cast<const uint4*>(t + r * PITCH + (((F * (2 * s + up) + x) ^ f(r)) << 4));
+    for (int i = 0; i < F; ++i) x.row[i] = at + (uint32_t)((l & 31) * PITCH + (((F * up + i) ^ f(l & 31)) << 4));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = 8 * j + 4 * up + r;
+      x.col[j] = E == 2 ? at + (uint32_t)(row * PITCH + ((b ^ f(row)) << 4) + 8 * (l & 1)) : at;
+    }
+    return x;
+  }
+  __device__ static inline At move(At x, uint32_t by) {
+#pragma unroll
+    for (int i = 0; i < F; ++i) x.row[i] += by;
+    x.col[0] += by;
+    x.col[1] += by;
+    return x;
+  }
+  template <typename V>
+  __device__ static inline V read(uint32_t at) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) V*>(at);
+  }
+  // rows r0 + (l & 31), elements 16 s + 8 (l / 32) .. + 7: r0 a multiple of 32
+  __device__ static inline void rows(Frag& a, const At& t, int r0, int s) {
+#pragma unroll
+    for (int x = 0; x < F; ++x) {
+      const u32x4 v = read<u32x4>((t.row[x] ^ (uint32_t)(32 * F * s)) + (uint32_t)(r0 * PITCH));
+      a[x] = make_uint4(v.x, v.y, v.z, v.w);
+    }
   }
   // columns 32 dt + (l & 31), rows r0 + 8 j + 4 (l / 32) + e for element 4 j + e, j < 2: r0 a multiple of 16
-  __device__ static inline void cols(Frag& a, const unsigned char* t, int r0, int dt, int l) {
-    const int up = l >> 5;
+  __device__ static inline void cols(Frag& a, const At& t, int r0, int dt, int l) {
     if constexpr (E == 2) {
-      const int r = (l & 15) >> 2, c = 4 * dt + 2 * ((l >> 4) & 1) + ((l & 3) >> 1);
       uint2 v[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = r0 + 8 * j + 4 * up + r;
-        v[j] = read_tr16(t + row * PITCH + ((c ^ f(row)) << 4) + 8 * (l & 1));
-      }
+      for (int j = 0; j < 2; ++j)
+        v[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                             (lds_s16x4)((t.col[j] ^ (uint32_t)(64 * dt)) + (uint32_t)(r0 * PITCH))));
       a[0] = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
     } else {
       uint32_t v[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        const int row = r0 + 8 * (x >> 2) + 4 * up + (x & 3), c = 8 * dt + ((l & 31) >> 2);
-        v[x] = *reinterpret_cast<const uint32_t*>(t + row * PITCH + ((c ^ f(row)) << 4) + 4 * (l & 3));
+        const int row = r0 + 8 * (x >> 2) + 4 * (l >> 5) + (x & 3), c = 8 * dt + ((l & 31) >> 2);
+        v[x] = read<uint32_t>(t.col[0] + (uint32_t)(row * PITCH + ((c ^ f(row)) << 4) + 4 * (l & 3)));
       }
       a[0] = make_uint4(v[0], v[1], v[2], v[3]);
       a[F - 1] = make_uint4(v[4], v[5], v[6], v[7]);
@@ -106,11 +133,9 @@ struct Tile {
     for (int i = 0; i < 4; ++i) any |= E == 2 ? ((x[i] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u : ((x[i] & 0x7fffffffu) + 0x00800000u) & 0x80000000u;
     return any != 0;
   }
-  // Bits of the bad rows into words[2] (zero before; a barrier makes them whole)
-  __device__ static inline void find_bad(const unsigned char* t, int tid, uint32_t* words) {
-#pragma unroll
-    for (int i = 0; i < BYTES / 4096; ++i) {
-      const int x = tid + 256 * i;
+  // bits of the bad rows into words[2] (zero before; a barrier makes them whole), by n threads
+  __device__ static inline void find_bad(const unsigned char* t, int tid, int n, uint32_t* words) {
+    for (int x = tid; x < BYTES / 16; x += n) {
       if (bad(*reinterpret_cast<const uint4*>(t + 16 * x))) {
         const int r = x / CPR;
         atomicOr(&words[r >> 5], 1u << (r & 31));
@@ -132,7 +157,7 @@ struct Tile {
   }
   // acc += cols(rows r0 .. r0 + 31 of the tile) x: 32 DT elements of the head dimension, 32 columns
   template <bool CLEAN>
-  __device__ static inline void along(f32x16 (&acc)[DT], const unsigned char* t, int r0, const f32x16& x, int l) {
+  __device__ static inline void along(f32x16 (&acc)[DT], const At& t, int r0, const f32x16& x, int l) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       Frag b;
@@ -174,6 +199,28 @@ __device__ inline __attribute__((always_inline)) void add_bad_rows(f32x16 (&acc)
       }
   }
 }
+
+// not a number if any of the sums is not finite: a sum that met 0 times a NaN or an
+// infinity, or one that is so by right
+template <int DT>
+__device__ inline float finite(const f32x16 (&acc)[DT]) {
+  float z = 0.f;
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) z = fmaf(acc[i][v], 0.f, z);
+  return z;
+}
+
+// minimum and maximum over the wave (lanes 32 apart hold the same)
+__device__ inline int wave_min(int x) {
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x121, 0xf, 0xf, false));   // rows of 16 lanes rotated by 1, 2, 4, 8
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x122, 0xf, 0xf, false));
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x124, 0xf, 0xf, false));
+  x = min(x, __builtin_amdgcn_update_dpp(x, x, 0x128, 0xf, 0xf, false));
+  return min(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16));
+}
+__device__ inline int wave_max(int x) { return ~wave_min(~x); }
 
 // joined over the two lanes that hold a column's rows
 __device__ inline float swap_max(float x) {

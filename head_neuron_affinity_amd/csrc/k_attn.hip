@@ -25,9 +25,9 @@ using namespace attn;
 template <typename T, int DT, bool CAP, bool BIAS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const AttnParams p) {
   typedef Tile<T, DT> L;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[4 * L::BYTES];   // K, V of two tiles
-  __shared__ int span[4][4];
-  __shared__ uint32_t bad[2];
+  __shared__ __attribute__((aligned(512))) unsigned char lds[4 * L::BYTES];   // K, V of two tiles
+  __shared__ int span[4][2];
+  __shared__ uint32_t bad[2], again;
   const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -43,29 +43,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
   const Span mine = Span::of(p.rows, p.causal, p.T, t);
   const int lo = mine.lo, hi = mine.hi;
   {
-    // the keys that any query of the workgroup sees, and those that all of them see
-    int a = mine.live && lo < hi ? lo : INT32_MAX, b = mine.live && lo < hi ? hi : 0;
-    int c = mine.live ? lo : 0, e = mine.live ? hi : INT32_MAX;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      a = min(a, __shfl_xor(a, o));
-      b = max(b, __shfl_xor(b, o));
-      c = max(c, __shfl_xor(c, o));
-      e = min(e, __shfl_xor(e, o));
-    }
+    // the keys that any query of the workgroup sees
+    const bool on = mine.live && lo < hi;
+    const int a = wave_min(on ? lo : INT32_MAX), b = wave_max(on ? hi : 0);
     if (l == 0) {
       span[w][0] = a;
       span[w][1] = b;
-      span[w][2] = c;
-      span[w][3] = e;
     }
     if (tid < 2) bad[tid] = 0;
+    if (tid == 0) again = 0;
   }
   __syncthreads();
   const int first = __builtin_amdgcn_readfirstlane(min(min(span[0][0], span[1][0]), min(span[2][0], span[3][0])));
   const int end = __builtin_amdgcn_readfirstlane(max(max(span[0][1], span[1][1]), max(span[2][1], span[3][1])));
-  const int all_lo = __builtin_amdgcn_readfirstlane(max(max(span[0][2], span[1][2]), max(span[2][2], span[3][2])));
-  const int all_hi = __builtin_amdgcn_readfirstlane(min(min(span[0][3], span[1][3]), min(span[2][3], span[3][3])));
 
   const T* K = static_cast<const T*>(p.k) + (int64_t)g * p.d;
   const T* V = static_cast<const T*>(p.v) + (int64_t)g * p.d;
@@ -73,6 +63,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
   L::offsets(ko, w, l, p.ld_k, p.d);
   L::offsets(vo, w, l, p.ld_v, p.d);
   const uint32_t base = lds_addr(lds);
+  const typename L::At lane0 = L::lane(base, l);
   auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
     L::copy(K, p.ld_k, p.d, kb, end, ko, base + (uint32_t)(buf * 2 * L::BYTES), w);
     L::copy(V, p.ld_v, p.d, kb, end, vo, base + (uint32_t)(buf * 2 * L::BYTES + L::BYTES), w);
@@ -89,9 +80,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
   const float cap = kLog2e * p.cap;
   const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
 
-  // The walk over the keys.  A value that some queries of a tile do not see must not
-  // reach them as 0 times a NaN: where such a tile holds a NaN or an infinity, the
-  // walk ends (false) and is made again with those elements apart (CAREFUL).
+  // The walk over the keys.  A value that a query does not see must not reach it as 0
+  // times a NaN: where a sum is not finite at the end, the walk is made again with
+  // the values' NaNs and infinities apart (CAREFUL).
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
     int buf = 0;
@@ -104,19 +95,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // this tile's copies
       __syncthreads();                                        // all waves' copies, and the other tile is read
       if (kb + 64 < end) issue(kb + 64, buf ^ 1);
-      const unsigned char* kt = lds + buf * 2 * L::BYTES;
-      const unsigned char* vt = lds + buf * 2 * L::BYTES + L::BYTES;
+      const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), vt = L::move(kt, L::BYTES);
       uint32_t bad0 = 0, bad1 = 0;
-      if (kb < all_lo || kb + 64 > all_hi) {
-        L::find_bad(vt, tid, bad);
+      if constexpr (CAREFUL) {
+        L::find_bad(lds + buf * 2 * L::BYTES + L::BYTES, tid, 256, bad);
         __syncthreads();
         bad0 = __builtin_amdgcn_readfirstlane(bad[0]);
         bad1 = __builtin_amdgcn_readfirstlane(bad[1]);
-        if (bad0 | bad1) {
-          __syncthreads();
-          if (tid < 2) bad[tid] = 0;
-          if constexpr (!CAREFUL) return false;
-        }
+        __syncthreads();
+        if (tid < 2) bad[tid] = 0;
       }
       if (!__any(mine.live && lo < kb + 64 && hi > kb)) continue;
 
@@ -127,7 +114,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           typename L::Frag a;
-          L::rows(a, kt, 32 * i, x, l);
+          L::rows(a, kt, 32 * i, x);
           mma(s[i], a, qf[x]);
         }
       // scores in powers of two
@@ -184,13 +171,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
                               [&](int x) { return kb + 32 * i + x >= lo && kb + 32 * i + x < hi; });
       }
     }
-    return true;
   };
-  if (!walk(std::false_type{})) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // the next tile's copies
-    __syncthreads();
-    walk(std::true_type{});
-  }
+  walk(std::false_type{});
+  const float z = finite<DT>(o);
+  if (__any(mine.live && z != z)) again = 1;
+  __syncthreads();
+  if (again) walk(std::true_type{});
 
   sum = swap_sum(sum);
   if (!mine.live) return;

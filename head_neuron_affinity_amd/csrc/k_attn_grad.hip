@@ -33,9 +33,9 @@ __device__ inline float score(float x, float c1, float cap, float slope, float d
 template <typename T, int DT, bool CAP, bool BIAS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(const AttnParams p) {
   typedef Tile<T, DT> L;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[4 * L::BYTES];   // K, V of two tiles
-  __shared__ int span[4][4];
-  __shared__ uint32_t bad[2];
+  __shared__ __attribute__((aligned(512))) unsigned char lds[4 * L::BYTES];   // K, V of two tiles
+  __shared__ int span[4][2];
+  __shared__ uint32_t bad[2], again;
   const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -50,28 +50,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   const Span mine = Span::of(p.rows, p.causal, p.T, t);
   const int lo = mine.lo, hi = mine.hi;
   {
-    int a = mine.live && lo < hi ? lo : INT32_MAX, b = mine.live && lo < hi ? hi : 0;
-    int c = mine.live ? lo : 0, e = mine.live ? hi : INT32_MAX;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      a = min(a, __shfl_xor(a, o));
-      b = max(b, __shfl_xor(b, o));
-      c = max(c, __shfl_xor(c, o));
-      e = min(e, __shfl_xor(e, o));
-    }
+    // the keys that any query of the workgroup sees
+    const bool on = mine.live && lo < hi;
+    const int a = wave_min(on ? lo : INT32_MAX), b = wave_max(on ? hi : 0);
     if (l == 0) {
       span[w][0] = a;
       span[w][1] = b;
-      span[w][2] = c;
-      span[w][3] = e;
     }
     if (tid < 2) bad[tid] = 0;
+    if (tid == 0) again = 0;
   }
   __syncthreads();
   const int first = __builtin_amdgcn_readfirstlane(min(min(span[0][0], span[1][0]), min(span[2][0], span[3][0])));
   const int end = __builtin_amdgcn_readfirstlane(max(max(span[0][1], span[1][1]), max(span[2][1], span[3][1])));
-  const int all_lo = __builtin_amdgcn_readfirstlane(max(max(span[0][2], span[1][2]), max(span[2][2], span[3][2])));
-  const int all_hi = __builtin_amdgcn_readfirstlane(min(min(span[0][3], span[1][3]), min(span[2][3], span[3][3])));
 
   const T* K = static_cast<const T*>(p.k) + (int64_t)g * p.d;
   const T* V = static_cast<const T*>(p.v) + (int64_t)g * p.d;
@@ -79,6 +70,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   L::offsets(ko, w, l, p.ld_k, p.d);
   L::offsets(vo, w, l, p.ld_v, p.d);
   const uint32_t base = lds_addr(lds);
+  const typename L::At lane0 = L::lane(base, l);
   auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
     L::copy(K, p.ld_k, p.d, kb, end, ko, base + (uint32_t)(buf * 2 * L::BYTES), w);
     L::copy(V, p.ld_v, p.d, kb, end, vo, base + (uint32_t)(buf * 2 * L::BYTES + L::BYTES), w);
@@ -116,8 +108,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   const float cap = kLog2e * p.cap;
   const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
 
-  // the walk over the keys, as in the forward pass: again and CAREFUL where a tile
-  // that some queries do not see whole holds a NaN or an infinity
+  // the walk over the keys, as in the forward pass: again and CAREFUL with the keys
+  // where a sum is not finite
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
     int buf = 0;
@@ -128,19 +120,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (kb + 64 < end) issue(kb + 64, buf ^ 1);
-      const unsigned char* kt = lds + buf * 2 * L::BYTES;
-      const unsigned char* vt = kt + L::BYTES;
+      const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), vt = L::move(kt, L::BYTES);
       uint32_t bad0 = 0, bad1 = 0;
-      if (kb < all_lo || kb + 64 > all_hi) {
-        L::find_bad(kt, tid, bad);
+      if constexpr (CAREFUL) {
+        L::find_bad(lds + buf * 2 * L::BYTES, tid, 256, bad);
         __syncthreads();
         bad0 = __builtin_amdgcn_readfirstlane(bad[0]);
         bad1 = __builtin_amdgcn_readfirstlane(bad[1]);
-        if (bad0 | bad1) {
-          __syncthreads();
-          if (tid < 2) bad[tid] = 0;
-          if constexpr (!CAREFUL) return false;
-        }
+        __syncthreads();
+        if (tid < 2) bad[tid] = 0;
       }
       if (!__any(mine.live && lo < kb + 64 && hi > kb)) continue;
       const bool whole = __all(!mine.live || (lo <= kb && hi >= kb + 64));
@@ -152,9 +140,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
 #pragma unroll
         for (int x = 0; x < 2 * DT; ++x) {
           typename L::Frag a;
-          L::rows(a, kt, 32 * i, x, l);
+          L::rows(a, kt, 32 * i, x);
           mma(s, a, qf[x]);
-          L::rows(a, vt, 32 * i, x, l);
+          L::rows(a, vt, 32 * i, x);
           mma(dp, a, af[x]);
         }
 #pragma unroll
@@ -176,13 +164,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
                               [&](int x) { return kb + 32 * i + x >= lo && kb + 32 * i + x < hi; });
       }
     }
-    return true;
   };
-  if (!walk(std::false_type{})) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // the next tile's copies
-    __syncthreads();
-    walk(std::true_type{});
-  }
+  walk(std::false_type{});
+  const float z = finite<DT>(o);
+  if (__any(mine.live && z != z)) again = 1;
+  __syncthreads();
+  if (again) walk(std::true_type{});
   if (!mine.live) return;
   T* out = static_cast<T*>(p.dq) + (t * p.H + h) * p.d;
   const float sc = p.scale;
@@ -197,17 +184,24 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
 }
 
 // A workgroup has 128 keys of a group, 32 a wave, and walks over tiles of 64 queries
-// of each of the group's heads; a lane holds one key.
+// of each of the group's heads; a lane holds one key.  bf16: 8 waves, of which two
+// share keys and take 32 queries of a tile each (their sums meet in LDS at the end),
+// and v's rows are read from LDS: dk, dv and k's rows leave no registers for them at
+// two waves a SIMD.  fp32: 4 waves, all of it in registers at one wave a SIMD.
 template <typename T, int DT, bool CAP, bool BIAS>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(const AttnParams p) {
+__global__ __launch_bounds__(sizeof(T) == 2 ? 512 : 256) void attn_dkv_kernel(const AttnParams p) {
   typedef Tile<T, DT> L;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[4 * L::BYTES];   // Q, dA of two tiles
+  constexpr bool SPLIT = sizeof(T) == 2;
+  constexpr int NW = SPLIT ? 8 : 4;
+  __shared__ __attribute__((aligned(512))) unsigned char lds[(SPLIT ? 6 : 4) * L::BYTES];   // Q, dA of two tiles; V
   __shared__ __attribute__((aligned(16))) float stat[2][2][64];              // lse2, D
   __shared__ __attribute__((aligned(16))) int4 sees[2][64];
+  __shared__ __attribute__((aligned(16))) uint32_t seen[NW][64];             // of a wave's keys, by query
   __shared__ int span[4][2];
-  __shared__ uint32_t bad[4];                                                // of Q, of dA
+  __shared__ uint32_t bad[4], again;                                         // of Q, of dA
   const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = w & 3, half = w >> 2;                        // keys; (SPLIT) queries of a tile
 
   // blocks of an XCD are consecutive: the keys from the first on (with the longest columns), then the groups
   const int nk = (int)((p.T + 127) / 128), total = nk * p.G;
@@ -216,7 +210,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
   const int g = n / nk, k0 = (n - g * nk) * 128;
   const int heads0 = p.group_start[g], heads = p.group_start[g + 1] - heads0;
 
-  const int64_t t = (int64_t)k0 + 32 * w + (l & 31);
+  const int64_t t = (int64_t)k0 + 32 * wk + (l & 31);
   bool live = t < p.T;
   int qfirst = 0, qend = 0;                                   // the queries that see this lane's key
   if (live) {
@@ -231,33 +225,38 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
     }
   }
   {
-    int a = qfirst < qend ? qfirst : INT32_MAX, b = qfirst < qend ? qend : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      a = min(a, __shfl_xor(a, o));
-      b = max(b, __shfl_xor(b, o));
-    }
-    if (l == 0) {
-      span[w][0] = a;
-      span[w][1] = b;
+    const bool on = qfirst < qend;
+    const int a = wave_min(on ? qfirst : INT32_MAX), b = wave_max(on ? qend : 0);
+    if (l == 0 && half == 0) {
+      span[wk][0] = a;
+      span[wk][1] = b;
     }
     if (tid < 4) bad[tid] = 0;
+    if (tid == 0) again = 0;
   }
   __syncthreads();
   const int first = __builtin_amdgcn_readfirstlane(min(min(span[0][0], span[1][0]), min(span[2][0], span[3][0])));
   const int end = __builtin_amdgcn_readfirstlane(max(max(span[0][1], span[1][1]), max(span[2][1], span[3][1])));
   const int tiles = first < end ? (end - first + 63) / 64 : 0, steps = tiles * heads;
 
-  uint32_t qo[L::PERIOD], ao[L::PERIOD];
   const int64_t ld_a = (int64_t)p.H * p.d;
-  L::offsets(qo, w, l, p.ld_q, p.d);
-  L::offsets(ao, w, l, ld_a, p.d);
   const uint32_t base = lds_addr(lds);
+  const typename L::At lane0 = L::lane(base, l);
+  uint32_t qo[L::PERIOD], ao[L::PERIOD];                      // SPLIT: waves 0 .. 3 copy Q, 4 .. 7 dA
+  L::offsets(qo, wk, l, SPLIT && half ? ld_a : p.ld_q, p.d);
+  if constexpr (!SPLIT) L::offsets(ao, wk, l, ld_a, p.d);
   int ih = 0, it = 0;                                         // the copies' head and tile
   auto issue = [&](int buf) __attribute__((always_inline)) {
     const int h = p.head_order[heads0 + ih], qb = first + 64 * it;
-    L::copy(static_cast<const T*>(p.q) + (int64_t)h * p.d, p.ld_q, p.d, qb, end, qo, base + (uint32_t)(buf * 2 * L::BYTES), w);
-    L::copy(static_cast<const T*>(p.da) + (int64_t)h * p.d, ld_a, p.d, qb, end, ao, base + (uint32_t)(buf * 2 * L::BYTES + L::BYTES), w);
+    const T* q = static_cast<const T*>(p.q) + (int64_t)h * p.d;
+    const T* da = static_cast<const T*>(p.da) + (int64_t)h * p.d;
+    const uint32_t to = base + (uint32_t)(buf * 2 * L::BYTES);
+    if constexpr (SPLIT) {
+      L::copy(half ? da : q, half ? ld_a : p.ld_q, p.d, qb, end, qo, to + (uint32_t)(half * L::BYTES), wk);
+    } else {
+      L::copy(q, p.ld_q, p.d, qb, end, qo, to, wk);
+      L::copy(da, ld_a, p.d, qb, end, ao, to + L::BYTES, wk);
+    }
     const uint32_t left = (uint32_t)min(end - qb, 64);
     if (w < 2) dma4s(uniform_rsrc(p.stat + ((int64_t)w * p.H + h) * p.T + qb, 4 * left), 4u * (uint32_t)l, lds_addr(stat[buf][w]));
     if (w == 2 && p.rows) dma16s(uniform_rsrc(p.rows + qb, 16 * left), 16u * (uint32_t)l, 0u, lds_addr(sees[buf]));
@@ -266,22 +265,30 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
       ++ih;
     }
   };
+
   const int64_t tr = min<int64_t>(t, p.T - 1);
-  typename L::Frag kf[2 * DT], vf[2 * DT];
+  typename L::Frag kf[2 * DT], vf[SPLIT ? 1 : 2 * DT];
   const T* krow = static_cast<const T*>(p.k) + tr * p.ld_k + (int64_t)g * p.d;
-  const T* vrow = static_cast<const T*>(p.v) + tr * p.ld_v + (int64_t)g * p.d;
 #pragma unroll
-  for (int s = 0; s < 2 * DT; ++s) {
-    L::load(kf[s], krow, s, p.d, l);
-    L::load(vf[s], vrow, s, p.d, l);
+  for (int s = 0; s < 2 * DT; ++s) L::load(kf[s], krow, s, p.d, l);
+  if constexpr (SPLIT) {
+    uint32_t vo[L::PERIOD];
+    L::offsets(vo, wk, l, p.ld_v, p.d);
+    L::copy(static_cast<const T*>(p.v) + (int64_t)g * p.d, p.ld_v, p.d, k0 + 64 * half, p.T, vo, base + (uint32_t)((4 + half) * L::BYTES), wk);
+  } else {
+    const T* vrow = static_cast<const T*>(p.v) + tr * p.ld_v + (int64_t)g * p.d;
+#pragma unroll
+    for (int s = 0; s < 2 * DT; ++s) L::load(vf[s], vrow, s, p.d, l);
   }
+  const typename L::At vt = L::move(lane0, (uint32_t)((4 + (wk >> 1)) * L::BYTES + (wk & 1) * 32 * L::PITCH));
+
   f32x16 dk[DT], dv[DT];
   const float c1 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
   const float cap = kLog2e * p.cap;
-  const int kw = k0 + 32 * w, kw_end = (int)min<int64_t>(kw + 32, p.T), wg_end = (int)min<int64_t>(k0 + 128, p.T);
+  const int kw = k0 + 32 * wk, kw_end = (int)min<int64_t>(kw + 32, p.T);
 
-  // the walk over the queries, as in the forward pass: again and CAREFUL where a tile
-  // that is not seen whole holds a NaN or an infinity
+  // the walk over the queries, as in the forward pass: again and CAREFUL with q and
+  // da where a sum is not finite
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
     int buf = 0, head = 0, tile = 0;
@@ -299,49 +306,50 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
         ++head;
       }
       const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
-      const unsigned char* qt = lds + buf * 2 * L::BYTES;
-      const unsigned char* at = qt + L::BYTES;
-      // what the tile's queries see of this wave's and this workgroup's keys
-      auto seen_by = [&](int q) __attribute__((always_inline)) {   // q of the tile: its keys [x, y)
-        int2 v;
-        if (p.rows) {
-          v = *reinterpret_cast<const int2*>(&sees[buf][q]);       // zeros behind the last query
-          if (v.x < 0) v.y = 0;
-        } else {
-          v = make_int2(0, qb + q < p.T ? (p.causal ? qb + q + 1 : (int)p.T) : 0);
-        }
-        return v;
-      };
-      const int2 sq = seen_by(l);
+      const typename L::At qt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), at = L::move(qt, L::BYTES);
       uint32_t bad_q[2] = {0, 0}, bad_a[2] = {0, 0};
-      if (!__all(sq.x <= k0 && sq.y >= wg_end)) {
-        L::find_bad(qt, tid, bad);
-        L::find_bad(at, tid, bad + 2);
+      if constexpr (CAREFUL) {
+        L::find_bad(lds + buf * 2 * L::BYTES, tid, 64 * NW, bad);
+        L::find_bad(lds + buf * 2 * L::BYTES + L::BYTES, tid, 64 * NW, bad + 2);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           bad_q[i] = __builtin_amdgcn_readfirstlane(bad[i]);
           bad_a[i] = __builtin_amdgcn_readfirstlane(bad[2 + i]);
         }
-        if (bad_q[0] | bad_q[1] | bad_a[0] | bad_a[1]) {
-          __syncthreads();
-          if (tid < 4) bad[tid] = 0;
-          if constexpr (!CAREFUL) return false;
-        }
+        __syncthreads();
+        if (tid < 4) bad[tid] = 0;
       }
-      if (!__any(sq.x < kw_end && sq.y > kw)) continue;
-      const bool whole = __all(sq.x <= kw && sq.y >= kw_end);
+      // what query l of the tile sees: its keys [x, y)
+      int2 sq;
+      if (p.rows) {
+        sq = *reinterpret_cast<const int2*>(&sees[buf][l]);      // zeros behind the last query
+        if (sq.x < 0) sq.y = 0;
+      } else {
+        sq = make_int2(0, qb + l < p.T ? (p.causal ? qb + l + 1 : (int)p.T) : 0);
+      }
+      const bool mine = !SPLIT || up == half;
+      if (!__any(mine && sq.x < kw_end && sq.y > kw)) continue;
+      const bool whole = __all(!mine || (sq.x <= kw && sq.y >= kw_end));
+      if (!whole || CAREFUL) {
+        const uint32_t a = (uint32_t)min(max(sq.x - kw, 0), 32), b = (uint32_t)min(max(sq.y - kw, 0), 32);
+        seen[w][l] = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
+      }
       const float from = (float)((int)t - qb - 4 * up);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      auto block = [&](int i) __attribute__((always_inline)) {     // queries 32 i .. of the tile
         f32x16 s = {}, dp = {};
 #pragma unroll
         for (int x = 0; x < 2 * DT; ++x) {
-          typename L::Frag a;
-          L::rows(a, qt, 32 * i, x, l);
+          typename L::Frag a, b;
+          L::rows(a, qt, 32 * i, x);
           mma(s, a, kf[x]);
-          L::rows(a, at, 32 * i, x, l);
-          mma(dp, a, vf[x]);
+          L::rows(a, at, 32 * i, x);
+          if constexpr (SPLIT) {
+            L::rows(b, vt, 0, x);
+            mma(dp, a, b);
+          } else {
+            mma(dp, a, vf[x]);
+          }
         }
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
@@ -353,50 +361,88 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
             const int v = 4 * a + e;
             float bent = 1.f;
             const float y = score<T, CAP, BIAS>(s[v], c1, cap, slope, from - (float)(32 * i + 8 * a + e), bent);
-            float pr = __builtin_amdgcn_exp2f(y - ls[e]), ds = pr * (dp[v] - D[e]);
+            const float pr = __builtin_amdgcn_exp2f(y - ls[e]);
+            float ds = pr * (dp[v] - D[e]);
             if constexpr (CAP) ds *= bent;
-            if (!whole) {
-              const int2 z = seen_by(q + e);
-              const bool on = t >= z.x && t < z.y;
-              pr = on ? pr : 0.f;
-              ds = on ? ds : 0.f;
-            }
             dp[v] = pr;
             s[v] = ds;
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const uint4 m4 = *reinterpret_cast<const uint4*>(&seen[w][32 * i + 8 * a + 4 * up]);
+            const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool on = (m[e] >> (l & 31)) & 1;
+              dp[4 * a + e] = on ? dp[4 * a + e] : 0.f;
+              s[4 * a + e] = on ? s[4 * a + e] : 0.f;
+            }
           }
         }
         L::template along<CAREFUL>(dv, at, 32 * i, dp, l);
         L::template along<CAREFUL>(dk, qt, 32 * i, s, l);
         if constexpr (CAREFUL) {
-          auto seen = [&](int x) {
-            const int2 z = seen_by(32 * i + x);
-            return t >= z.x && t < z.y;
-          };
-          add_bad_rows<T, DT>(dv, dp, bad_a[i], p.d, l, [&](int x) { return static_cast<const T*>(p.da) + (int64_t)(qb + 32 * i + x) * ld_a + (int64_t)h * p.d; }, seen);
-          add_bad_rows<T, DT>(dk, s, bad_q[i], p.d, l, [&](int x) { return static_cast<const T*>(p.q) + (int64_t)(qb + 32 * i + x) * p.ld_q + (int64_t)h * p.d; }, seen);
+          auto on = [&](int x) { return ((seen[w][32 * i + x] >> (l & 31)) & 1) != 0; };
+          add_bad_rows<T, DT>(dv, dp, i ? bad_a[1] : bad_a[0], p.d, l, [&](int x) { return static_cast<const T*>(p.da) + (int64_t)(qb + 32 * i + x) * ld_a + (int64_t)h * p.d; }, on);
+          add_bad_rows<T, DT>(dk, s, i ? bad_q[1] : bad_q[0], p.d, l, [&](int x) { return static_cast<const T*>(p.q) + (int64_t)(qb + 32 * i + x) * p.ld_q + (int64_t)h * p.d; }, on);
         }
+      };
+      if constexpr (SPLIT) {
+        block(half);
+      } else {
+        block(0);
+        block(1);
       }
     }
-    return true;
   };
-  if (!walk(std::false_type{})) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");         // the next tile's copies
-    __syncthreads();
-    walk(std::true_type{});
-  }
-  if (!live) return;
-  T* ok = static_cast<T*>(p.dk) + (t * p.G + g) * p.d;
-  T* ov = static_cast<T*>(p.dv) + (t * p.G + g) * p.d;
+  walk(std::false_type{});
+  const float z = finite<DT>(dk) + finite<DT>(dv);
+  if (__any(live && z != z)) again = 1;
+  __syncthreads();
+  if (again) walk(std::true_type{});
+
   const float sc = p.scale;
+  auto put = [&](f32x16 (&x)[DT], void* to, float by) __attribute__((always_inline)) {
+    if constexpr (SPLIT) {
+      // the second half's sums to the first, through the stages
+      constexpr int OP = 32 * DT + 4;
+      static_assert(4 * 32 * OP * 4 <= 6 * L::BYTES, "the sums of four waves fit");
+      float* o = reinterpret_cast<float*>(lds) + (wk * 32 + (l & 31)) * OP;
+      __syncthreads();
+      if (half) {
 #pragma unroll
-  for (int i = 0; i < DT; ++i)
+        for (int i = 0; i < DT; ++i)
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int e = 32 * i + 8 * a + 4 * up;
-      if (e >= p.d) continue;
-      *reinterpret_cast<typename Four<T>::type*>(ok + e) = Four<T>::of(dk[i][4 * a] * sc, dk[i][4 * a + 1] * sc, dk[i][4 * a + 2] * sc, dk[i][4 * a + 3] * sc);
-      *reinterpret_cast<typename Four<T>::type*>(ov + e) = Four<T>::of(dv[i][4 * a], dv[i][4 * a + 1], dv[i][4 * a + 2], dv[i][4 * a + 3]);
+          for (int a = 0; a < 4; ++a)
+            *reinterpret_cast<float4*>(o + 32 * i + 8 * a + 4 * up) = make_float4(x[i][4 * a], x[i][4 * a + 1], x[i][4 * a + 2], x[i][4 * a + 3]);
+      }
+      __syncthreads();
+      if (half) return;
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const float4 v = *reinterpret_cast<const float4*>(o + 32 * i + 8 * a + 4 * up);
+          x[i][4 * a] += v.x;
+          x[i][4 * a + 1] += v.y;
+          x[i][4 * a + 2] += v.z;
+          x[i][4 * a + 3] += v.w;
+        }
     }
+    if (!live) return;
+    T* out = static_cast<T*>(to) + (t * p.G + g) * p.d;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int e = 32 * i + 8 * a + 4 * up;
+        if (e < p.d) *reinterpret_cast<typename Four<T>::type*>(out + e) = Four<T>::of(x[i][4 * a] * by, x[i][4 * a + 1] * by, x[i][4 * a + 2] * by, x[i][4 * a + 3] * by);
+      }
+  };
+  put(dk, p.dk, sc);
+  put(dv, p.dv, 1.f);
 }
 
 template <typename T, int DT, bool CAP, bool BIAS>
@@ -405,7 +451,7 @@ hipError_t launch_one(const AttnParams& p, hipStream_t st) {
   hipLaunchKernelGGL((attn_dq_kernel<T, DT, CAP, BIAS>), dim3((unsigned)(8 * ((nq + 7) / 8))), dim3(256), 0, st, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_dkv_kernel<T, DT, CAP, BIAS>), dim3((unsigned)(8 * ((nk + 7) / 8))), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((attn_dkv_kernel<T, DT, CAP, BIAS>), dim3((unsigned)(8 * ((nk + 7) / 8))), dim3(sizeof(T) == 2 ? 512 : 256), 0, st, p);
   return hipGetLastError();
 }
 template <typename T, int DT>

@@ -27,7 +27,7 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
   constexpr int CP = HALF / 1024, PERIOD = 16 / L::RPC > 1 ? 16 / L::RPC : 1;
   constexpr int OP = 32 * DT + 4;                           // floats of a column of sums
   static_assert(32 * OP * 4 <= REGION, "the sums fit a wave's stages");
-  __shared__ __attribute__((aligned(16))) unsigned char lds[NW * REGION];
+  __shared__ __attribute__((aligned(512))) unsigned char lds[NW * REGION];
   __shared__ float ms[2][NW][32];
   const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -57,6 +57,7 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
     vo[i] = on ? (uint32_t)(r * p.ld_v * L::E) + 16u * (uint32_t)c : kOutOfRange;
   }
   const uint32_t base = lds_addr(lds) + (uint32_t)(w * REGION);
+  const typename L::At lane0 = L::lane(base, l);
   auto one = [&](const T* x, int64_t ld, const uint32_t (&voff)[PERIOD], int kb, uint32_t to) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < CP; i += PERIOD) {
@@ -93,13 +94,12 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
     // this stage's copies; the other's (as many, zeros past the end) may be in flight
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * CP) : "memory");
     __builtin_amdgcn_sched_barrier(0);
-    const unsigned char* kt = lds + w * REGION + buf * 2 * HALF;
-    const unsigned char* vt = kt + HALF;
+    const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * HALF)), vt = L::move(kt, HALF);
     f32x16 s = {};
 #pragma unroll
     for (int x = 0; x < 2 * DT; ++x) {
       typename L::Frag a;
-      L::rows(a, kt, 0, x, l);
+      L::rows(a, kt, 0, x);
       mma(s, a, qf[x]);
     }
     const float at = (float)(length - 1 - kb - 4 * up);
