@@ -377,7 +377,7 @@ FfnWorkspace ffn_workspace(const hna_ffn_dims* dm) {
   FfnWorkspace w{};
   w.I8 = round_up(dm->I, 8);
   const size_t plane = align256((size_t)dm->T * w.I8 * esize_of(dm->dtype));
-  w.splits = ffn_dn_splits(dm->T, dm->hidden, dm->I);
+  w.splits = ffn_dn_splits(dm->T, dm->hidden, dm->I, dm->dtype == HNA_BF16);
   w.dg = 0;
   w.du = plane;
   w.part = 2 * plane;

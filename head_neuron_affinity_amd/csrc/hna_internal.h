@@ -353,7 +353,7 @@ struct FfnMmParams {
   int64_t lda, ldb, N, K;
   int M, splits;
 };
-int ffn_dn_splits(int64_t T, int C, int I);
+int ffn_dn_splits(int64_t T, int C, int I, int bf16);
 hipError_t launch_ffn_mm(const FfnMmParams& p, int mode, int bf16, hipStream_t st);
 // dg = dh u silu'(g), du = dh silu(g) [rows][I8], zeros behind I
 hipError_t launch_ffn_grad(const void* dh, const void* g, const void* u, int64_t rows, int I, int I8, void* dg, void* du, int bf16,

@@ -108,7 +108,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
       if (!__any(mine.live && lo < kb + 64 && hi > kb)) continue;
 
       f32x16 s[2];
-      s[0] = s[1] = f32x16{};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s[i] = f32x16{};
 #pragma unroll
       for (int x = 0; x < 2 * DT; ++x)
 #pragma unroll
@@ -117,6 +118,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
           L::rows(a, kt, 32 * i, x);
           mma(s[i], a, qf[x]);
         }
+      if constexpr (sizeof(T) == 2) {
+        // the fragments of AHEAD steps in flight: a read takes as long as several products
+        constexpr int READS = 4 * DT, AHEAD = READS < 8 ? READS : 8;
+        __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+        for (int x = 0; x < (READS - AHEAD) / 2; ++x) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
+      }
       // scores in powers of two
       if constexpr (CAP || BIAS) {
         const float at = (float)((int)t - kb - 4 * up);

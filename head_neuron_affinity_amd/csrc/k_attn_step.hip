@@ -174,23 +174,38 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
   }
 }
 
-// the parts of a row joined: a workgroup a row (sequence and head)
+// the parts of a row (sequence and head) joined, a workgroup a row: each lane has a
+// part's reference and total, each thread an element
 template <typename T>
 __global__ __launch_bounds__(128) void attn_join_kernel(const StepParams p) {
+  __shared__ float factor[64];
   const int64_t row = blockIdx.x;
-  const float2* ms = p.part_ms + row * p.splits;
-  float M = -__builtin_inff();
-  for (int i = 0; i < p.splits; ++i) M = fmaxf(M, ms[i].x);
-  const float ref = M == -__builtin_inff() ? 0.f : M;
-  const int e = threadIdx.x;
-  float total = 0.f, y = 0.f;
-  for (int i = 0; i < p.splits; ++i) {
-    const float2 v = ms[i];
-    const float f = __builtin_amdgcn_exp2f(v.x - ref);
-    total = fmaf(f, v.y, total);
-    if (e < p.d) y = fmaf(f, p.part[(row * p.splits + i) * p.d + e], y);
+  const int e = threadIdx.x, l = e & 63;
+  const float2 v = l < p.splits ? p.part_ms[row * p.splits + l] : make_float2(-__builtin_inff(), 0.f);
+  float y[8], M = v.x;
+  const float* part = p.part + row * p.splits * p.d + min(e, p.d - 1);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = part[(int64_t)min(i, p.splits - 1) * p.d];      // under the reductions
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) M = fmaxf(M, __shfl_xor(M, o));
+  const float f = v.x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(v.x - M);
+  float total = f * v.y;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) total += __shfl_xor(total, o);
+  if (e < 64) factor[e] = f;
+  __syncthreads();
+  float sum = 0.f;
+  for (int s = 0; s < p.splits; s += 8) {
+    float next[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) next[i] = part[(int64_t)min(s + 8 + i, p.splits - 1) * p.d];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s + i < p.splits) sum = fmaf(factor[s + i], y[i], sum);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = next[i];
   }
-  if (e < p.d) static_cast<T*>(p.a)[row * p.d + e] = to_type<T>(total == 0.f ? 0.f : y / total);
+  if (e < p.d) static_cast<T*>(p.a)[row * p.d + e] = to_type<T>(total == 0.f ? 0.f : sum / total);
   if (e == 0 && p.lse) p.lse[row] = total == 0.f ? -__builtin_inff() : kLn2 * (M + __builtin_amdgcn_logf(total));
 }
 

@@ -580,23 +580,24 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(const float* part, int sp
 }
 
 // dg = dh u silu'(g), du = dh silu(g) in rows of I8 = I rounded up to 8 elements,
-// zeros behind I (they are k of dn's product).  A thread has 8 channels of a token.
-template <typename T>
-__global__ __launch_bounds__(256) void ffn_grad_kernel(const T* dh, const T* g, const T* u, int64_t rows, int I, int I8, T* dg, T* du) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= rows * I8) return;
-  const int64_t t = i / I8;
-  const int c = (int)(i - t * I8);
-  const int64_t o = t * I + c;
+// zeros behind I (they are k of dn's product).  A thread has 8 channels of a token;
+// rows that start on any element are loaded one element at a time.
+template <typename T, bool WIDE>
+__global__ __launch_bounds__(256) void ffn_grad_kernel(const T* dh, const T* g, const T* u, int64_t chunks, int I, int I8, T* dg, T* du) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // of 8 channels
+  if (i >= chunks) return;
   T x[3][8];
   const T* src[3] = {dh, g, u};
   constexpr int V = 16 / sizeof(T);
-  if (I % 8 == 0) {
+  if constexpr (WIDE) {                                        // I = I8: the planes are alike
 #pragma unroll
     for (int s = 0; s < 3; ++s)
 #pragma unroll
-      for (int v = 0; v < 8 / V; ++v) *reinterpret_cast<uint4*>(&x[s][v * V]) = *reinterpret_cast<const uint4*>(src[s] + o + v * V);
+      for (int v = 0; v < 8 / V; ++v) *reinterpret_cast<uint4*>(&x[s][v * V]) = *reinterpret_cast<const uint4*>(src[s] + 8 * i + v * V);
   } else {
+    const int64_t t = (uint64_t)i < (1ull << 32) ? (uint32_t)i / (uint32_t)(I8 / 8) : i / (I8 / 8);
+    const int c = (int)(8 * (i - t * (I8 / 8)));
+    const int64_t o = t * I + c;
 #pragma unroll
     for (int s = 0; s < 3; ++s)
 #pragma unroll
@@ -618,8 +619,8 @@ __global__ __launch_bounds__(256) void ffn_grad_kernel(const T* dh, const T* g, 
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    reinterpret_cast<typename Four<T>::type*>(dg + i)[h] = og[h];
-    reinterpret_cast<typename Four<T>::type*>(du + i)[h] = ou[h];
+    reinterpret_cast<typename Four<T>::type*>(dg + 8 * i)[h] = og[h];
+    reinterpret_cast<typename Four<T>::type*>(du + 8 * i)[h] = ou[h];
   }
 }
 
@@ -632,22 +633,46 @@ hipError_t launch_tile(const FfnMmParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The variant for a product of this shape; splits (kDn) are chosen here too.
-enum { kBig = 0, k128 = 1, k64 = 2, k32 = 3 };
-int choose(int mode, int64_t N, int M) {
-  const int mats = mode == kFfnGate ? 1 : mode == kFfnDw ? 2 : 1;
-  const int64_t rows = mode == kFfnGate ? 2 * (int64_t)M : M;
+// Variants, by the rounds of tiles they make on 256 CUs (two workgroups of the
+// smaller tiles fit a CU).  Times in us of both sides of each border, T x hidden x I,
+// operands in cache; dn's with the kernel that forms dg and du.
+enum FfnVariant { kBig, k128, k64, k64x32 };
+template <typename T>
+FfnVariant choose(int mode, int64_t N, int M) {
+  const int64_t rows = mode == kFfnGate ? 2 * (int64_t)M : M, mats = mode == kFfnDw ? 2 : 1;
   auto tiles = [&](int m, int n) { return mats * ((rows + m - 1) / m) * ((N + n - 1) / n); };
+  auto rounds = [&](int m, int n) { return (tiles(m, n) + 255) / 256 * (m * n); };
+  // 256 x 256 from 160 tiles on.  Gate, bf16: 2048 x 1536 x 4096 (256 tiles) 49 against
+  // 59 with 128 x 128, 1024 x 1024 x 4096 (128 tiles) 28 against 23; dw 69 against 79
+  // and 40 against 33.
   if (tiles(256, 256) >= 160) return kBig;
-  if (tiles(128, 128) > 256) return k128;
-  if (mode == kFfnGate || tiles(64, 64) > 128) return k64;
-  return k32;
+  if (mode == kFfnDn) {
+    // k is split among workgroups (ffn_dn_splits), so that fewer tiles are no loss:
+    // 128 x 128 from 64 tiles on.  bf16: 1024 x 1024 x 4096 (64 tiles) 43 against 53 with 64 x 64;
+    // 333 x 1024 x 2531 (24 tiles) 28 against 26.  64 x 32 in fp32 for up to 32 tokens: 1 x
+    // 4096 x 14336 98 against 149 (bf16 44 against 42).
+    if (tiles(128, 128) >= 64) return k128;
+    return sizeof(T) == 4 && N <= 32 ? k64x32 : k64;
+  }
+  // fp32 is bound by its products: the tiles that make the least work a CU.  219 x
+  // 1000 x 2531: gate 37 with 64 x 32 against 45 with 64 x 64 and 81 with 128 x 128, dw 39 with
+  // 64 x 64 against 46 with 128 x 128.  512 x 4096 x 4096: gate 298 with 128 x 128, 303 with
+  // 64 x 64.
+  if (sizeof(T) == 4) {
+    if (rounds(128, 128) <= rounds(64, 64)) return k128;
+    return mode == kFfnGate && rounds(64, 32) < rounds(64, 64) ? k64x32 : k64;
+  }
+  // bf16, gate: 512 x 4096 x 4096 (256 tiles of 128 x 128) 47 against 59 with 64 x 64, 333 x
+  // 1024 x 2531 (120 tiles) 23 against 13; up to 32 tokens 64 x 32: 1 x 1024 x 4096 8.2 against
+  // 9.5.  dw: 1 x 1024 x 4096 (512 tiles) 14.8 against 18.5, 219 x 1000 x 2531 (320) 16.5 against 20.3.
+  if (tiles(128, 128) >= 256) return k128;
+  return mode == kFfnGate && N <= 32 ? k64x32 : k64;
 }
 
 template <typename T>
 hipError_t launch_ffn_t(const FfnMmParams& p0, int mode, hipStream_t st) {
   FfnMmParams p = p0;
-  const int v = choose(mode, p.N, p.M);
+  const FfnVariant v = choose<T>(mode, p.N, p.M);
   if (mode == kFfnGate) {
     if (v == kBig) {
       if ((p.M * sizeof(T)) % 16 == 0) hipLaunchKernelGGL((ffn_big_kernel<T, kFfnGate, true>), dim3(256), dim3(256), 0, st, p);
@@ -655,7 +680,8 @@ hipError_t launch_ffn_t(const FfnMmParams& p0, int mode, hipStream_t st) {
       return hipGetLastError();
     }
     if (v == k128) return launch_tile<T, kFfnGate, 128, 128, 2, 2, 1, 2>(p, st);
-    return launch_tile<T, kFfnGate, 64, 64, 2, 2, 2, 2>(p, st);
+    if (v == k64) return launch_tile<T, kFfnGate, 64, 64, 2, 2, 2, 2>(p, st);
+    return launch_tile<T, kFfnGate, 64, 32, 2, 1, 2, 2>(p, st);
   }
   if (mode == kFfnDw) {
     if (v == kBig) {
@@ -663,7 +689,7 @@ hipError_t launch_ffn_t(const FfnMmParams& p0, int mode, hipStream_t st) {
       return hipGetLastError();
     }
     if (v == k128) return launch_tile<T, kFfnDw, 128, 128, 2, 2, 1, 2>(p, st);
-    return launch_tile<T, kFfnDw, 64, 64, 2, 2, 2, 2>(p, st);
+    return launch_tile<T, kFfnDw, 64, 64, 2, 2, 1, 2>(p, st);
   }
   if (v == kBig) {
     hipLaunchKernelGGL((ffn_big_kernel<T, kFfnDn, true>), dim3(256), dim3(256), 0, st, p);
@@ -672,41 +698,53 @@ hipError_t launch_ffn_t(const FfnMmParams& p0, int mode, hipStream_t st) {
   hipError_t e;
   if (p.splits == 1) p.part = nullptr;
   if (v == k128) e = launch_tile<T, kFfnDn, 128, 128, 2, 2, 1, 2>(p, st);
+  else if constexpr (sizeof(T) == 2) e = launch_tile<T, kFfnDn, 64, 64, 2, 2, 2, 4>(p, st);
   else if (v == k64) e = launch_tile<T, kFfnDn, 64, 64, 2, 2, 2, 2>(p, st);
-  else e = launch_tile<T, kFfnDn, 32, 32, 1, 1, 4, 4>(p, st);
+  else e = launch_tile<T, kFfnDn, 64, 32, 2, 1, 4, 2>(p, st);
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t n4 = p.N * p.M / 4;
   hipLaunchKernelGGL(ffn_join_kernel<T>, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st, p.part, p.splits, n4, static_cast<T*>(p.out[0]));
   return hipGetLastError();
 }
 
+// Workgroups of dn that share a tile's k: as many as fill the CUs, two a CU where
+// the variant's LDS lets them (one for bf16's four stages of 64 x 64, and for 64 x 32).
+// bf16, us with 1, 2, 4 and 8: 1024 x 4096 x 14336 (256 tiles) 464, 321, 333, 355; 64 x 4096 x 14336
+// (64 tiles) 125, 72, 52, 55; 333 x 1024 x 2531 (96 tiles) 34, 26, 29, 31.
+template <typename T>
+int splits_of(int64_t N, int C, int I) {
+  const FfnVariant v = choose<T>(kFfnDn, N, C);
+  if (v == kBig || N == 0) return 1;
+  const int m = v == k128 ? 128 : 64, n = v == k128 ? 128 : v == k64 ? 64 : 32;
+  const int64_t tiles = (int64_t)((C + m - 1) / m) * ((N + n - 1) / n);
+  const int64_t slots = v == k128 || (v == k64 && sizeof(T) == 4) ? 512 : 256;
+  const int64_t steps = 2 * (((int64_t)I * sizeof(T) + 255) / 256);         // of 256 bytes of k
+  return (int)std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 2, 16}));
+}
+
 }  // namespace
 
-int ffn_dn_splits(int64_t T, int C, int I) {
-  const int v = choose(kFfnDn, T, C);
-  if (v == kBig) return 1;
-  const int b = v == k128 ? 128 : v == k64 ? 64 : 32;
-  const int64_t tiles = (int64_t)((C + b - 1) / b) * ((T + b - 1) / b);
-  const int64_t most = std::min<int64_t>(16, ((int64_t)I + 1023) / 1024);   // 2048 of k a split at least
-  return (int)std::max<int64_t>(1, std::min(most, 256 / std::max<int64_t>(tiles, 1)));
-}
+int ffn_dn_splits(int64_t T, int C, int I, int bf16) { return bf16 ? splits_of<__bf16>(T, C, I) : splits_of<float>(T, C, I); }
 
 hipError_t launch_ffn_mm(const FfnMmParams& p, int mode, int bf16, hipStream_t st) {
   if (p.N == 0 || p.M == 0) return hipSuccess;
   return bf16 ? launch_ffn_t<__bf16>(p, mode, st) : launch_ffn_t<float>(p, mode, st);
 }
 
+template <typename T>
+static hipError_t launch_grad_t(const void* dh, const void* g, const void* u, int64_t rows, int I, int I8, void* dg, void* du, hipStream_t st) {
+  const int64_t chunks = rows * (I8 / 8);
+  const dim3 grid((unsigned)((chunks + 255) / 256));
+  const T *a = static_cast<const T*>(dh), *b = static_cast<const T*>(g), *c = static_cast<const T*>(u);
+  if (I == I8) hipLaunchKernelGGL((ffn_grad_kernel<T, true>), grid, dim3(256), 0, st, a, b, c, chunks, I, I8, static_cast<T*>(dg), static_cast<T*>(du));
+  else hipLaunchKernelGGL((ffn_grad_kernel<T, false>), grid, dim3(256), 0, st, a, b, c, chunks, I, I8, static_cast<T*>(dg), static_cast<T*>(du));
+  return hipGetLastError();
+}
+
 hipError_t launch_ffn_grad(const void* dh, const void* g, const void* u, int64_t rows, int I, int I8, void* dg, void* du, int bf16,
                            hipStream_t st) {
   if (rows == 0) return hipSuccess;
-  const dim3 grid((unsigned)((rows * I8 / 8 + 255) / 256));
-  if (bf16)
-    hipLaunchKernelGGL(ffn_grad_kernel<__bf16>, grid, dim3(256), 0, st, static_cast<const __bf16*>(dh), static_cast<const __bf16*>(g),
-                       static_cast<const __bf16*>(u), rows, I, I8, static_cast<__bf16*>(dg), static_cast<__bf16*>(du));
-  else
-    hipLaunchKernelGGL(ffn_grad_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(dh), static_cast<const float*>(g),
-                       static_cast<const float*>(u), rows, I, I8, static_cast<float*>(dg), static_cast<float*>(du));
-  return hipGetLastError();
+  return bf16 ? launch_grad_t<__bf16>(dh, g, u, rows, I, I8, dg, du, st) : launch_grad_t<float>(dh, g, u, rows, I, I8, dg, du, st);
 }
 
 }  // namespace hna
