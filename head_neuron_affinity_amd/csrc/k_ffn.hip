@@ -35,13 +35,20 @@ template <int MODE> constexpr bool kMajorB = MODE == kFfnDw;
 // 256 x 256 tiles on 4 waves, one per SIMD, each 128 x 128 (16 accumulators of
 // 32 x 32).  128 bytes of k a step in two stages; a step is four quarters, and
 // the fragments of the next quarter are read while the MFMAs of this one run:
-//   quarters 0 .. 2 of step s, reading quarters 1 .. 3
+//   quarter 0 of step s, reading quarter 1 and issuing the second half of step s + 1's copies
+//   quarters 1 and 2, reading quarters 2 and 3
 //   wait for the reads and for step s + 1's copies; barrier
-//   quarter 3, reading quarter 0 of step s + 1 and copying step s + 2 over step s
+//   quarter 3, reading quarter 0 of step s + 1 and issuing half of step s + 2's
+//   copies, over step s
 // The barrier says that every wave holds step s in registers (its stage is
-// free) and that every wave's part of step s + 1 is in LDS.  One workgroup a CU
-// walks over its tiles, and the steps of all of them are one stream, so that the
-// copies never drain and stores overlap the next tile's MFMAs.
+// free) and that every wave's part of step s + 1 is in LDS.  The copies of a step
+// are 64 KB, 1024 cycles of a CU's 64 bytes a cycle: spread over two quarters (1024
+// cycles) they cost 8 to 10% less than in one.  One workgroup a CU walks over its tiles, and the
+// steps of all of them are one stream, so that the copies never drain between tiles.
+// Power sets the pace on data (MFMAs busy 60% of the cycles at 1.5 to 1.8 GHz):
+// lines touched ahead in L2, and copies spread over three quarters, made no difference.
+// Measured, T x hidden x I, bf16: 65536 x 1536 x 4096 forward (g and u) 1.46 ms, 1.13e15 operations
+// a second; 8192 x 4096 x 14336 gradients 3.2 to 3.3 ms, 1.75e15.
 // A gate tile's 256 rows are 128 channels of both matrices, 64 + 64 a wave, so
 // that a wave holds g and u of the same channels and tokens.
 struct FfnTiles {
@@ -213,16 +220,12 @@ __global__ __launch_bounds__(256, 1) void ffn_big_kernel(const FfnMmParams p) {
   for (int c = 0; c < 16; ++c) issue(0, c);
   next_copy();
 #pragma unroll
-  for (int c = 0; c < 16; ++c) issue(1, c);
-  next_copy();
-  __builtin_amdgcn_s_waitcnt(vm_wait(16));                  // the first step is in
+  for (int c = 0; c < 8; ++c) issue(1, c);
+  __builtin_amdgcn_s_waitcnt(vm_wait(8));                  // the first step is in
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
 
-  const int outs = MODE == kFfnGate ? (p.out[0] != nullptr) + (p.out[1] != nullptr) + (p.out[2] != nullptr) : 1;
-  constexpr int STORES = 16 * (MODE == kFfnGate ? 1 : 2) * E / 2;   // of an output of a tile, per thread
   int buf = 0;
-  bool stored = false;                                      // the previous tile's stores may be in flight
   while (true) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -233,28 +236,22 @@ __global__ __launch_bounds__(256, 1) void ffn_big_kernel(const FfnMmParams p) {
     for (int kt = 0; kt < nk; ++kt) {
       mm(Q0, [&](auto i) __attribute__((always_inline)) {
         if constexpr (i < 8) rd(buf, Q1, i);
+        if constexpr (i % 2 == 0) issue(buf ^ 1, 8 + i / 2);
       });
+      next_copy();
       mm(Q1, [&](auto i) __attribute__((always_inline)) {
         if constexpr (i < 8) rd(buf, Q2, i);
       });
       mm(Q2, [&](auto i) __attribute__((always_inline)) {
         if constexpr (i < 8) rd(buf, Q3, i);
       });
-      // step s + 1's copies are older than the stores of the tile before
-      if (kt == 0 && stored) {
-        if (outs == 3) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(3 * STORES > 63 ? 63 : 3 * STORES) : "memory");
-        else if (outs == 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * STORES > 63 ? 63 : 2 * STORES) : "memory");
-        else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(STORES > 63 ? 63 : STORES) : "memory");
-      } else {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      }
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
       mm(Q3, [&](auto i) __attribute__((always_inline)) {
         if constexpr (i < 8) rd(buf ^ 1, Q0, i);
-        issue(buf, i);
+        if constexpr (i % 2 == 0) issue(buf, i / 2);
       });
-      next_copy();
       buf ^= 1;
     }
 
@@ -344,8 +341,6 @@ __global__ __launch_bounds__(256, 1) void ffn_big_kernel(const FfnMmParams p) {
         __builtin_amdgcn_sched_barrier(0);
       });
     });
-    if constexpr (WIDE) stored = true;
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // a varying number of stores
     tile = after(tile);
     if (tile >= g.ntiles) break;
   }
