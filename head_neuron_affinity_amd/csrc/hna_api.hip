@@ -332,7 +332,19 @@ AttnParams attn_params(const hna_attn_dims* dm, const void* q, const void* k, co
   return p;
 }
 
-size_t attn_stat_bytes(const hna_attn_dims* dm) { return align256((size_t)2 * dm->H * dm->T * sizeof(float)); }
+struct AttnWorkspace {
+  size_t order, part_q, part_k, total;
+  AttnSplits splits;
+};
+AttnWorkspace attn_workspace(const hna_attn_dims* dm) {
+  AttnWorkspace w{};
+  w.splits = attention_splits(dm->T, dm->H, dm->G);
+  w.order = align256((size_t)2 * dm->H * dm->T * sizeof(float));
+  w.part_q = w.order + align256((size_t)((dm->T + 127) / 128) * sizeof(int));
+  w.part_k = w.part_q + (w.splits.q > 1 ? align256((size_t)w.splits.q * dm->T * dm->H * dm->d * sizeof(float)) : 0);
+  w.total = w.part_k + (w.splits.k > 1 ? align256((size_t)2 * w.splits.k * dm->T * dm->G * dm->d * sizeof(float)) : 0);
+  return w;
+}
 
 struct StepWorkspace {
   size_t ms, total;
@@ -1571,7 +1583,7 @@ int hna_attention(const hna_attn_dims* dm, const void* q, const void* k, const v
 
 size_t hna_attention_workspace_bytes(const hna_attn_dims* dm) {
   if (check_attn_dims("hna_attention_workspace_bytes", dm)) return 0;
-  return std::max(attn_stat_bytes(dm), size_t(256));
+  return std::max(attn_workspace(dm).total, size_t(256));
 }
 
 int hna_attention_backward(const hna_attn_dims* dm, const void* da, const void* q, const void* k, const void* v,
@@ -1596,9 +1608,9 @@ int hna_attention_backward(const hna_attn_dims* dm, const void* da, const void* 
     REQUIRE_PTR(dv);
   }
   REQUIRE_PTR(workspace);
-  const size_t need = attn_stat_bytes(dm);
-  if (workspace_bytes < need)
-    return fail(HNA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, need);
+  const AttnWorkspace w = attn_workspace(dm);
+  if (workspace_bytes < w.total)
+    return fail(HNA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, w.total);
   AttnParams p = attn_params(dm, q, k, v, rows, slopes, group_of_head);
   p.da = da;
   p.a = const_cast<void*>(a);
@@ -1606,7 +1618,13 @@ int hna_attention_backward(const hna_attn_dims* dm, const void* da, const void* 
   p.dq = dq;
   p.dk = dk;
   p.dv = dv;
+  char* ws = static_cast<char*>(workspace);
   p.stat = static_cast<float*>(workspace);
+  if (rows && (dm->T + 127) / 128 <= kMaxSortedBlocks) p.order = reinterpret_cast<int*>(ws + w.order);
+  p.splits_q = w.splits.q;
+  p.splits_k = w.splits.k;
+  p.part_q = reinterpret_cast<float*>(ws + w.part_q);
+  p.part_k = reinterpret_cast<float*>(ws + w.part_k);
   hipStream_t st = static_cast<hipStream_t>(stream);
   return finish(launch_attention_backward(p, dm->dtype == HNA_BF16, st), st, fn);
 }

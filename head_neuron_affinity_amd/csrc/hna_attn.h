@@ -13,16 +13,16 @@ namespace attn {
 using namespace hot;
 using namespace mm;
 
-// 64 rows of d elements (d a multiple of 16, at most 32 DT) in LDS; 16-byte chunk
+// N rows of d elements (d a multiple of 16, at most 32 DT) in LDS; 16-byte chunk
 // c of row r lies in slot c ^ f(r).  f is distinct over 16 rows of one chunk (a
 // fragment of rows), and puts the four rows that a transposed read takes at once
 // (64 bytes of each) in different banks.  Chunks from d on are zeros.
-template <typename T, int DT>
+template <typename T, int DT, int N = 64>
 struct Tile {
   static constexpr int E = sizeof(T), F = E / 2;         // F: 16-byte pieces of a lane's 8 elements
-  static constexpr int DP = DT == 3 ? 128 : 32 * DT, PITCH = DP * E, CPR = PITCH / 16, BYTES = 64 * PITCH;
+  static constexpr int DP = DT == 3 ? 128 : 32 * DT, PITCH = DP * E, CPR = PITCH / 16, BYTES = N * PITCH;
   static constexpr int RPC = 64 / CPR;                   // rows of a 1 KB copy
-  static constexpr int COPIES = BYTES / 4096;            // of each of 4 waves
+  static constexpr int COPIES = BYTES < 4096 ? 1 : BYTES / 4096;   // of each of 4 waves (of two, for 2 KB)
   typedef uint4 Frag[F];
 
   __device__ static inline int f(int r) {
@@ -49,7 +49,8 @@ struct Tile {
       const u32x4 rs = uniform_rsrc(static_cast<const char*>(x) + from * ld * E,
                                     end <= from ? 0u : n > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)n);
 #pragma unroll
-      for (int j = 0; j < PERIOD; ++j) dma16s(rs, voff[j], 0u, lds + (uint32_t)((4 * (i + j) + w) * 1024));
+      for (int j = 0; j < PERIOD; ++j)
+        if (BYTES >= 4096 || 1024 * w < BYTES) dma16s(rs, voff[j], 0u, lds + (uint32_t)((4 * (i + j) + w) * 1024));
     }
   }
   // A lane's addresses in a tile at LDS address `at` (a multiple of 512): of row
@@ -221,6 +222,20 @@ __device__ inline int wave_min(int x) {
   return min(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16));
 }
 __device__ inline int wave_max(int x) { return ~wave_min(~x); }
+
+// The order of READS fragment reads, STEP of them for two products: AHEAD in flight,
+// since a read takes as long as several products
+template <int READS, int STEP, int AHEAD>
+__device__ inline __attribute__((always_inline)) void reads_ahead() {
+  constexpr int A = READS < AHEAD ? READS : AHEAD;
+  __builtin_amdgcn_sched_group_barrier(0x100, A, 0);
+#pragma unroll
+  for (int x = 0; x < (READS - A) / STEP; ++x) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, STEP, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, 2 * A / STEP, 0);
+}
 
 // joined over the two lanes that hold a column's rows
 __device__ inline float swap_max(float x) {

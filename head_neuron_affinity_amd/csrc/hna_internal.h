@@ -370,8 +370,11 @@ struct AttnParams {
   const void* da;           // [T][H][d]
   void *dq, *dk, *dv;       // [T][H][d], [T][G][d], or NULL
   float* stat;              // [2][H][T]: lse in powers of two, then sum_e da a
+  int* order;               // [ceil(T / 128)] blocks of keys, the longest first, or NULL: as they are
+  float* part_q;            // splits_q > 1: [splits_q][T][H][d] sums of dq
+  float* part_k;            // splits_k > 1: [splits_k][2][T][G][d] sums of dk, dv
   int64_t T, ld_q, ld_k, ld_v;
-  int H, G, d, causal;
+  int H, G, d, causal, splits_q, splits_k;
   float scale, cap;         // cap 0: none
   int8_t head_order[kMaxHeads];        // heads sorted by KV group (stable)
   int8_t head_group[kMaxHeads];        // group of head h
@@ -379,6 +382,11 @@ struct AttnParams {
 };
 hipError_t launch_attention(const AttnParams& p, int bf16, hipStream_t st);
 hipError_t launch_attention_rows(int64_t T, int docs, const int32_t* start, const int32_t* prefix, int causal, void* rows, hipStream_t st);
+struct AttnSplits {
+  int q, k;
+};
+AttnSplits attention_splits(int64_t T, int H, int G);
+constexpr int64_t kMaxSortedBlocks = 16384;   // one workgroup sorts them, beside the others' work
 hipError_t launch_attention_backward(const AttnParams& p, int bf16, hipStream_t st);
 
 struct StepParams {

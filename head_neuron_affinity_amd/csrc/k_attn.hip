@@ -31,13 +31,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
   const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // blocks of an XCD are consecutive: the heads of a group next to each other, then
-  // the queries from the last on (the longest rows first), then the groups
-  const int nq = (int)((p.T + 127) / 128), r = p.H / p.G, total = nq * p.H;
-  const int per_xcd = (total + 7) / 8, slot = (int)(blockIdx.x >> 3), n = (int)(blockIdx.x & 7) * per_xcd + slot;
-  if (slot >= per_xcd || n >= total) return;
-  const int gi = n / (nq * r), rem = n - gi * nq * r, qt = nq - 1 - rem / r;
-  const int h = p.head_order[gi * r + rem % r], g = p.head_group[h];
+  // the groups by turns (with 8 of them, one to an XCD: consecutive blocks go round the
+  // XCDs), a group's heads next to each other, the queries from the last on (the
+  // longest rows first)
+  const int nq = (int)((p.T + 127) / 128), r = p.H / p.G, gi = (int)blockIdx.x % p.G, rest = (int)blockIdx.x / p.G;
+  const int qt = nq - 1 - rest / r;
+  const int h = p.head_order[gi * r + rest % r], g = p.head_group[h];
 
   const int64_t q0 = (int64_t)qt * 128, t = q0 + 32 * w + (l & 31);
   const Span mine = Span::of(p.rows, p.causal, p.T, t);
@@ -118,17 +117,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
           L::rows(a, kt, 32 * i, x);
           mma(s[i], a, qf[x]);
         }
-      if constexpr (sizeof(T) == 2) {
-        // the fragments of AHEAD steps in flight: a read takes as long as several products
-        constexpr int READS = 4 * DT, AHEAD = READS < 8 ? READS : 8;
-        __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
-#pragma unroll
-        for (int x = 0; x < (READS - AHEAD) / 2; ++x) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
-      }
+      if constexpr (sizeof(T) == 2) reads_ahead<4 * DT, 2, 8>();
       // scores in powers of two
       if constexpr (CAP || BIAS) {
         const float at = (float)((int)t - kb - 4 * up);
@@ -232,8 +221,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(int T, int docs, const i
 
 template <typename T, int DT, bool CAP, bool BIAS>
 hipError_t launch_one(const AttnParams& p, hipStream_t st) {
-  const int64_t total = (p.T + 127) / 128 * p.H;
-  hipLaunchKernelGGL((attn_kernel<T, DT, CAP, BIAS>), dim3((unsigned)(8 * ((total + 7) / 8))), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((attn_kernel<T, DT, CAP, BIAS>), dim3((unsigned)((p.T + 127) / 128 * p.H)), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 template <typename T, int DT>

@@ -9,6 +9,8 @@
 // added from two sides: no atomics, sums in a fixed order.  That is 7 products
 // where one walk with sums of dq in memory would have 5.
 // p and ds are rounded to the inputs' type, as operands of products in that type.
+#include <algorithm>
+
 #include "hna_internal.h"
 #include "hna_attn.h"
 
@@ -30,6 +32,42 @@ __device__ inline float score(float x, float c1, float cap, float slope, float d
   return x;
 }
 
+// a lane's column, as a row of out, or as fp32 sums of a part
+template <typename T, int DT>
+__device__ inline void put_rows(const f32x16 (&x)[DT], float by, void* out, float* part, int64_t at, int d, int up) {
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int e = 32 * i + 8 * a + 4 * up;
+      if (e >= d) continue;
+      const float v[4] = {x[i][4 * a] * by, x[i][4 * a + 1] * by, x[i][4 * a + 2] * by, x[i][4 * a + 3] * by};
+      if (part) *reinterpret_cast<float4*>(part + at + e) = make_float4(v[0], v[1], v[2], v[3]);
+      else *reinterpret_cast<typename Four<T>::type*>(static_cast<T*>(out) + at + e) = Four<T>::of(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// The blocks of 128 keys by the queries that see their first key, the most first
+// (in 256 classes), so that the long ones do not start last: p.order.
+__device__ inline void sort_key_blocks(const AttnParams& p, int* lds) {
+  const int n = (int)((p.T + 127) / 128), tid = threadIdx.x;
+  int* count = lds;                                           // [256], then where a class begins
+  auto cls = [&](int i) {
+    const int4 v = p.rows[(int64_t)i * 128];
+    return 255 - (int)((int64_t)max(min(v.w, (int)p.T) - max(v.z, 0), 0) * 255 / p.T);
+  };
+  count[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += 256) atomicAdd(&count[cls(i)], 1);
+  __syncthreads();
+  int at = 0;
+  for (int i = 0; i < tid; ++i) at += count[i];
+  __syncthreads();
+  count[tid] = at;
+  __syncthreads();
+  for (int i = tid; i < n; i += 256) p.order[atomicAdd(&count[cls(i)], 1)] = i;
+}
+
 template <typename T, int DT, bool CAP, bool BIAS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(const AttnParams p) {
   typedef Tile<T, DT> L;
@@ -39,12 +77,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // blocks as in the forward pass
-  const int nq = (int)((p.T + 127) / 128), r = p.H / p.G, total = nq * p.H;
-  const int per_xcd = (total + 7) / 8, slot = (int)(blockIdx.x >> 3), n = (int)(blockIdx.x & 7) * per_xcd + slot;
-  if (slot >= per_xcd || n >= total) return;
-  const int gi = n / (nq * r), rem = n - gi * nq * r, qt = nq - 1 - rem / r;
-  const int h = p.head_order[gi * r + rem % r], g = p.head_group[h];
+  // blocks as in the forward pass, the parts of a walk next to each other; the last block sorts the other kernel's
+  const int nq = (int)((p.T + 127) / 128), r = p.H / p.G, gi = (int)blockIdx.x % p.G, turn = (int)blockIdx.x / p.G;
+  const int rest = turn / p.splits_q, part = turn - rest * p.splits_q;
+  if (rest == nq * r) {
+    sort_key_blocks(p, reinterpret_cast<int*>(lds));
+    return;
+  }
+  const int qt = nq - 1 - rest / r;
+  const int h = p.head_order[gi * r + rest % r], g = p.head_group[h];
 
   const int64_t q0 = (int64_t)qt * 128, t = q0 + 32 * w + (l & 31);
   const Span mine = Span::of(p.rows, p.causal, p.T, t);
@@ -61,8 +102,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
     if (tid == 0) again = 0;
   }
   __syncthreads();
-  const int first = __builtin_amdgcn_readfirstlane(min(min(span[0][0], span[1][0]), min(span[2][0], span[3][0])));
-  const int end = __builtin_amdgcn_readfirstlane(max(max(span[0][1], span[1][1]), max(span[2][1], span[3][1])));
+  int first = __builtin_amdgcn_readfirstlane(min(min(span[0][0], span[1][0]), min(span[2][0], span[3][0])));
+  int end = __builtin_amdgcn_readfirstlane(max(max(span[0][1], span[1][1]), max(span[2][1], span[3][1])));
+  if (p.splits_q > 1 && first < end) {                        // this part's tiles
+    const int64_t tiles = (end - first + 63) / 64;
+    const int from = first + 64 * (int)(tiles * part / p.splits_q), to = first + 64 * (int)(tiles * (part + 1) / p.splits_q);
+    first = from;
+    end = min(end, to);
+  }
 
   const T* K = static_cast<const T*>(p.k) + (int64_t)g * p.d;
   const T* V = static_cast<const T*>(p.v) + (int64_t)g * p.d;
@@ -98,7 +145,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   D = swap_sum(D);
   const float lse = p.lse[tr * p.H + h];
   const float lse2 = lse == -__builtin_inff() ? __builtin_inff() : kLog2e * lse;   // a row that sees nothing: p = 0
-  if (up == 0 && t < p.T) {
+  if (up == 0 && t < p.T && part == 0) {
     p.stat[(int64_t)h * p.T + t] = lse2;
     p.stat[((int64_t)p.H + h) * p.T + t] = D;
   }
@@ -145,6 +192,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
           L::rows(a, vt, 32 * i, x);
           mma(dp, a, af[x]);
         }
+        if constexpr (sizeof(T) == 2) reads_ahead<4 * DT, 2, 8>();
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const int off = 32 * i + 8 * (v >> 2) + (v & 3);
@@ -171,46 +219,33 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   __syncthreads();
   if (again) walk(std::true_type{});
   if (!mine.live) return;
-  T* out = static_cast<T*>(p.dq) + (t * p.H + h) * p.d;
-  const float sc = p.scale;
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int e = 32 * i + 8 * a + 4 * up;
-      if (e < p.d)
-        *reinterpret_cast<typename Four<T>::type*>(out + e) = Four<T>::of(o[i][4 * a] * sc, o[i][4 * a + 1] * sc, o[i][4 * a + 2] * sc, o[i][4 * a + 3] * sc);
-    }
+  put_rows<T, DT>(o, p.scale, p.dq, p.splits_q > 1 ? p.part_q + (int64_t)part * p.T * p.H * p.d : nullptr, (t * p.H + h) * p.d, p.d, up);
 }
 
-// A workgroup has 128 keys of a group, 32 a wave, and walks over tiles of 64 queries
-// of each of the group's heads; a lane holds one key.  bf16: 8 waves, of which two
-// share keys and take 32 queries of a tile each (their sums meet in LDS at the end),
-// and v's rows are read from LDS: dk, dv and k's rows leave no registers for them at
-// two waves a SIMD.  fp32: 4 waves, all of it in registers at one wave a SIMD.
+// A workgroup has 128 keys of a group, 32 a wave, and walks over tiles of 32 queries
+// of each of the group's heads; a lane holds one key.  dk, dv and k's rows stay in
+// registers and v's are read from LDS, which leaves two waves a SIMD for bf16: two
+// workgroups a CU, with no barrier in common, so that the products of one run under
+// the exponentials of the other (8 waves in one workgroup took 1.4 times as long).
 template <typename T, int DT, bool CAP, bool BIAS>
-__global__ __launch_bounds__(sizeof(T) == 2 ? 512 : 256) void attn_dkv_kernel(const AttnParams p) {
-  typedef Tile<T, DT> L;
-  constexpr bool SPLIT = sizeof(T) == 2;
-  constexpr int NW = SPLIT ? 8 : 4;
-  __shared__ __attribute__((aligned(512))) unsigned char lds[(SPLIT ? 6 : 4) * L::BYTES];   // Q, dA of two tiles; V
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(const AttnParams p) {
+  typedef Tile<T, DT, 32> L;                                  // queries
+  typedef Tile<T, DT> LV;                                     // keys
+  __shared__ __attribute__((aligned(512))) unsigned char lds[4 * L::BYTES + 2 * LV::BYTES];   // Q, dA of two tiles; V
   __shared__ __attribute__((aligned(16))) float stat[2][2][64];              // lse2, D
   __shared__ __attribute__((aligned(16))) int4 sees[2][64];
-  __shared__ __attribute__((aligned(16))) uint32_t seen[NW][64];             // of a wave's keys, by query
+  __shared__ __attribute__((aligned(16))) uint32_t seen[4][32];              // of a wave's keys, by query
   __shared__ int span[4][2];
-  __shared__ uint32_t bad[4], again;                                         // of Q, of dA
+  __shared__ uint32_t bad[4], again;                                         // of Q, of dA (two words each, the second 0)
   const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wk = w & 3, half = w >> 2;                        // keys; (SPLIT) queries of a tile
 
-  // blocks of an XCD are consecutive: the keys from the first on (with the longest columns), then the groups
-  const int nk = (int)((p.T + 127) / 128), total = nk * p.G;
-  const int per_xcd = (total + 7) / 8, slot = (int)(blockIdx.x >> 3), n = (int)(blockIdx.x & 7) * per_xcd + slot;
-  if (slot >= per_xcd || n >= total) return;
-  const int g = n / nk, k0 = (n - g * nk) * 128;
+  // the groups by turns, as in the forward pass; the longest columns first
+  const int g = (int)blockIdx.x % p.G, turn = (int)blockIdx.x / p.G, rank = turn / p.splits_k, part = turn - rank * p.splits_k;
+  const int k0 = 128 * (p.order ? p.order[rank] : rank);
   const int heads0 = p.group_start[g], heads = p.group_start[g + 1] - heads0;
 
-  const int64_t t = (int64_t)k0 + 32 * wk + (l & 31);
+  const int64_t t = (int64_t)k0 + 32 * w + (l & 31);
   bool live = t < p.T;
   int qfirst = 0, qend = 0;                                   // the queries that see this lane's key
   if (live) {
@@ -227,9 +262,9 @@ __global__ __launch_bounds__(sizeof(T) == 2 ? 512 : 256) void attn_dkv_kernel(co
   {
     const bool on = qfirst < qend;
     const int a = wave_min(on ? qfirst : INT32_MAX), b = wave_max(on ? qend : 0);
-    if (l == 0 && half == 0) {
-      span[wk][0] = a;
-      span[wk][1] = b;
+    if (l == 0) {
+      span[w][0] = a;
+      span[w][1] = b;
     }
     if (tid < 4) bad[tid] = 0;
     if (tid == 0) again = 0;
@@ -237,27 +272,23 @@ __global__ __launch_bounds__(sizeof(T) == 2 ? 512 : 256) void attn_dkv_kernel(co
   __syncthreads();
   const int first = __builtin_amdgcn_readfirstlane(min(min(span[0][0], span[1][0]), min(span[2][0], span[3][0])));
   const int end = __builtin_amdgcn_readfirstlane(max(max(span[0][1], span[1][1]), max(span[2][1], span[3][1])));
-  const int tiles = first < end ? (end - first + 63) / 64 : 0, steps = tiles * heads;
+  const int tiles = first < end ? (end - first + 31) / 32 : 0;
+  // this part of the heads' tiles
+  const int step0 = (int)((int64_t)tiles * heads * part / p.splits_k), steps = (int)((int64_t)tiles * heads * (part + 1) / p.splits_k);
 
   const int64_t ld_a = (int64_t)p.H * p.d;
   const uint32_t base = lds_addr(lds);
   const typename L::At lane0 = L::lane(base, l);
-  uint32_t qo[L::PERIOD], ao[L::PERIOD];                      // SPLIT: waves 0 .. 3 copy Q, 4 .. 7 dA
-  L::offsets(qo, wk, l, SPLIT && half ? ld_a : p.ld_q, p.d);
-  if constexpr (!SPLIT) L::offsets(ao, wk, l, ld_a, p.d);
+  uint32_t qo[L::PERIOD], ao[L::PERIOD];
+  L::offsets(qo, w, l, p.ld_q, p.d);
+  L::offsets(ao, w, l, ld_a, p.d);
   int ih = 0, it = 0;                                         // the copies' head and tile
   auto issue = [&](int buf) __attribute__((always_inline)) {
-    const int h = p.head_order[heads0 + ih], qb = first + 64 * it;
-    const T* q = static_cast<const T*>(p.q) + (int64_t)h * p.d;
-    const T* da = static_cast<const T*>(p.da) + (int64_t)h * p.d;
+    const int h = p.head_order[heads0 + ih], qb = first + 32 * it;
     const uint32_t to = base + (uint32_t)(buf * 2 * L::BYTES);
-    if constexpr (SPLIT) {
-      L::copy(half ? da : q, half ? ld_a : p.ld_q, p.d, qb, end, qo, to + (uint32_t)(half * L::BYTES), wk);
-    } else {
-      L::copy(q, p.ld_q, p.d, qb, end, qo, to, wk);
-      L::copy(da, ld_a, p.d, qb, end, ao, to + L::BYTES, wk);
-    }
-    const uint32_t left = (uint32_t)min(end - qb, 64);
+    L::copy(static_cast<const T*>(p.q) + (int64_t)h * p.d, p.ld_q, p.d, qb, end, qo, to, w);
+    L::copy(static_cast<const T*>(p.da) + (int64_t)h * p.d, ld_a, p.d, qb, end, ao, to + L::BYTES, w);
+    const uint32_t left = (uint32_t)min(end - qb, 32);
     if (w < 2) dma4s(uniform_rsrc(p.stat + ((int64_t)w * p.H + h) * p.T + qb, 4 * left), 4u * (uint32_t)l, lds_addr(stat[buf][w]));
     if (w == 2 && p.rows) dma16s(uniform_rsrc(p.rows + qb, 16 * left), 16u * (uint32_t)l, 0u, lds_addr(sees[buf]));
     if (++it == tiles) {
@@ -267,133 +298,118 @@ __global__ __launch_bounds__(sizeof(T) == 2 ? 512 : 256) void attn_dkv_kernel(co
   };
 
   const int64_t tr = min<int64_t>(t, p.T - 1);
-  typename L::Frag kf[2 * DT], vf[SPLIT ? 1 : 2 * DT];
+  typename L::Frag kf[2 * DT];
   const T* krow = static_cast<const T*>(p.k) + tr * p.ld_k + (int64_t)g * p.d;
 #pragma unroll
   for (int s = 0; s < 2 * DT; ++s) L::load(kf[s], krow, s, p.d, l);
-  if constexpr (SPLIT) {
-    uint32_t vo[L::PERIOD];
-    L::offsets(vo, wk, l, p.ld_v, p.d);
-    L::copy(static_cast<const T*>(p.v) + (int64_t)g * p.d, p.ld_v, p.d, k0 + 64 * half, p.T, vo, base + (uint32_t)((4 + half) * L::BYTES), wk);
-  } else {
-    const T* vrow = static_cast<const T*>(p.v) + tr * p.ld_v + (int64_t)g * p.d;
-#pragma unroll
-    for (int s = 0; s < 2 * DT; ++s) L::load(vf[s], vrow, s, p.d, l);
+  {
+    uint32_t vo[LV::PERIOD];
+    LV::offsets(vo, w, l, p.ld_v, p.d);
+    const T* v = static_cast<const T*>(p.v) + (int64_t)g * p.d;
+    LV::copy(v, p.ld_v, p.d, k0, p.T, vo, base + 4 * L::BYTES, w);
+    LV::copy(v, p.ld_v, p.d, k0 + 64, p.T, vo, base + 4 * L::BYTES + LV::BYTES, w);
   }
-  const typename L::At vt = L::move(lane0, (uint32_t)((4 + (wk >> 1)) * L::BYTES + (wk & 1) * 32 * L::PITCH));
+  const typename L::At vt = L::move(lane0, (uint32_t)(4 * L::BYTES + w * 32 * L::PITCH));
 
   f32x16 dk[DT], dv[DT];
   const float c1 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
   const float cap = kLog2e * p.cap;
-  const int kw = k0 + 32 * wk, kw_end = (int)min<int64_t>(kw + 32, p.T);
+  const int kw = k0 + 32 * w, kw_end = (int)min<int64_t>(kw + 32, p.T);
 
   // the walk over the queries, as in the forward pass: again and CAREFUL with q and
   // da where a sum is not finite
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
-    int buf = 0, head = 0, tile = 0;
-    ih = it = 0;
+    int buf = 0, head = tiles ? step0 / tiles : 0, tile = step0 - head * tiles;
+    ih = head;
+    it = tile;
 #pragma unroll
     for (int i = 0; i < DT; ++i) dk[i] = dv[i] = f32x16{};
-    if (steps > 0) issue(0);
-    for (int step = 0; step < steps; ++step, buf ^= 1) {
+    if (step0 < steps) issue(0);
+    for (int step = step0; step < steps; ++step, buf ^= 1) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (step + 1 < steps) issue(buf ^ 1);
-      const int h = p.head_order[heads0 + head], qb = first + 64 * tile;
+      const int h = p.head_order[heads0 + head], qb = first + 32 * tile;
       if (++tile == tiles) {
         tile = 0;
         ++head;
       }
       const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
       const typename L::At qt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), at = L::move(qt, L::BYTES);
-      uint32_t bad_q[2] = {0, 0}, bad_a[2] = {0, 0};
+      uint32_t bad_q = 0, bad_a = 0;
       if constexpr (CAREFUL) {
-        L::find_bad(lds + buf * 2 * L::BYTES, tid, 64 * NW, bad);
-        L::find_bad(lds + buf * 2 * L::BYTES + L::BYTES, tid, 64 * NW, bad + 2);
+        L::find_bad(lds + buf * 2 * L::BYTES, tid, 256, bad);
+        L::find_bad(lds + buf * 2 * L::BYTES + L::BYTES, tid, 256, bad + 2);
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          bad_q[i] = __builtin_amdgcn_readfirstlane(bad[i]);
-          bad_a[i] = __builtin_amdgcn_readfirstlane(bad[2 + i]);
-        }
+        bad_q = __builtin_amdgcn_readfirstlane(bad[0]);
+        bad_a = __builtin_amdgcn_readfirstlane(bad[2]);
         __syncthreads();
         if (tid < 4) bad[tid] = 0;
       }
-      // what query l of the tile sees: its keys [x, y)
+      // what query l & 31 of the tile sees: its keys [x, y)
       int2 sq;
       if (p.rows) {
-        sq = *reinterpret_cast<const int2*>(&sees[buf][l]);      // zeros behind the last query
+        sq = *reinterpret_cast<const int2*>(&sees[buf][l & 31]);  // zeros behind the last query
         if (sq.x < 0) sq.y = 0;
       } else {
-        sq = make_int2(0, qb + l < p.T ? (p.causal ? qb + l + 1 : (int)p.T) : 0);
+        const int q = qb + (l & 31);
+        sq = make_int2(0, q < p.T ? (p.causal ? q + 1 : (int)p.T) : 0);
       }
-      const bool mine = !SPLIT || up == half;
-      if (!__any(mine && sq.x < kw_end && sq.y > kw)) continue;
-      const bool whole = __all(!mine || (sq.x <= kw && sq.y >= kw_end));
+      if (!__any(sq.x < kw_end && sq.y > kw)) continue;
+      const bool whole = __all(sq.x <= kw && sq.y >= kw_end);
       if (!whole || CAREFUL) {
         const uint32_t a = (uint32_t)min(max(sq.x - kw, 0), 32), b = (uint32_t)min(max(sq.y - kw, 0), 32);
-        seen[w][l] = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
+        seen[w][l & 31] = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
       }
       const float from = (float)((int)t - qb - 4 * up);
-      auto block = [&](int i) __attribute__((always_inline)) {     // queries 32 i .. of the tile
-        f32x16 s = {}, dp = {};
+      f32x16 s = {}, dp = {};
 #pragma unroll
-        for (int x = 0; x < 2 * DT; ++x) {
-          typename L::Frag a, b;
-          L::rows(a, qt, 32 * i, x);
-          mma(s, a, kf[x]);
-          L::rows(a, at, 32 * i, x);
-          if constexpr (SPLIT) {
-            L::rows(b, vt, 0, x);
-            mma(dp, a, b);
-          } else {
-            mma(dp, a, vf[x]);
-          }
+      for (int x = 0; x < 2 * DT; ++x) {
+        typename L::Frag a, b;
+        L::rows(a, qt, 0, x);
+        mma(s, a, kf[x]);
+        L::rows(a, at, 0, x);
+        L::rows(b, vt, 0, x);
+        mma(dp, a, b);
+      }
+      if constexpr (sizeof(T) == 2) reads_ahead<6 * DT, 3, 9>();
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int q = 8 * a + 4 * up;
+        const float4 l4 = *reinterpret_cast<const float4*>(&stat[buf][0][q]), d4 = *reinterpret_cast<const float4*>(&stat[buf][1][q]);
+        const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, D[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 4 * a + e;
+          float bent = 1.f;
+          const float y = score<T, CAP, BIAS>(s[v], c1, cap, slope, from - (float)(8 * a + e), bent);
+          const float pr = __builtin_amdgcn_exp2f(y - ls[e]);
+          float ds = pr * (dp[v] - D[e]);
+          if constexpr (CAP) ds *= bent;
+          dp[v] = pr;
+          s[v] = ds;
         }
+      }
+      if (!whole) {
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-          const int q = 32 * i + 8 * a + 4 * up;
-          const float4 l4 = *reinterpret_cast<const float4*>(&stat[buf][0][q]), d4 = *reinterpret_cast<const float4*>(&stat[buf][1][q]);
-          const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, D[4] = {d4.x, d4.y, d4.z, d4.w};
+          const uint4 m4 = *reinterpret_cast<const uint4*>(&seen[w][8 * a + 4 * up]);
+          const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int v = 4 * a + e;
-            float bent = 1.f;
-            const float y = score<T, CAP, BIAS>(s[v], c1, cap, slope, from - (float)(32 * i + 8 * a + e), bent);
-            const float pr = __builtin_amdgcn_exp2f(y - ls[e]);
-            float ds = pr * (dp[v] - D[e]);
-            if constexpr (CAP) ds *= bent;
-            dp[v] = pr;
-            s[v] = ds;
+            const bool on = (m[e] >> (l & 31)) & 1;
+            dp[4 * a + e] = on ? dp[4 * a + e] : 0.f;
+            s[4 * a + e] = on ? s[4 * a + e] : 0.f;
           }
         }
-        if (!whole) {
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const uint4 m4 = *reinterpret_cast<const uint4*>(&seen[w][32 * i + 8 * a + 4 * up]);
-            const uint32_t m[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool on = (m[e] >> (l & 31)) & 1;
-              dp[4 * a + e] = on ? dp[4 * a + e] : 0.f;
-              s[4 * a + e] = on ? s[4 * a + e] : 0.f;
-            }
-          }
-        }
-        L::template along<CAREFUL>(dv, at, 32 * i, dp, l);
-        L::template along<CAREFUL>(dk, qt, 32 * i, s, l);
-        if constexpr (CAREFUL) {
-          auto on = [&](int x) { return ((seen[w][32 * i + x] >> (l & 31)) & 1) != 0; };
-          add_bad_rows<T, DT>(dv, dp, i ? bad_a[1] : bad_a[0], p.d, l, [&](int x) { return static_cast<const T*>(p.da) + (int64_t)(qb + 32 * i + x) * ld_a + (int64_t)h * p.d; }, on);
-          add_bad_rows<T, DT>(dk, s, i ? bad_q[1] : bad_q[0], p.d, l, [&](int x) { return static_cast<const T*>(p.q) + (int64_t)(qb + 32 * i + x) * p.ld_q + (int64_t)h * p.d; }, on);
-        }
-      };
-      if constexpr (SPLIT) {
-        block(half);
-      } else {
-        block(0);
-        block(1);
+      }
+      L::template along<CAREFUL>(dv, at, 0, dp, l);
+      L::template along<CAREFUL>(dk, qt, 0, s, l);
+      if constexpr (CAREFUL) {
+        auto on = [&](int x) { return ((seen[w][x] >> (l & 31)) & 1) != 0; };
+        add_bad_rows<T, DT>(dv, dp, bad_a, p.d, l, [&](int x) { return static_cast<const T*>(p.da) + (int64_t)(qb + x) * ld_a + (int64_t)h * p.d; }, on);
+        add_bad_rows<T, DT>(dk, s, bad_q, p.d, l, [&](int x) { return static_cast<const T*>(p.q) + (int64_t)(qb + x) * p.ld_q + (int64_t)h * p.d; }, on);
       }
     }
   };
@@ -403,55 +419,64 @@ __global__ __launch_bounds__(sizeof(T) == 2 ? 512 : 256) void attn_dkv_kernel(co
   __syncthreads();
   if (again) walk(std::true_type{});
 
-  const float sc = p.scale;
-  auto put = [&](f32x16 (&x)[DT], void* to, float by) __attribute__((always_inline)) {
-    if constexpr (SPLIT) {
-      // the second half's sums to the first, through the stages
-      constexpr int OP = 32 * DT + 4;
-      static_assert(4 * 32 * OP * 4 <= 6 * L::BYTES, "the sums of four waves fit");
-      float* o = reinterpret_cast<float*>(lds) + (wk * 32 + (l & 31)) * OP;
-      __syncthreads();
-      if (half) {
+  if (!live) return;
+  const int64_t at = (t * p.G + g) * p.d, plane = p.T * p.G * p.d;
+  float* parts = p.splits_k > 1 ? p.part_k + 2 * part * plane : nullptr;
+  put_rows<T, DT>(dk, p.scale, p.dk, parts, at, p.d, up);
+  put_rows<T, DT>(dv, 1.f, p.dv, parts ? parts + plane : nullptr, at, p.d, up);
+}
+
+// the parts' sums added in order: four elements a thread, of dq, then dk, then dv.  (Walks
+// are cut where there are few: fewer than 2^31 elements.)
+template <typename T>
+__global__ __launch_bounds__(256) void attn_add_parts_kernel(const AttnParams p, uint32_t nq4, uint32_t nk4) {
+  uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const float* part;
+  void* out;
+  uint32_t step, row4;
+  int splits;
+  if (i < nq4) {
+    part = p.part_q;
+    out = p.dq;
+    splits = p.splits_q;
+    step = nq4;
+    row4 = p.H * p.d / 4;
+  } else if (i < nq4 + 2 * nk4) {
+    i -= nq4;
+    const bool v = i >= nk4;
+    if (v) i -= nk4;
+    part = p.part_k + (v ? 4 * (size_t)nk4 : 0);
+    out = v ? p.dv : p.dk;
+    splits = p.splits_k;
+    step = 2 * nk4;
+    row4 = p.G * p.d / 4;
+  } else {
+    return;
+  }
+  const float4* x = reinterpret_cast<const float4*>(part) + i;
+  float4 y[8];                                                // splits <= 8
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
+  for (int k = 0; k < 8; ++k) y[k] = x[(size_t)min(k, splits - 1) * step];
+  if (p.rows && p.rows[i / row4].x < 0) return;               // a token of no document
+  float4 s = y[0];
 #pragma unroll
-          for (int a = 0; a < 4; ++a)
-            *reinterpret_cast<float4*>(o + 32 * i + 8 * a + 4 * up) = make_float4(x[i][4 * a], x[i][4 * a + 1], x[i][4 * a + 2], x[i][4 * a + 3]);
-      }
-      __syncthreads();
-      if (half) return;
-#pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const float4 v = *reinterpret_cast<const float4*>(o + 32 * i + 8 * a + 4 * up);
-          x[i][4 * a] += v.x;
-          x[i][4 * a + 1] += v.y;
-          x[i][4 * a + 2] += v.z;
-          x[i][4 * a + 3] += v.w;
-        }
-    }
-    if (!live) return;
-    T* out = static_cast<T*>(to) + (t * p.G + g) * p.d;
-#pragma unroll
-    for (int i = 0; i < DT; ++i)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int e = 32 * i + 8 * a + 4 * up;
-        if (e < p.d) *reinterpret_cast<typename Four<T>::type*>(out + e) = Four<T>::of(x[i][4 * a] * by, x[i][4 * a + 1] * by, x[i][4 * a + 2] * by, x[i][4 * a + 3] * by);
-      }
-  };
-  put(dk, p.dk, sc);
-  put(dv, p.dv, 1.f);
+  for (int k = 1; k < 8; ++k)
+    if (k < splits) s = make_float4(s.x + y[k].x, s.y + y[k].y, s.z + y[k].z, s.w + y[k].w);
+  reinterpret_cast<typename Four<T>::type*>(out)[i] = Four<T>::of(s.x, s.y, s.z, s.w);
 }
 
 template <typename T, int DT, bool CAP, bool BIAS>
 hipError_t launch_one(const AttnParams& p, hipStream_t st) {
-  const int64_t blocks = (p.T + 127) / 128, nq = blocks * p.H, nk = blocks * p.G;
-  hipLaunchKernelGGL((attn_dq_kernel<T, DT, CAP, BIAS>), dim3((unsigned)(8 * ((nq + 7) / 8))), dim3(256), 0, st, p);
+  // one block more than dq's, if the other kernel's are to be sorted
+  const int64_t blocks = (p.T + 127) / 128, nq = blocks * p.H * p.splits_q, nk = blocks * p.G * p.splits_k;
+  hipLaunchKernelGGL((attn_dq_kernel<T, DT, CAP, BIAS>), dim3((unsigned)(nq + (p.order ? 1 : 0))), dim3(256), 0, st, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_dkv_kernel<T, DT, CAP, BIAS>), dim3((unsigned)(8 * ((nk + 7) / 8))), dim3(sizeof(T) == 2 ? 512 : 256), 0, st, p);
+  hipLaunchKernelGGL((attn_dkv_kernel<T, DT, CAP, BIAS>), dim3((unsigned)nk), dim3(256), 0, st, p);
+  e = hipGetLastError();
+  if (e != hipSuccess || (p.splits_q == 1 && p.splits_k == 1)) return e;
+  const int64_t nq4 = p.splits_q > 1 ? p.T * p.H * p.d / 4 : 0, nk4 = p.splits_k > 1 ? p.T * p.G * p.d / 4 : 0;
+  hipLaunchKernelGGL(attn_add_parts_kernel<T>, dim3((unsigned)((nq4 + 2 * nk4 + 255) / 256)), dim3(256), 0, st, p, (uint32_t)nq4, (uint32_t)nk4);
   return hipGetLastError();
 }
 template <typename T, int DT>
@@ -468,6 +493,17 @@ hipError_t launch_t(const AttnParams& p, hipStream_t st) {
 }
 
 }  // namespace
+
+// Workgroups that share the walk of 128 queries of a head, and of 128 keys of a group:
+// a walk over a long document is a chain of steps (2.6 us each over 64 keys, 1.8 us over 32
+// queries), so where the blocks leave CUs idle it is cut into parts of 4 steps and more.
+// 2047 tokens in ragged documents of up to 1258, 16 heads of 96 in 8 groups: 99 us with 2 and 4
+// parts, 192 without.
+AttnSplits attention_splits(int64_t T, int H, int G) {
+  const int64_t blocks = (T + 127) / 128;
+  auto parts = [&](int64_t walks, int64_t steps) { return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(walks, 1), steps / 4, 8})); };
+  return {parts(blocks * H, (T + 63) / 64), parts(blocks * G, (T + 31) / 32 * (H / G))};
+}
 
 hipError_t launch_attention_backward(const AttnParams& p, int bf16, hipStream_t st) {
   if (p.T == 0) return hipSuccess;

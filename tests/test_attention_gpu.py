@@ -355,11 +355,13 @@ def test_captured(hna):
     rows = torch.empty(T, 4, dtype=torch.int32, device="cuda")
     out = [torch.empty(T, H, d, dtype=BF16, device="cuda"), torch.empty(T, H, device="cuda")]
     grads = [torch.empty(T, x, d, dtype=BF16, device="cuda") for x in (H, G, G)]
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    dims = hna.hna_attn_dims(T, H * d, G * d, G * d, H, G, d, hna.HNA_BF16, 1, d ** -0.5, 0.0)
+    ws = torch.empty(hna.attention_workspace_bytes(dims), dtype=torch.uint8, device="cuda")
     qs, ks, vs = cache(1, 3000, H, G, d, BF16)
     n = i32([2900])
     one = [torch.empty(1, H, d, dtype=BF16, device="cuda"), torch.empty(1, H, device="cuda")]
-    ws2 = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    sdims = hna.hna_step_dims(1, G * d, G * d, 0, 0, 3000, H, G, d, hna.HNA_BF16, d ** -0.5, 0.0)
+    ws2 = torch.empty(hna.attention_step_workspace_bytes(sdims), dtype=torch.uint8, device="cuda")
 
     def step():
         hna.attention_rows(T, starts, rows=rows)
