@@ -19,7 +19,7 @@ from ._binding import (HnaError, HNA_BF16, HNA_F32, HNA_ACCUMULATE, hna_dims, hn
                        attention_rows, attention, attention_backward, attention_workspace_bytes,
                        attention_step, attention_step_workspace_bytes)
 from .pipeline import (AffinityPass, StackPass, FfnInputs, pass_for_layer, affinity_layer,
-                       ffn_inputs)
+                       ffn_inputs, layer_inputs)
 
 __all__ = [
     "HnaError", "HNA_BF16", "HNA_F32", "HNA_ACCUMULATE", "hna_dims", "hna_down_dims", "make_dims",
@@ -31,7 +31,7 @@ __all__ = [
     "neuron_step", "head_step", "layout_search", "DUAL_ITERS", "loo_workspace_bytes",
     "affinity_loo", "static_scratch_bytes", "affinity_up_static", "mfma_rate_probe",
     "hna_norm_dims", "block_norm", "block_norm_quant", "block_norm_backward",
-    "block_norm_workspace_bytes", "quant_pitch", "quant_rows", "quant_matmul", "quant_matmul_pair", "FfnInputs", "ffn_inputs",
+    "block_norm_workspace_bytes", "quant_pitch", "quant_rows", "quant_matmul", "quant_matmul_pair", "FfnInputs", "ffn_inputs", "layer_inputs",
     "hna_ffn_dims", "gated_ffn", "gated_ffn_backward", "gated_ffn_workspace_bytes",
     "hna_attn_dims", "hna_step_dims", "attention_rows", "attention", "attention_backward",
     "attention_workspace_bytes", "attention_step", "attention_step_workspace_bytes",

@@ -153,6 +153,30 @@ class FfnInputs:
         return ffn_inputs(x, self.gamma, self.w_gate, self.w_up, y=y, eps=self.eps, dtype=self.dtype, **step)
 
 
+def layer_inputs(x, q, k, v, w_o, gamma, W_gate, W_up, rows=None, w_down=None, *, causal: bool = True,
+                 scale: Optional[float] = None, cap: float = 0.0, slopes=None,
+                 group_of_head: Optional[Sequence[int]] = None, eps: float = 1e-6) -> Dict[str, torch.Tensor]:
+    """What the affinity pass reads of a layer, from the residual x [T, hidden] before its attention
+    and the heads' q [T, H, d], k, v [T, G, d]: attention (rows, causal, scale, cap and slopes as for
+    attention), its projection by the 8-bit W_o (a (rows, scales) pair of quant_rows), the norm step,
+    and the FFN's pre-activations in the type of W_gate and W_up.
+
+    Returns a [T, H, d], x_in, r, g and u under the names a layer dict of AffinityPass has them, and n,
+    the normed FFN input; with w_down, a pair of quant_rows of W_down [hidden, I], also h = silu(g) u
+    and r_next, the rms of the residual behind the FFN.
+    """
+    a, _ = B.attention(q, k, v, rows, causal=causal, scale=scale, cap=cap, slopes=slopes, group_of_head=group_of_head)
+    dtype = W_gate.dtype
+    y = B.quant_matmul(*B.quant_rows(a.view(a.shape[0], -1)), *w_o, dtype=dtype)
+    x_in, n, r, _ = B.block_norm(x, y, gamma, eps=eps)
+    g, u, h = B.gated_ffn(n, W_gate, W_up, want_h=w_down is not None)
+    out = {"a": a, "x_in": x_in, "r": r, "n": n, "g": g, "u": u}
+    if w_down is not None:
+        z = B.quant_matmul(*B.quant_rows(h), *w_down, dtype=dtype)
+        out.update(h=h, r_next=B.block_norm(x_in, z, eps=eps)[2])
+    return out
+
+
 class StackPass:
     """The affinity pass over an N-layer stack (section 3, "Affinity scores").
 
