@@ -237,6 +237,33 @@ __device__ inline __attribute__((always_inline)) void reads_ahead() {
   __builtin_amdgcn_sched_group_barrier(0x008, 2 * A / STEP, 0);
 }
 
+// A lane's column times `by`, as a row of out (the two lanes of a column exchange
+// halves, so that each stores 16 bytes in bf16), or as fp32 sums of a part
+template <typename T, int DT>
+__device__ inline void put_rows(const f32x16 (&x)[DT], float by, void* out, float* part, int64_t at, int d, int up, bool live) {
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int a = 0; a < 4; a += 2) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = x[i][4 * a + e] * by;
+      const int first = 32 * i + 8 * a;                       // 16 elements: d is a multiple of 16
+      if (part || sizeof(T) == 4) {
+        float* to = part ? part : static_cast<float*>(out);
+        if (live && first < d) {
+          *reinterpret_cast<float4*>(to + at + first + 4 * up) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(to + at + first + 8 + 4 * up) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      } else {
+        const auto s0 = __builtin_amdgcn_permlane32_swap(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[4], v[5]), false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(pack_bf16x2(v[2], v[3]), pack_bf16x2(v[6], v[7]), false, false);
+        if (live && first < d)
+          *reinterpret_cast<uint4*>(static_cast<__bf16*>(out) + at + first + 8 * up) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+      }
+    }
+}
+
 // joined over the two lanes that hold a column's rows
 __device__ inline float swap_max(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);

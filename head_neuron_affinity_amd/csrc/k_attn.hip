@@ -75,9 +75,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
 
   f32x16 o[DT];
   float m, sum;
-  const float c1 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+  const bool capped = sizeof(T) == 2 ? CAP : p.cap > 0.f;
+  const float c1 = capped ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
   const float cap = kLog2e * p.cap;
-  const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
+  const float slope = BIAS && p.slopes ? kLog2e * p.slopes[h] : 0.f;
 
   // The walk over the keys.  A value that a query does not see must not reach it as 0
   // times a NaN: where a sum is not finite at the end, the walk is made again with
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
             float x = s[i][v] * c1;
-            if constexpr (CAP) x = cap * tanh_of<T>(x);
+            if (CAP && capped) x = cap * tanh_of<T>(x);
             if constexpr (BIAS) x = fmaf(-slope, fabsf(at - (float)(32 * i + 8 * (v >> 2) + (v & 3))), x);
             s[i][v] = x;
           }
@@ -180,18 +181,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
   if (again) walk(std::true_type{});
 
   sum = swap_sum(sum);
-  if (!mine.live) return;
-  if (p.lse && up == 0) p.lse[t * p.H + h] = sum == 0.f ? -__builtin_inff() : kLn2 * (m + __builtin_amdgcn_logf(sum));
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-  T* out = static_cast<T*>(p.a) + (t * p.H + h) * p.d;
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int e = 32 * i + 8 * a + 4 * up;
-      if (e < p.d)
-        *reinterpret_cast<typename Four<T>::type*>(out + e) = Four<T>::of(o[i][4 * a] * inv, o[i][4 * a + 1] * inv, o[i][4 * a + 2] * inv, o[i][4 * a + 3] * inv);
-    }
+  if (p.lse && up == 0 && mine.live) p.lse[t * p.H + h] = sum == 0.f ? -__builtin_inff() : kLn2 * (m + __builtin_amdgcn_logf(sum));
+  put_rows<T, DT>(o, sum == 0.f ? 0.f : 1.0f / sum, p.a, nullptr, (t * p.H + h) * p.d, p.d, up, mine.live);
 }
 
 // rows[t]: the document of t by bisection of its starts, then the interval of keys
@@ -226,8 +217,10 @@ hipError_t launch_one(const AttnParams& p, hipStream_t st) {
 }
 template <typename T, int DT>
 hipError_t launch_dt(const AttnParams& p, hipStream_t st) {
-  if (p.cap > 0.f) return p.slopes ? launch_one<T, DT, true, true>(p, st) : launch_one<T, DT, true, false>(p, st);
-  return p.slopes ? launch_one<T, DT, false, true>(p, st) : launch_one<T, DT, false, false>(p, st);
+  // (fp32, whose products take 16 times as long, has one variant that looks at cap and slopes itself)
+  if constexpr (sizeof(T) == 4) return launch_one<T, DT, true, true>(p, st);
+  else if (p.cap > 0.f) return p.slopes ? launch_one<T, DT, true, true>(p, st) : launch_one<T, DT, true, false>(p, st);
+  else return p.slopes ? launch_one<T, DT, false, true>(p, st) : launch_one<T, DT, false, false>(p, st);
 }
 template <typename T>
 hipError_t launch_t(const AttnParams& p, hipStream_t st) {

@@ -21,30 +21,15 @@ using namespace attn;
 
 // score in powers of two, and (CAP) the cap's slope, of a product x
 template <typename T, bool CAP, bool BIAS>
-__device__ inline float score(float x, float c1, float cap, float slope, float distance, float& bent) {
+__device__ inline float score(float x, float c1, bool capped, float cap, float slope, float distance, float& bent) {
   x *= c1;
-  if constexpr (CAP) {
+  if (CAP && capped) {
     const float t = tanh_of<T>(x);
     bent = fmaf(-t, t, 1.0f);
     x = cap * t;
   }
   if constexpr (BIAS) x = fmaf(-slope, fabsf(distance), x);
   return x;
-}
-
-// a lane's column, as a row of out, or as fp32 sums of a part
-template <typename T, int DT>
-__device__ inline void put_rows(const f32x16 (&x)[DT], float by, void* out, float* part, int64_t at, int d, int up) {
-#pragma unroll
-  for (int i = 0; i < DT; ++i)
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int e = 32 * i + 8 * a + 4 * up;
-      if (e >= d) continue;
-      const float v[4] = {x[i][4 * a] * by, x[i][4 * a + 1] * by, x[i][4 * a + 2] * by, x[i][4 * a + 3] * by};
-      if (part) *reinterpret_cast<float4*>(part + at + e) = make_float4(v[0], v[1], v[2], v[3]);
-      else *reinterpret_cast<typename Four<T>::type*>(static_cast<T*>(out) + at + e) = Four<T>::of(v[0], v[1], v[2], v[3]);
-    }
 }
 
 // The blocks of 128 keys by the queries that see their first key, the most first
@@ -151,9 +136,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   }
 
   f32x16 o[DT];
-  const float c1 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+  const bool capped = sizeof(T) == 2 ? CAP : p.cap > 0.f;
+  const float c1 = capped ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
   const float cap = kLog2e * p.cap;
-  const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
+  const float slope = BIAS && p.slopes ? kLog2e * p.slopes[h] : 0.f;
 
   // the walk over the keys, as in the forward pass: again and CAREFUL with the keys
   // where a sum is not finite
@@ -197,7 +183,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
         for (int v = 0; v < 16; ++v) {
           const int off = 32 * i + 8 * (v >> 2) + (v & 3);
           float bent = 1.f;
-          const float y = score<T, CAP, BIAS>(s[v], c1, cap, slope, at - (float)off, bent);
+          const float y = score<T, CAP, BIAS>(s[v], c1, capped, cap, slope, at - (float)off, bent);
           float ds = __builtin_amdgcn_exp2f(y - lse2) * (dp[v] - D);
           if constexpr (CAP) ds *= bent;
           s[v] = ds;
@@ -218,8 +204,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   if (__any(mine.live && z != z)) again = 1;
   __syncthreads();
   if (again) walk(std::true_type{});
-  if (!mine.live) return;
-  put_rows<T, DT>(o, p.scale, p.dq, p.splits_q > 1 ? p.part_q + (int64_t)part * p.T * p.H * p.d : nullptr, (t * p.H + h) * p.d, p.d, up);
+  put_rows<T, DT>(o, p.scale, p.dq, p.splits_q > 1 ? p.part_q + (int64_t)part * p.T * p.H * p.d : nullptr, (t * p.H + h) * p.d, p.d, up, mine.live);
 }
 
 // A workgroup has 128 keys of a group, 32 a wave, and walks over tiles of 32 queries
@@ -312,7 +297,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
   const typename L::At vt = L::move(lane0, (uint32_t)(4 * L::BYTES + w * 32 * L::PITCH));
 
   f32x16 dk[DT], dv[DT];
-  const float c1 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+  const bool capped = sizeof(T) == 2 ? CAP : p.cap > 0.f;
+  const float c1 = capped ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
   const float cap = kLog2e * p.cap;
   const int kw = k0 + 32 * w, kw_end = (int)min<int64_t>(kw + 32, p.T);
 
@@ -335,7 +321,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
         tile = 0;
         ++head;
       }
-      const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
+      const float slope = BIAS && p.slopes ? kLog2e * p.slopes[h] : 0.f;
       const typename L::At qt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), at = L::move(qt, L::BYTES);
       uint32_t bad_q = 0, bad_a = 0;
       if constexpr (CAREFUL) {
@@ -383,7 +369,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
         for (int e = 0; e < 4; ++e) {
           const int v = 4 * a + e;
           float bent = 1.f;
-          const float y = score<T, CAP, BIAS>(s[v], c1, cap, slope, from - (float)(8 * a + e), bent);
+          const float y = score<T, CAP, BIAS>(s[v], c1, capped, cap, slope, from - (float)(8 * a + e), bent);
           const float pr = __builtin_amdgcn_exp2f(y - ls[e]);
           float ds = pr * (dp[v] - D[e]);
           if constexpr (CAP) ds *= bent;
@@ -419,11 +405,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
   __syncthreads();
   if (again) walk(std::true_type{});
 
-  if (!live) return;
   const int64_t at = (t * p.G + g) * p.d, plane = p.T * p.G * p.d;
   float* parts = p.splits_k > 1 ? p.part_k + 2 * part * plane : nullptr;
-  put_rows<T, DT>(dk, p.scale, p.dk, parts, at, p.d, up);
-  put_rows<T, DT>(dv, 1.f, p.dv, parts ? parts + plane : nullptr, at, p.d, up);
+  put_rows<T, DT>(dk, p.scale, p.dk, parts, at, p.d, up, live);
+  put_rows<T, DT>(dv, 1.f, p.dv, parts ? parts + plane : nullptr, at, p.d, up, live);
 }
 
 // the parts' sums added in order: four elements a thread, of dq, then dk, then dv.  (Walks
@@ -481,8 +466,10 @@ hipError_t launch_one(const AttnParams& p, hipStream_t st) {
 }
 template <typename T, int DT>
 hipError_t launch_dt(const AttnParams& p, hipStream_t st) {
-  if (p.cap > 0.f) return p.slopes ? launch_one<T, DT, true, true>(p, st) : launch_one<T, DT, true, false>(p, st);
-  return p.slopes ? launch_one<T, DT, false, true>(p, st) : launch_one<T, DT, false, false>(p, st);
+  // (fp32, whose products take 16 times as long, has one variant that looks at cap and slopes itself)
+  if constexpr (sizeof(T) == 4) return launch_one<T, DT, true, true>(p, st);
+  else if (p.cap > 0.f) return p.slopes ? launch_one<T, DT, true, true>(p, st) : launch_one<T, DT, true, false>(p, st);
+  else return p.slopes ? launch_one<T, DT, false, true>(p, st) : launch_one<T, DT, false, false>(p, st);
 }
 template <typename T>
 hipError_t launch_t(const AttnParams& p, hipStream_t st) {

@@ -81,9 +81,10 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
   const T* qrow = static_cast<const T*>(p.q) + (b * p.H + h) * p.d;
 #pragma unroll
   for (int s = 0; s < 2 * DT; ++s) L::load(qf[s], qrow, s, p.d, l);
-  const float c1 = CAP ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+  const bool capped = sizeof(T) == 2 ? CAP : p.cap > 0.f;
+  const float c1 = capped ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
   const float cap = kLog2e * p.cap;
-  const float slope = BIAS ? kLog2e * p.slopes[h] : 0.f;
+  const float slope = BIAS && p.slopes ? kLog2e * p.slopes[h] : 0.f;
 
   f32x16 o[DT];
 #pragma unroll
@@ -109,7 +110,7 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
     for (int v = 0; v < 16; ++v) {
       const int off = 8 * (v >> 2) + (v & 3);
       float x = s[v] * c1;
-      if constexpr (CAP) x = cap * tanh_of<T>(x);
+      if (CAP && capped) x = cap * tanh_of<T>(x);
       if constexpr (BIAS) x = fmaf(-slope, at - (float)off, x);
       x = off < left ? x : -__builtin_inff();
       s[v] = x;
@@ -220,8 +221,10 @@ hipError_t launch_one(const StepParams& p, hipStream_t st) {
 }
 template <typename T, int DT>
 hipError_t launch_dt(const StepParams& p, hipStream_t st) {
-  if (p.cap > 0.f) return p.slopes ? launch_one<T, DT, true, true>(p, st) : launch_one<T, DT, true, false>(p, st);
-  return p.slopes ? launch_one<T, DT, false, true>(p, st) : launch_one<T, DT, false, false>(p, st);
+  // (fp32, whose products take 16 times as long, has one variant that looks at cap and slopes itself)
+  if constexpr (sizeof(T) == 4) return launch_one<T, DT, true, true>(p, st);
+  else if (p.cap > 0.f) return p.slopes ? launch_one<T, DT, true, true>(p, st) : launch_one<T, DT, true, false>(p, st);
+  else return p.slopes ? launch_one<T, DT, false, true>(p, st) : launch_one<T, DT, false, false>(p, st);
 }
 template <typename T>
 hipError_t launch_t(const StepParams& p, hipStream_t st) {
