@@ -290,6 +290,52 @@ __device__ inline float tanh_of(float y) {
   }
 }
 
+// Streams of a wave's own: 32 keys at a time in two stages, no barriers.  Waves that
+// have room for them in LDS (four in 128 KB, or two).
+template <typename T, int DT>
+constexpr int kStreamWaves = Tile<T, DT>::BYTES * 8 <= 128 * 1024 ? 4 : 2;
+template <typename T, int DT>
+struct Stream {
+  typedef Tile<T, DT, 32> L;
+  static constexpr int CP = L::BYTES / 1024, PERIOD = 16 / L::RPC > 1 ? 16 / L::RPC : 1;
+  static constexpr int REGION = 4 * L::BYTES;              // K, V of two stages
+  static constexpr int WAIT = 2 * CP;                      // copies of a stage
+  const T *K, *V;
+  int64_t ld_k, ld_v;
+  int d, end;
+  uint32_t base, ko[PERIOD], vo[PERIOD];                   // copy i of 32 rows: rows RPC i .., f repeats every 16 rows
+  __device__ inline void init(const T* k, const T* v, int64_t ldk, int64_t ldv, int dd, int last, uint32_t lds, int l) {
+    K = k;
+    V = v;
+    ld_k = ldk;
+    ld_v = ldv;
+    d = dd;
+    end = last;
+    base = lds;
+#pragma unroll
+    for (int i = 0; i < PERIOD; ++i) {
+      const int r = i * L::RPC + l / L::CPR, c = (l % L::CPR) ^ L::f(r);
+      const bool on = 16 * c < d * L::E;
+      ko[i] = on ? (uint32_t)(r * ld_k * L::E) + 16u * (uint32_t)c : kOutOfRange;
+      vo[i] = on ? (uint32_t)(r * ld_v * L::E) + 16u * (uint32_t)c : kOutOfRange;
+    }
+  }
+  __device__ inline void one(const T* x, int64_t ld, const uint32_t (&voff)[PERIOD], int kb, uint32_t to) const {
+#pragma unroll
+    for (int i = 0; i < CP; i += PERIOD) {
+      const int64_t from = kb + i * L::RPC, bytes = ((end - 1 - from) * ld + d) * L::E;
+      const u32x4 rs = uniform_rsrc(x + (end > from ? from * ld : 0), end <= from ? 0u : bytes > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)bytes);
+#pragma unroll
+      for (int j = 0; j < PERIOD; ++j) dma16s(rs, voff[j], 0u, to + (uint32_t)((i + j) * 1024));
+    }
+  }
+  // keys kb .. kb + 31 (zeros from `end` on) into stage buf
+  __device__ inline void issue(int kb, int buf) const {
+    one(K, ld_k, ko, kb, base + (uint32_t)(buf * 2 * L::BYTES));
+    one(V, ld_v, vo, kb, base + (uint32_t)(buf * 2 * L::BYTES + L::BYTES));
+  }
+};
+
 // asynchronous 4-byte copy of 64 lanes to 256 bytes of LDS
 __device__ inline void dma4s(u32x4 rs, uint32_t voff, uint32_t m0) {
   asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" :: "s"(m0), "v"(voff), "s"(rs) : "memory");

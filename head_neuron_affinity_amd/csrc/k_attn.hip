@@ -39,6 +39,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
   const int h = p.head_order[gi * r + rest % r], g = p.head_group[h];
 
   const int64_t q0 = (int64_t)qt * 128, t = q0 + 32 * w + (l & 31);
+  // q's rows come through the second tile's place, in whole lines
+  const uint32_t base = lds_addr(lds);
+  const typename L::At lane0 = L::lane(base, l);
+  {
+    uint32_t qo[L::PERIOD];
+    L::offsets(qo, w, l, p.ld_q, p.d);
+    const T* q = static_cast<const T*>(p.q) + (int64_t)h * p.d;
+    L::copy(q, p.ld_q, p.d, q0, p.T, qo, base + 2 * L::BYTES, w);
+    L::copy(q, p.ld_q, p.d, q0 + 64, p.T, qo, base + 3 * L::BYTES, w);
+  }
   const Span mine = Span::of(p.rows, p.causal, p.T, t);
   const int lo = mine.lo, hi = mine.hi;
   {
@@ -61,17 +71,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
   uint32_t ko[L::PERIOD], vo[L::PERIOD];
   L::offsets(ko, w, l, p.ld_k, p.d);
   L::offsets(vo, w, l, p.ld_v, p.d);
-  const uint32_t base = lds_addr(lds);
-  const typename L::At lane0 = L::lane(base, l);
   auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
     L::copy(K, p.ld_k, p.d, kb, end, ko, base + (uint32_t)(buf * 2 * L::BYTES), w);
     L::copy(V, p.ld_v, p.d, kb, end, vo, base + (uint32_t)(buf * 2 * L::BYTES + L::BYTES), w);
   };
 
+  if (first < end) issue(first, 0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
   typename L::Frag qf[2 * DT];
-  const T* qrow = static_cast<const T*>(p.q) + min<int64_t>(t, p.T - 1) * p.ld_q + (int64_t)h * p.d;
+  const typename L::At qt_at = L::move(lane0, (uint32_t)((2 + (w >> 1)) * L::BYTES + (w & 1) * 32 * L::PITCH));
 #pragma unroll
-  for (int s = 0; s < 2 * DT; ++s) L::load(qf[s], qrow, s, p.d, l);
+  for (int s = 0; s < 2 * DT; ++s) L::rows(qf[s], qt_at, 0, s);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");           // before the second tile is copied there
 
   f32x16 o[DT];
   float m, sum;
@@ -90,7 +102,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = f32x16{};
-    if (first < end) issue(first, 0);
+    if (CAREFUL) issue(first, 0);
     for (int kb = first; kb < end; kb += 64, buf ^= 1) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // this tile's copies
       __syncthreads();                                        // all waves' copies, and the other tile is read
@@ -185,6 +197,154 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
   put_rows<T, DT>(o, sum == 0.f ? 0.f : 1.0f / sum, p.a, nullptr, (t * p.H + h) * p.d, p.d, up, mine.live);
 }
 
+// Few blocks of 128 queries: a workgroup has 32 queries of a head, and its waves walk
+// over every NWth 32 keys in streams of their own, so that a walk's chain of steps is
+// a fourth (or half) as long; their sums meet in LDS.  The border is in launch_one.
+template <typename T, int DT, bool CAP, bool BIAS>
+__global__ __launch_bounds__((64 * kStreamWaves<T, DT>)) void attn_short_kernel(const AttnParams p) {
+  typedef Stream<T, DT> S;
+  typedef typename S::L L;
+  constexpr int NW = kStreamWaves<T, DT>;
+  constexpr int OP = 32 * DT + 4;                           // floats of a column of sums
+  static_assert(32 * OP * 4 <= S::REGION, "the sums fit a wave's stages");
+  __shared__ __attribute__((aligned(512))) unsigned char lds[NW * S::REGION];
+  __shared__ float ms[2][NW][32];
+  __shared__ uint32_t bad[NW][2];
+  const int tid = threadIdx.x, l = tid & 63, up = l >> 5, col = l & 31;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // blocks as in attn_kernel
+  const int nq = (int)((p.T + 31) / 32), r = p.H / p.G, gi = (int)blockIdx.x % p.G, rest = (int)blockIdx.x / p.G;
+  const int t0 = 32 * (nq - 1 - rest / r);
+  const int h = p.head_order[gi * r + rest % r], g = p.head_group[h];
+  const int t = t0 + col;
+  const Span mine = Span::of(p.rows, p.causal, p.T, t);
+  const int lo = mine.lo, hi = mine.hi;
+  const bool on = mine.live && lo < hi;
+  const int first = wave_min(on ? lo : INT32_MAX), end = wave_max(on ? hi : 0);
+
+  S keys;
+  const T* V = static_cast<const T*>(p.v) + (int64_t)g * p.d;
+  keys.init(static_cast<const T*>(p.k) + (int64_t)g * p.d, V, p.ld_k, p.ld_v, p.d, end, lds_addr(lds) + (uint32_t)(w * S::REGION), l);
+  const typename L::At lane0 = L::lane(keys.base, l);
+  typename L::Frag qf[2 * DT];
+  const T* qrow = static_cast<const T*>(p.q) + min<int64_t>(t, p.T - 1) * p.ld_q + (int64_t)h * p.d;
+#pragma unroll
+  for (int s = 0; s < 2 * DT; ++s) L::load(qf[s], qrow, s, p.d, l);
+  const bool capped = sizeof(T) == 2 ? CAP : p.cap > 0.f;
+  const float c1 = capped ? 2.0f * kLog2e * p.scale / p.cap : kLog2e * p.scale;
+  const float cap = kLog2e * p.cap;
+  const float slope = BIAS && p.slopes ? kLog2e * p.slopes[h] : 0.f;
+
+  f32x16 o[DT];
+  float m, sum;
+  auto walk = [&](auto careful) __attribute__((always_inline)) {
+    constexpr bool CAREFUL = decltype(careful)::value;
+    m = -__builtin_inff();
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] = f32x16{};
+    const int kb0 = first + 32 * w;
+    if (first >= end || kb0 >= end) return;
+    keys.issue(kb0, 0);
+    keys.issue(kb0 + 32 * NW, 1);
+    int buf = 0;
+    for (int kb = kb0; kb < end; kb += 32 * NW, buf ^= 1) {
+      // this stage's copies; the other's (as many, zeros past the end) may be in flight
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::WAIT) : "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), vt = L::move(kt, L::BYTES);
+      f32x16 s = {};
+#pragma unroll
+      for (int x = 0; x < 2 * DT; ++x) {
+        // a head dim of an odd number of sixteens has no last step (a fp32 step is 512 cycles)
+        if (sizeof(T) == 4 && x == 2 * DT - 1 && 16 * x >= p.d) continue;
+        typename L::Frag a;
+        L::rows(a, kt, 0, x);
+        mma(s, a, qf[x]);
+      }
+      const float at = (float)(t - kb - 4 * up);
+      const uint32_t from = (uint32_t)(lo - kb - 4 * up), len = (uint32_t)max(hi - lo, 0);
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int off = 8 * (v >> 2) + (v & 3);
+        float x = s[v] * c1;
+        if (CAP && capped) x = cap * tanh_of<T>(x);
+        if constexpr (BIAS) x = fmaf(-slope, fabsf(at - (float)off), x);
+        x = (uint32_t)off - from < len ? x : -__builtin_inff();
+        s[v] = x;
+        top = fmaxf(top, x);
+      }
+      top = swap_max(top);
+      if (__any(top > m + 8.f)) {
+        const float to = top > m + 8.f ? top : m;
+        const float f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        sum *= f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) o[i][v] *= f;
+      }
+      const float ref = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        s[v] = __builtin_amdgcn_exp2f(s[v] - ref);
+        sum += s[v];
+      }
+      L::template along<CAREFUL>(o, vt, 0, s, l);
+      if constexpr (CAREFUL) {
+        if (l < 2) bad[w][l] = 0;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        L::find_bad(lds + w * S::REGION + buf * 2 * L::BYTES + L::BYTES, l, 64, bad[w]);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const uint32_t words = __builtin_amdgcn_readfirstlane(*(volatile uint32_t*)&bad[w][0]);
+        add_bad_rows<T, DT>(o, s, words, p.d, l, [&](int x) { return V + (int64_t)(kb + x) * p.ld_v; },
+                            [&](int x) { return kb + x >= lo && kb + x < hi; });
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the stage is read
+      __builtin_amdgcn_sched_barrier(0);
+      keys.issue(kb + 64 * NW, buf);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // the last copies (zeros) are in
+  };
+  walk(std::false_type{});
+  const float z = finite<DT>(o);
+  if (__any(mine.live && z != z)) walk(std::true_type{});     // as in attn_kernel, a wave for itself
+
+  sum = swap_sum(sum);
+  float* mine_o = reinterpret_cast<float*>(lds + w * S::REGION);
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      *reinterpret_cast<float4*>(mine_o + col * OP + 32 * i + 8 * a + 4 * up) = make_float4(o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]);
+  if (up == 0) {
+    ms[0][w][col] = m;
+    ms[1][w][col] = mine.live ? sum : -1.f;
+  }
+  __syncthreads();
+  for (int x = tid; x < 32 * p.d; x += 64 * NW) {
+    const int c = x / p.d, e = x - c * p.d;
+    if (ms[1][0][c] == -1.f) continue;                        // a token of no document
+    float M = ms[0][0][c];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) M = fmaxf(M, ms[0][i][c]);
+    const float ref = M == -__builtin_inff() ? 0.f : M;
+    float total = 0.f, y = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const float f = __builtin_amdgcn_exp2f(ms[0][i][c] - ref);
+      total = fmaf(f, ms[1][i][c], total);
+      y = fmaf(f, reinterpret_cast<const float*>(lds + i * S::REGION)[c * OP + e], y);
+    }
+    const int64_t row = (int64_t)(t0 + c) * p.H + h;
+    static_cast<T*>(p.a)[row * p.d + e] = to_type<T>(total == 0.f ? 0.f : y / total);
+    if (e == 0 && p.lse) p.lse[row] = total == 0.f ? -__builtin_inff() : kLn2 * (M + __builtin_amdgcn_logf(total));
+  }
+}
+
 // rows[t]: the document of t by bisection of its starts, then the interval of keys
 // that its query sees and of queries that see its key
 __global__ __launch_bounds__(256) void attn_rows_kernel(int T, int docs, const int* start, const int* prefix, int causal, int4* rows) {
@@ -212,6 +372,19 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(int T, int docs, const i
 
 template <typename T, int DT, bool CAP, bool BIAS>
 hipError_t launch_one(const AttnParams& p, hipStream_t st) {
+  // Streams while they are at most two rounds (a CU has room for 160 KB of them) and
+  // the walk may be long, or its steps are (fp32).  One document, us, 128 queries a workgroup against
+  // streams: bf16, 8 heads of 64, 256, 1024, 4096 tokens 8.2, 20.9, 71.6 against 8.5, 13.9, 55.9; 16 heads of 128,
+  // 512 and 1024 tokens 16.8, 29.0 against 15.8, 31.1 (short documents 5.7 against 11.3: left out); fp32,
+  // 4 heads of 16, 64, 256, 2048 tokens 7.5, 18.9, 122.9 against 6.1, 8.0, 35.8; 16 heads of 128, 64, 256, 1024,
+  // 2048 (four rounds) 17.4, 52, 188, 370 against 20.9, 39, 132, 458.
+  if constexpr (sizeof(T) == 4 || DT <= 2) {
+    const int64_t streams = (p.T + 31) / 32 * p.H, slots = 256 * (160 * 1024 / (kStreamWaves<T, DT> * Stream<T, DT>::REGION + 1024));
+    if (streams <= 2 * slots && p.T >= (sizeof(T) == 2 ? 1024 : DT <= 2 ? 1 : 256)) {
+      hipLaunchKernelGGL((attn_short_kernel<T, DT, CAP, BIAS>), dim3((unsigned)streams), dim3(64 * kStreamWaves<T, DT>), 0, st, p);
+      return hipGetLastError();
+    }
+  }
   hipLaunchKernelGGL((attn_kernel<T, DT, CAP, BIAS>), dim3((unsigned)((p.T + 127) / 128 * p.H)), dim3(256), 0, st, p);
   return hipGetLastError();
 }

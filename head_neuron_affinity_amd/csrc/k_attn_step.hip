@@ -18,16 +18,14 @@ namespace {
 
 using namespace attn;
 
-template <typename T, int DT> constexpr int kStepWaves = Tile<T, DT>::BYTES * 8 <= 128 * 1024 ? 4 : 2;
-
 template <typename T, int DT, bool CAP, bool BIAS>
-__global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(const StepParams p) {
-  typedef Tile<T, DT> L;
-  constexpr int NW = kStepWaves<T, DT>, HALF = L::BYTES / 2, REGION = 4 * HALF;   // K, V of 32 keys, two stages
-  constexpr int CP = HALF / 1024, PERIOD = 16 / L::RPC > 1 ? 16 / L::RPC : 1;
+__global__ __launch_bounds__((64 * kStreamWaves<T, DT>)) void attn_step_kernel(const StepParams p) {
+  typedef Stream<T, DT> S;
+  typedef typename S::L L;
+  constexpr int NW = kStreamWaves<T, DT>;
   constexpr int OP = 32 * DT + 4;                           // floats of a column of sums
-  static_assert(32 * OP * 4 <= REGION, "the sums fit a wave's stages");
-  __shared__ __attribute__((aligned(512))) unsigned char lds[NW * REGION];
+  static_assert(32 * OP * 4 <= S::REGION, "the sums fit a wave's stages");
+  __shared__ __attribute__((aligned(512))) unsigned char lds[NW * S::REGION];
   __shared__ float ms[2][NW][32];
   const int tid = threadIdx.x, l = tid & 63, up = l >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -45,35 +43,13 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
   const int first = __builtin_amdgcn_readfirstlane((int)min<int64_t>(start + (int64_t)part * per, length));
   const int end = __builtin_amdgcn_readfirstlane((int)min<int64_t>(first + (int64_t)per, length));
 
-  const T* K = static_cast<const T*>(p.k) + b * p.bs_k + (int64_t)g * p.d;
-  const T* V = static_cast<const T*>(p.v) + b * p.bs_v + (int64_t)g * p.d;
-  // copy i of 32 rows: rows RPC i .., f repeats every 16 rows
-  uint32_t ko[PERIOD], vo[PERIOD];
-#pragma unroll
-  for (int i = 0; i < PERIOD; ++i) {
-    const int r = i * L::RPC + l / L::CPR, c = (l % L::CPR) ^ L::f(r);
-    const bool on = 16 * c < p.d * L::E;
-    ko[i] = on ? (uint32_t)(r * p.ld_k * L::E) + 16u * (uint32_t)c : kOutOfRange;
-    vo[i] = on ? (uint32_t)(r * p.ld_v * L::E) + 16u * (uint32_t)c : kOutOfRange;
-  }
-  const uint32_t base = lds_addr(lds) + (uint32_t)(w * REGION);
-  const typename L::At lane0 = L::lane(base, l);
-  auto one = [&](const T* x, int64_t ld, const uint32_t (&voff)[PERIOD], int kb, uint32_t to) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < CP; i += PERIOD) {
-      const int64_t from = kb + i * L::RPC, bytes = ((end - 1 - from) * ld + p.d) * L::E;
-      const u32x4 rs = uniform_rsrc(x + (end > from ? from * ld : 0), end <= from ? 0u : bytes > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)bytes);
-#pragma unroll
-      for (int j = 0; j < PERIOD; ++j) dma16s(rs, voff[j], 0u, to + (uint32_t)((i + j) * 1024));
-    }
-  };
-  auto issue = [&](int kb, int buf) __attribute__((always_inline)) {
-    one(K, p.ld_k, ko, kb, base + (uint32_t)(buf * 2 * HALF));
-    one(V, p.ld_v, vo, kb, base + (uint32_t)(buf * 2 * HALF + HALF));
-  };
+  S keys;
+  keys.init(static_cast<const T*>(p.k) + b * p.bs_k + (int64_t)g * p.d, static_cast<const T*>(p.v) + b * p.bs_v + (int64_t)g * p.d, p.ld_k, p.ld_v,
+            p.d, end, lds_addr(lds) + (uint32_t)(w * S::REGION), l);
+  const typename L::At lane0 = L::lane(keys.base, l);
   const int mine = first + 32 * w;
-  issue(mine, 0);
-  issue(mine + 32 * NW, 1);
+  keys.issue(mine, 0);
+  keys.issue(mine + 32 * NW, 1);
 
   const int col = l & 31;
   const int h = p.head_order[heads0 + min(col, heads - 1)];
@@ -93,9 +69,9 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
   int buf = 0;
   for (int kb = mine; kb < end; kb += 32 * NW, buf ^= 1) {
     // this stage's copies; the other's (as many, zeros past the end) may be in flight
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * CP) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::WAIT) : "memory");
     __builtin_amdgcn_sched_barrier(0);
-    const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * HALF)), vt = L::move(kt, HALF);
+    const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), vt = L::move(kt, L::BYTES);
     f32x16 s = {};
 #pragma unroll
     for (int x = 0; x < 2 * DT; ++x) {
@@ -136,11 +112,11 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
     L::template along<false>(o, vt, 0, s, l);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the stage is read
     __builtin_amdgcn_sched_barrier(0);
-    issue(kb + 64 * NW, buf);
+    keys.issue(kb + 64 * NW, buf);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // the last copies (zeros) are in
   sum = swap_sum(sum);
-  float* mine_o = reinterpret_cast<float*>(lds + w * REGION);
+  float* mine_o = reinterpret_cast<float*>(lds + w * S::REGION);
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -162,7 +138,7 @@ __global__ __launch_bounds__((64 * kStepWaves<T, DT>)) void attn_step_kernel(con
     for (int i = 0; i < NW; ++i) {
       const float f = __builtin_amdgcn_exp2f(ms[0][i][c] - ref);
       total = fmaf(f, ms[1][i][c], total);
-      y = fmaf(f, reinterpret_cast<const float*>(lds + i * REGION)[c * OP + e], y);
+      y = fmaf(f, reinterpret_cast<const float*>(lds + i * S::REGION)[c * OP + e], y);
     }
     const int64_t row = b * p.H + hc;
     if (p.splits == 1) {
@@ -213,7 +189,7 @@ __global__ __launch_bounds__(128) void attn_join_kernel(const StepParams p) {
 template <typename T, int DT, bool CAP, bool BIAS>
 hipError_t launch_one(const StepParams& p, hipStream_t st) {
   const int64_t grid = p.B * p.G * p.column_blocks * p.splits;
-  hipLaunchKernelGGL((attn_step_kernel<T, DT, CAP, BIAS>), dim3((unsigned)grid), dim3(64 * kStepWaves<T, DT>), 0, st, p);
+  hipLaunchKernelGGL((attn_step_kernel<T, DT, CAP, BIAS>), dim3((unsigned)grid), dim3(64 * kStreamWaves<T, DT>), 0, st, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL(attn_join_kernel<T>, dim3((unsigned)(p.B * p.H)), dim3(128), 0, st, p);
