@@ -945,11 +945,11 @@ def gated_ffn(n, w_gate, w_up, *, want_gu: bool = True, want_h: bool = True, g=N
             return gated_ffn(n, w_gate, w_up, want_gu=want_gu, want_h=want_h, g=g, u=u, h=h)
     if want_gu:
         if g is None:
-            g = torch.empty(shape, dtype=dt, device=n.device)
+            g = n.new_empty(shape)
         if u is None:
-            u = torch.empty(shape, dtype=dt, device=n.device)
+            u = n.new_empty(shape)
     if want_h and h is None:
-        h = torch.empty(shape, dtype=dt, device=n.device)
+        h = n.new_empty(shape)
     _check(lib().hna_gated_ffn(ctypes.byref(dims), _at(n), _at(w_gate), _at(w_up), _at(g), _at(u), _at(h),
                                _raw_stream(index)), "hna_gated_ffn")
     return g, u, h
@@ -1009,8 +1009,11 @@ def _gpu_of(index, *ts) -> int:
 
 def _heads_ld(t, name: str, shape: tuple, dtype: torch.dtype) -> int:
     """Elements from token to token of t [tokens, heads, d], whose heads lie next to each other."""
-    _is(t, name, shape, dtype)
+    if t.shape != shape or t.dtype != dtype:
+        _expect(t, name, shape, dtype)
     tokens, heads, d = shape
+    if t.is_contiguous():
+        return heads * d
     if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
         raise ValueError(f"{name}: a token's heads must lie next to each other (strides {t.stride()})")
     return t.stride(0) if tokens > 1 else heads * d
@@ -1067,20 +1070,26 @@ def _attn_args(q, k, v, rows, slopes, causal, scale, cap):
     dims = hna_attn_dims(T, _heads_ld(q, "q", (T, H, d), dt), _heads_ld(k, "k", (T, G, d), dt),
                          _heads_ld(v, "v", (T, G, d), dt), H, G, d, _code(dt), int(bool(causal)),
                          d ** -0.5 if scale is None else scale, cap)
-    _is(rows, "rows", (T, 4), torch.int32)
-    _is(slopes, "slopes", (H,), torch.float32)
+    if rows is not None:
+        _is(rows, "rows", (T, 4), torch.int32)
+    if slopes is not None:
+        _is(slopes, "slopes", (H,), torch.float32)
     index = q.get_device()
     if index < 0:
         raise ValueError("all tensors must live on the GPU")
-    _gpu_of(index, k, v)
+    if k.get_device() != index or v.get_device() != index:
+        raise ValueError("all tensors must live on the same GPU")
     return dims, index
 
 
 def _same_gpu(index: int, *ts):
     """Contiguous tensors, if any, on the GPU `index`."""
-    other = _index_of(*ts)
-    if other is not None and other != index:
-        raise ValueError("all tensors must live on the same GPU")
+    for t in ts:
+        if t is not None:
+            if t.get_device() != index:
+                raise ValueError("all tensors must live on the same GPU")
+            if not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous")
 
 
 def attention(q, k, v, rows=None, *, causal: bool = True, scale: Optional[float] = None, cap: float = 0.0,
@@ -1092,17 +1101,19 @@ def attention(q, k, v, rows=None, *, causal: bool = True, scale: Optional[float]
     d^-0.5; cap > 0: scores become cap tanh(score / cap); slopes fp32 [H]: minus slopes[h] |i - j|."""
     dims, index = _attn_args(q, k, v, rows, slopes, causal, scale, cap)
     T, H, d = q.shape
-    _is(out, "out", (T, H, d), q.dtype)
-    _is(lse, "lse", (T, H), torch.float32)
+    if out is not None:
+        _is(out, "out", (T, H, d), q.dtype)
+    if lse is not None:
+        _is(lse, "lse", (T, H), torch.float32)
     _same_gpu(index, rows, slopes, out, lse)
     if index != _current():
         with torch.cuda.device(index):
             return attention(q, k, v, rows, causal=causal, scale=scale, cap=cap, slopes=slopes,
                              group_of_head=group_of_head, out=out, lse=lse)
     if out is None:
-        out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+        out = q.new_empty((T, H, d))
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((T, H), dtype=torch.float32)
     _check(lib().hna_attention(ctypes.byref(dims), _at(q), _at(k), _at(v), _at(rows), _at(slopes),
                                _head_map(group_of_head, H, dims.G), _at(out), _at(lse), _raw_stream(index)),
            "hna_attention")
@@ -1169,29 +1180,28 @@ def attention_step(q, k, v, lengths, starts=None, *, scale: Optional[float] = No
     _is(k, "k", (B, S, G, d), dt)
     _is(v, "v", (B, S, G, d), dt)
     for t, name in ((k, "k"), (v, "v")):
-        if t.numel() and (t.stride(3) != 1 or (G > 1 and t.stride(2) != d)):
+        if not t.is_contiguous() and t.numel() and (t.stride(3) != 1 or (G > 1 and t.stride(2) != d)):
             raise ValueError(f"{name}: a key's heads must lie next to each other (strides {t.stride()})")
     ld = [t.stride(1) if S > 1 else G * d for t in (k, v)]
     bs = [t.stride(0) if B > 1 else 0 for t in (k, v)]
     dims = hna_step_dims(B, *ld, *bs, S, H, G, d, _code(dt), d ** -0.5 if scale is None else scale, cap)
     _is(lengths, "lengths", (B,), torch.int32)
-    _is(starts, "starts", (B,), torch.int32)
-    _is(slopes, "slopes", (H,), torch.float32)
-    _is(out, "out", (B, H, d), dt)
-    _is(lse, "lse", (B, H), torch.float32)
+    for t, name, shape, of in ((starts, "starts", (B,), torch.int32), (slopes, "slopes", (H,), torch.float32),
+                               (out, "out", (B, H, d), dt), (lse, "lse", (B, H), torch.float32)):
+        if t is not None:
+            _is(t, name, shape, of)
     index = _gpu_of(_index_of(q, lengths, starts, slopes, out, lse, workspace), k, v)
     if index != _current():
         with torch.cuda.device(index):
             return attention_step(q, k, v, lengths, starts, scale=scale, cap=cap, slopes=slopes,
                                   group_of_head=group_of_head, out=out, lse=lse, workspace=workspace)
     if out is None:
-        out = torch.empty((B, H, d), dtype=dt, device=q.device)
+        out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, H), dtype=torch.float32)
     L = lib()
     if workspace is None:
-        workspace = torch.empty(L.hna_attention_step_workspace_bytes(ctypes.byref(dims)) or 16, dtype=torch.uint8,
-                                device=q.device)
+        workspace = q.new_empty(L.hna_attention_step_workspace_bytes(ctypes.byref(dims)) or 16, dtype=torch.uint8)
     _check(L.hna_attention_step(ctypes.byref(dims), _at(q), _at(k), _at(v), _at(lengths), _at(starts), _at(slopes),
                                 _head_map(group_of_head, H, G), _at(out), _at(lse), _at(workspace),
                                 workspace.numel() * workspace.element_size(), _raw_stream(index)),
