@@ -40,14 +40,17 @@ struct Tile {
       voff[i] = 16 * c < d * E ? (uint32_t)(r * ld * E) + 16u * (uint32_t)c : kOutOfRange;
     }
   }
-  // copies of rows first .. of x, rows from `end` on are zeros
-  __device__ static inline void copy(const void* x, int64_t ld, int d, int64_t first, int64_t end, const uint32_t (&voff)[PERIOD],
+  // copies of rows first .. of x, rows from `end` on are zeros (32-bit factors: few scalar instructions)
+  __device__ static inline void copy(const void* x, int64_t ld, int d, int first, int end, const uint32_t (&voff)[PERIOD],
                                      uint32_t lds, int w) {
+    const uint32_t row = (uint32_t)ld * E;
+    const char* at = static_cast<const char*>(x) + (uint64_t)(uint32_t)first * row;
+    const int64_t n = (int64_t)(end - 1 - first) * (int32_t)row + d * E;   // nothing or less: no rows (ld >= d)
+    const uint32_t left = n <= 0 ? 0u : n > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)n;
 #pragma unroll
     for (int i = 0; i < COPIES; i += PERIOD) {
-      const int64_t from = first + 4 * i * RPC, n = ((end - 1 - from) * ld + d) * E;
-      const u32x4 rs = uniform_rsrc(static_cast<const char*>(x) + from * ld * E,
-                                    end <= from ? 0u : n > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)n);
+      const uint32_t off = 4 * i * RPC * row;
+      const u32x4 rs = uniform_rsrc(at + off, left > off ? left - off : 0u);
 #pragma unroll
       for (int j = 0; j < PERIOD; ++j)
         if (BYTES >= 4096 || 1024 * w < BYTES) dma16s(rs, voff[j], 0u, lds + (uint32_t)((4 * (i + j) + w) * 1024));
@@ -122,8 +125,12 @@ struct Tile {
   // the same elements of a row in memory (elements from d on are zeros)
   __device__ static inline void load(Frag& a, const T* row, int s, int d, int l) {
     const int c = 16 * s + 8 * (l >> 5);
+    const bool on = c < d;                                    // a select, not a branch
 #pragma unroll
-    for (int x = 0; x < F; ++x) a[x] = c < d ? *reinterpret_cast<const uint4*>(row + c + x * (16 / E)) : make_uint4(0, 0, 0, 0);
+    for (int x = 0; x < F; ++x) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + (on ? c + x * (16 / E) : 0));
+      a[x] = make_uint4(on ? v.x : 0u, on ? v.y : 0u, on ? v.z : 0u, on ? v.w : 0u);
+    }
   }
 
   // ---- rows that hold a NaN or an infinity ----
@@ -223,18 +230,18 @@ __device__ inline int wave_min(int x) {
 }
 __device__ inline int wave_max(int x) { return ~wave_min(~x); }
 
-// The order of READS fragment reads, STEP of them for two products: AHEAD in flight,
+// The order of READS fragment reads, STEP of them for MFMAS products: AHEAD in flight,
 // since a read takes as long as several products
-template <int READS, int STEP, int AHEAD>
+template <int READS, int STEP, int AHEAD, int MFMAS = 2>
 __device__ inline __attribute__((always_inline)) void reads_ahead() {
   constexpr int A = READS < AHEAD ? READS : AHEAD;
   __builtin_amdgcn_sched_group_barrier(0x100, A, 0);
 #pragma unroll
   for (int x = 0; x < (READS - A) / STEP; ++x) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, MFMAS, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, STEP, 0);
   }
-  __builtin_amdgcn_sched_group_barrier(0x008, 2 * A / STEP, 0);
+  __builtin_amdgcn_sched_group_barrier(0x008, MFMAS * A / STEP, 0);
 }
 
 // A lane's column times `by`, as a row of out (the two lanes of a column exchange
@@ -321,10 +328,14 @@ struct Stream {
     }
   }
   __device__ inline void one(const T* x, int64_t ld, const uint32_t (&voff)[PERIOD], int kb, uint32_t to) const {
+    const uint32_t row = (uint32_t)ld * L::E;
+    const char* at = reinterpret_cast<const char*>(x) + (end > kb ? (uint64_t)(uint32_t)kb * row : 0);
+    const int64_t n = (int64_t)(end - 1 - kb) * (int32_t)row + d * L::E;
+    const uint32_t left = n <= 0 ? 0u : n > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)n;
 #pragma unroll
     for (int i = 0; i < CP; i += PERIOD) {
-      const int64_t from = kb + i * L::RPC, bytes = ((end - 1 - from) * ld + d) * L::E;
-      const u32x4 rs = uniform_rsrc(x + (end > from ? from * ld : 0), end <= from ? 0u : bytes > (int64_t)kMaxResourceBytes ? kMaxResourceBytes : (uint32_t)bytes);
+      const uint32_t off = i * L::RPC * row;
+      const u32x4 rs = uniform_rsrc(at + off, left > off ? left - off : 0u);
 #pragma unroll
       for (int j = 0; j < PERIOD; ++j) dma16s(rs, voff[j], 0u, to + (uint32_t)((i + j) * 1024));
     }

@@ -193,6 +193,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
           for (int v = 0; v < 16; ++v) s[v] = (uint32_t)(32 * i + 8 * (v >> 2) + (v & 3)) - from < len ? s[v] : 0.f;
         }
         L::template along<CAREFUL>(o, kt, 32 * i, s, l);
+        if constexpr (sizeof(T) == 2 && !CAREFUL) reads_ahead<4 * DT, 2, 8, 1>();
         if constexpr (CAREFUL)
           add_bad_rows<T, DT>(o, s, i ? bad1 : bad0, p.d, l, [&](int x) { return K + (int64_t)(kb + 32 * i + x) * p.ld_k; },
                               [&](int x) { return kb + 32 * i + x >= lo && kb + 32 * i + x < hi; });
@@ -392,6 +393,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
       }
       L::template along<CAREFUL>(dv, at, 0, dp, l);
       L::template along<CAREFUL>(dk, qt, 0, s, l);
+      if constexpr (sizeof(T) == 2 && !CAREFUL) reads_ahead<8 * DT, 2, 8, 1>();
       if constexpr (CAREFUL) {
         auto on = [&](int x) { return ((seen[w][x] >> (l & 31)) & 1) != 0; };
         add_bad_rows<T, DT>(dv, dp, bad_a, p.d, l, [&](int x) { return static_cast<const T*>(p.da) + (int64_t)(qb + x) * ld_a + (int64_t)h * p.d; }, on);
