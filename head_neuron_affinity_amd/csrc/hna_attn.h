@@ -57,34 +57,40 @@ struct Tile {
     }
   }
   // A lane's addresses in a tile at LDS address `at` (a multiple of 512): of row
-  // l & 31's elements 8 (l / 32) .., and (bf16) of the transposed reads of rows 8 j + 4 (l / 32) + ..
+  // l & 31's elements 8 (l / 32) .., and (bf16) of the transposed reads of rows
+  // 4 (l / 32) + .. (8 rows on f differs by 2)
   struct At {
-    uint32_t row[F], col[2];
+    uint32_t row[F], col;
   };
   __device__ static inline At lane(uint32_t at, int l) {
     const int up = l >> 5, r = (l & 15) >> 2, b = 2 * ((l >> 4) & 1) + ((l & 3) >> 1);
     At x;
 #pragma unroll
     for (int i = 0; i < F; ++i) x.row[i] = at + (uint32_t)((l & 31) * PITCH + (((F * up + i) ^ f(l & 31)) << 4));
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int row = 8 * j + 4 * up + r;
-      x.col[j] = E == 2 ? at + (uint32_t)(row * PITCH + ((b ^ f(row)) << 4) + 8 * (l & 1)) : at;
-    }
+    const int row = 4 * up + r;
+    x.col = E == 2 ? at + (uint32_t)(row * PITCH + ((b ^ f(row)) << 4) + 8 * (l & 1)) : at;
     return x;
   }
   __device__ static inline At move(At x, uint32_t by) {
 #pragma unroll
     for (int i = 0; i < F; ++i) x.row[i] += by;
-    x.col[0] += by;
-    x.col[1] += by;
+    x.col += by;
+    return x;
+  }
+  // the same, with nothing known of the result: what is computed from it stays next
+  // to its reads, and no registers hold it through a walk
+  __device__ static inline At here(At x, uint32_t by) {
+    x = move(x, by);
+#pragma unroll
+    for (int i = 0; i < F; ++i) asm volatile("" : "+v"(x.row[i]));
+    asm volatile("" : "+v"(x.col));
     return x;
   }
   template <typename V>
   __device__ static inline V read(uint32_t at) {
     return *reinterpret_cast<const __attribute__((address_space(3))) V*>(at);
   }
-  // rows r0 + (l & 31), elements 16 s + 8 (l / 32) .. + 7: r0 a multiple of 32
+  // rows r0 + (l & 31), elements 16 s + 8 (l / 32) .. + 7: r0 a multiple of 32 (a tile's rows and the next one's)
   __device__ static inline void rows(Frag& a, const At& t, int r0, int s) {
 #pragma unroll
     for (int x = 0; x < F; ++x) {
@@ -99,14 +105,14 @@ struct Tile {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         v[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                             (lds_s16x4)((t.col[j] ^ (uint32_t)(64 * dt)) + (uint32_t)(r0 * PITCH))));
+                                             (lds_s16x4)((t.col ^ (uint32_t)(64 * dt + 32 * j)) + (uint32_t)((r0 + 8 * j) * PITCH))));
       a[0] = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
     } else {
       uint32_t v[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int row = r0 + 8 * (x >> 2) + 4 * (l >> 5) + (x & 3), c = 8 * dt + ((l & 31) >> 2);
-        v[x] = read<uint32_t>(t.col[0] + (uint32_t)(row * PITCH + ((c ^ f(row)) << 4) + 4 * (l & 3)));
+        v[x] = read<uint32_t>(t.col + (uint32_t)(row * PITCH + ((c ^ f(row)) << 4) + 4 * (l & 3)));
       }
       a[0] = make_uint4(v[0], v[1], v[2], v[3]);
       a[F - 1] = make_uint4(v[4], v[5], v[6], v[7]);

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // this tile's copies
       __syncthreads();                                        // all waves' copies, and the other tile is read
       if (kb + 64 < end) issue(kb + 64, buf ^ 1);
-      const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), vt = L::move(kt, L::BYTES);
+      const typename L::At kv = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES));   // K, then V
       uint32_t bad0 = 0, bad1 = 0;
       if constexpr (CAREFUL) {
         L::find_bad(lds + buf * 2 * L::BYTES + L::BYTES, tid, 256, bad);
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           typename L::Frag a;
-          L::rows(a, kt, 32 * i, x);
+          L::rows(a, kv, 32 * i, x);
           mma(s[i], a, qf[x]);
         }
       if constexpr (sizeof(T) == 2) reads_ahead<4 * DT, 2, 8>();
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_kernel(const
         }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        L::template along<CAREFUL>(o, vt, 32 * i, s[i], l);
+        L::template along<CAREFUL>(o, kv, 64 + 32 * i, s[i], l);
         if constexpr (CAREFUL)
           add_bad_rows<T, DT>(o, s[i], i ? bad1 : bad0, p.d, l, [&](int x) { return V + (int64_t)(kb + 32 * i + x) * p.ld_v; },
                               [&](int x) { return kb + 32 * i + x >= lo && kb + 32 * i + x < hi; });
@@ -253,14 +253,14 @@ __global__ __launch_bounds__((64 * kStreamWaves<T, DT>)) void attn_short_kernel(
       // this stage's copies; the other's (as many, zeros past the end) may be in flight
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::WAIT) : "memory");
       __builtin_amdgcn_sched_barrier(0);
-      const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), vt = L::move(kt, L::BYTES);
+      const typename L::At kv = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES));   // K, then V
       f32x16 s = {};
 #pragma unroll
       for (int x = 0; x < 2 * DT; ++x) {
         // a head dim of an odd number of sixteens has no last step (a fp32 step is 512 cycles)
         if (sizeof(T) == 4 && x == 2 * DT - 1 && 16 * x >= p.d) continue;
         typename L::Frag a;
-        L::rows(a, kt, 0, x);
+        L::rows(a, kv, 0, x);
         mma(s, a, qf[x]);
       }
       const float at = (float)(t - kb - 4 * up);
@@ -293,7 +293,7 @@ __global__ __launch_bounds__((64 * kStreamWaves<T, DT>)) void attn_short_kernel(
         s[v] = __builtin_amdgcn_exp2f(s[v] - ref);
         sum += s[v];
       }
-      L::template along<CAREFUL>(o, vt, 0, s, l);
+      L::template along<CAREFUL>(o, kv, 32, s, l);
       if constexpr (CAREFUL) {
         if (l < 2) bad[w][l] = 0;
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

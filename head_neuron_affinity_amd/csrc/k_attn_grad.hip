@@ -145,6 +145,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
   // where a sum is not finite
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
+    if constexpr (CAREFUL) {                                  // read again, not kept in registers through the first walk
+#pragma unroll
+      for (int x = 0; x < 2 * DT; ++x) {
+        L::load(qf[x], qrow, x, p.d, l);
+        L::load(af[x], darow, x, p.d, l);
+      }
+    }
     int buf = 0;
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = f32x16{};
@@ -153,7 +160,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (kb + 64 < end) issue(kb + 64, buf ^ 1);
-      const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), vt = L::move(kt, L::BYTES);
+      const typename L::At kv = L::here(lane0, (uint32_t)(buf * 2 * L::BYTES));   // K, then V
       uint32_t bad0 = 0, bad1 = 0;
       if constexpr (CAREFUL) {
         L::find_bad(lds + buf * 2 * L::BYTES, tid, 256, bad);
@@ -173,9 +180,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
 #pragma unroll
         for (int x = 0; x < 2 * DT; ++x) {
           typename L::Frag a;
-          L::rows(a, kt, 32 * i, x);
+          L::rows(a, kv, 32 * i, x);
           mma(s, a, qf[x]);
-          L::rows(a, vt, 32 * i, x);
+          L::rows(a, kv, 64 + 32 * i, x);
           mma(dp, a, af[x]);
         }
         if constexpr (sizeof(T) == 2) reads_ahead<4 * DT, 2, 8>();
@@ -192,8 +199,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
 #pragma unroll
           for (int v = 0; v < 16; ++v) s[v] = (uint32_t)(32 * i + 8 * (v >> 2) + (v & 3)) - from < len ? s[v] : 0.f;
         }
-        L::template along<CAREFUL>(o, kt, 32 * i, s, l);
-        if constexpr (sizeof(T) == 2 && !CAREFUL) reads_ahead<4 * DT, 2, 8, 1>();
+        L::template along<CAREFUL>(o, kv, 32 * i, s, l);
+        if constexpr (sizeof(T) == 2 && !CAREFUL) reads_ahead<4 * DT, 2, 4, 1>();
         if constexpr (CAREFUL)
           add_bad_rows<T, DT>(o, s, i ? bad1 : bad0, p.d, l, [&](int x) { return K + (int64_t)(kb + 32 * i + x) * p.ld_k; },
                               [&](int x) { return kb + 32 * i + x >= lo && kb + 32 * i + x < hi; });
@@ -284,10 +291,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
   };
 
   const int64_t tr = min<int64_t>(t, p.T - 1);
-  typename L::Frag kf[2 * DT];
   const T* krow = static_cast<const T*>(p.k) + tr * p.ld_k + (int64_t)g * p.d;
-#pragma unroll
-  for (int s = 0; s < 2 * DT; ++s) L::load(kf[s], krow, s, p.d, l);
   {
     uint32_t vo[LV::PERIOD];
     LV::offsets(vo, w, l, p.ld_v, p.d);
@@ -295,7 +299,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
     LV::copy(v, p.ld_v, p.d, k0, p.T, vo, base + 4 * L::BYTES, w);
     LV::copy(v, p.ld_v, p.d, k0 + 64, p.T, vo, base + 4 * L::BYTES + LV::BYTES, w);
   }
-  const typename L::At vt = L::move(lane0, (uint32_t)(4 * L::BYTES + w * 32 * L::PITCH));
 
   f32x16 dk[DT], dv[DT];
   const bool capped = sizeof(T) == 2 ? CAP : p.cap > 0.f;
@@ -307,6 +310,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
   // da where a sum is not finite
   auto walk = [&](auto careful) __attribute__((always_inline)) {
     constexpr bool CAREFUL = decltype(careful)::value;
+    typename L::Frag kf[2 * DT];                              // (of each walk: none are spilled in the first for the second)
+#pragma unroll
+    for (int x = 0; x < 2 * DT; ++x) L::load(kf[x], krow, x, p.d, l);
     int buf = 0, head = tiles ? step0 / tiles : 0, tile = step0 - head * tiles;
     ih = head;
     it = tile;
@@ -323,7 +329,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
         ++head;
       }
       const float slope = BIAS && p.slopes ? kLog2e * p.slopes[h] : 0.f;
-      const typename L::At qt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), at = L::move(qt, L::BYTES);
+      const typename L::At qa = L::here(lane0, (uint32_t)(buf * 2 * L::BYTES));   // Q, then dA
+      const typename L::At vt = L::here(lane0, (uint32_t)(4 * L::BYTES + w * 32 * L::PITCH));
       uint32_t bad_q = 0, bad_a = 0;
       if constexpr (CAREFUL) {
         L::find_bad(lds + buf * 2 * L::BYTES, tid, 256, bad);
@@ -354,9 +361,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
 #pragma unroll
       for (int x = 0; x < 2 * DT; ++x) {
         typename L::Frag a, b;
-        L::rows(a, qt, 0, x);
+        L::rows(a, qa, 0, x);
         mma(s, a, kf[x]);
-        L::rows(a, at, 0, x);
+        L::rows(a, qa, 32, x);
         L::rows(b, vt, 0, x);
         mma(dp, a, b);
       }
@@ -391,9 +398,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(c
           }
         }
       }
-      L::template along<CAREFUL>(dv, at, 0, dp, l);
-      L::template along<CAREFUL>(dk, qt, 0, s, l);
-      if constexpr (sizeof(T) == 2 && !CAREFUL) reads_ahead<8 * DT, 2, 8, 1>();
+      L::template along<CAREFUL>(dv, qa, 32, dp, l);
+      L::template along<CAREFUL>(dk, qa, 0, s, l);
+      if constexpr (sizeof(T) == 2 && !CAREFUL) reads_ahead<8 * DT, 2, 4, 1>();
       if constexpr (CAREFUL) {
         auto on = [&](int x) { return ((seen[w][x] >> (l & 31)) & 1) != 0; };
         add_bad_rows<T, DT>(dv, dp, bad_a, p.d, l, [&](int x) { return static_cast<const T*>(p.da) + (int64_t)(qb + x) * ld_a + (int64_t)h * p.d; }, on);

@@ -71,12 +71,12 @@ __global__ __launch_bounds__((64 * kStreamWaves<T, DT>)) void attn_step_kernel(c
     // this stage's copies; the other's (as many, zeros past the end) may be in flight
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::WAIT) : "memory");
     __builtin_amdgcn_sched_barrier(0);
-    const typename L::At kt = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES)), vt = L::move(kt, L::BYTES);
+    const typename L::At kv = L::move(lane0, (uint32_t)(buf * 2 * L::BYTES));   // K, then V
     f32x16 s = {};
 #pragma unroll
     for (int x = 0; x < 2 * DT; ++x) {
       typename L::Frag a;
-      L::rows(a, kt, 0, x);
+      L::rows(a, kv, 0, x);
       mma(s, a, qf[x]);
     }
     const float at = (float)(length - 1 - kb - 4 * up);
@@ -109,7 +109,7 @@ __global__ __launch_bounds__((64 * kStreamWaves<T, DT>)) void attn_step_kernel(c
       s[v] = __builtin_amdgcn_exp2f(s[v] - ref);
       sum += s[v];
     }
-    L::template along<false>(o, vt, 0, s, l);
+    L::template along<false>(o, kv, 32, s, l);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the stage is read
     __builtin_amdgcn_sched_barrier(0);
     keys.issue(kb + 64 * NW, buf);
