@@ -352,7 +352,7 @@ struct StepWorkspace {
 };
 StepWorkspace step_workspace(const hna_step_dims* dm) {
   StepWorkspace w{};
-  w.splits = attention_step_splits(dm->B, dm->G, dm->S);
+  w.splits = attention_step_splits(dm->B, dm->G, dm->S, dm->d, dm->dtype == HNA_BF16);
   if (w.splits == 1) return w;
   const size_t rows = (size_t)dm->B * dm->H * w.splits;
   w.ms = align256(rows * dm->d * sizeof(float));

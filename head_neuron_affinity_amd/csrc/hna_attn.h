@@ -352,6 +352,9 @@ struct Stream {
     one(V, ld_v, vo, kb, base + (uint32_t)(buf * 2 * L::BYTES + L::BYTES));
   }
 };
+// workgroups of streams that fill the GPU: as many a CU as have room in its 160 KB
+template <typename T, int DT>
+constexpr int kStreamSlots = 256 * (160 * 1024 / (kStreamWaves<T, DT> * Stream<T, DT>::REGION + 1024));
 
 // asynchronous 4-byte copy of 64 lanes to 256 bytes of LDS
 __device__ inline void dma4s(u32x4 rs, uint32_t voff, uint32_t m0) {

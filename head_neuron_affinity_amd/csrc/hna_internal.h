@@ -404,7 +404,7 @@ struct StepParams {
   int8_t head_order[kMaxHeads];
   int16_t group_start[kMaxHeads + 1];
 };
-int attention_step_splits(int64_t B, int G, int S);
+int attention_step_splits(int64_t B, int G, int S, int d, int bf16);
 hipError_t launch_attention_step(const StepParams& p, int bf16, hipStream_t st);
 
 }  // namespace hna

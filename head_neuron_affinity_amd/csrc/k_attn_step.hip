@@ -8,6 +8,8 @@
 // no barrier, so that a CU has 64 KB and more of copies in flight.  The waves'
 // sums meet in LDS and, where the keys are split among workgroups too (few
 // sequences), a second kernel joins the parts in order.
+// 96 sequences of 4096 to 8192 keys, 8 groups of 128, bf16: 430 us, 5.7e12 bytes a second; one
+// of 4096 keys 7 us and 4 for the join, latency.
 #include <algorithm>
 
 #include "hna_internal.h"
@@ -212,9 +214,19 @@ hipError_t launch_t(const StepParams& p, hipStream_t st) {
 
 }  // namespace
 
-int attention_step_splits(int64_t B, int G, int S) {
+// Workgroups that share a sequence's keys for a group, of 128 keys and more each: one round
+// of workgroups on all CUs (one a CU for bf16 heads of more than 64, more for smaller ones).
+// From one round of unsplit ones on two parts, and from four on one: where lengths differ,
+// the halves of the long sequences fill the end of the last round.  us with the parts chosen
+// here against twice and four times as many, bf16, S keys a sequence, 8 groups of 128: 1 x 32768
+// 29 against 34 and 34, 8 x 4096 29 against 32 and 42, 16 x 4096 49 against 50 and 59; two
+// parts against one: 96 x 8192, lengths from half on 439 against 456, all equal 579 against 547.
+int attention_step_splits(int64_t B, int G, int S, int d, int bf16) {
   const int64_t rows = std::max<int64_t>(B * G, 1);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(1024 + rows - 1) / rows, ((int64_t)S + 127) / 128, 64}));
+  const int64_t slots = bf16 ? (d <= 32 ? kStreamSlots<__bf16, 1> : d <= 64 ? kStreamSlots<__bf16, 2> : kStreamSlots<__bf16, 4>)
+                             : (d <= 32 ? kStreamSlots<float, 1> : d <= 64 ? kStreamSlots<float, 2> : kStreamSlots<float, 4>);
+  const int64_t parts = rows <= slots ? slots / rows : rows < 4 * slots ? 2 : 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({parts, ((int64_t)S + 127) / 128, 64}));
 }
 
 hipError_t launch_attention_step(const StepParams& p, int bf16, hipStream_t st) {
