@@ -16,8 +16,8 @@
 // fp32's range, and the accumulators are seldom rescaled.
 // bf16, heads of 128: 16384 tokens of one document 1.0e15 operations a second (one product of 2
 // operations for each pair and dimension, twice), 64 documents of 1024 0.40 to 0.43 ms, 0.66e15: the
-// exponentials and their neighbours take the vector units as long as the products take the
-// matrix cores (49 and 43% busy, two waves a SIMD at 2.1 GHz), and a short walk's start
+// exponentials and their neighbours take the vector units about as long as the products take the
+// matrix cores (busy 53% of the cycles, two waves a SIMD at 2.1 GHz), and a short walk's start
 // and end are not hidden.  Tiles of 32 keys at three waves a SIMD 657 against 457 us then, at two 487.
 #include "hna_internal.h"
 #include "hna_attn.h"

@@ -56,7 +56,8 @@ __device__ inline void sort_key_blocks(const AttnParams& p, int* lds) {
 
 // A workgroup has 128 queries of a head, 32 a wave, q and da in registers, and walks over tiles
 // of 64 keys as the forward pass does, with three products where that has two.  16384 tokens
-// in documents of 2048, 32 capped heads of 128: 0.62 ms, 0.67e15 operations a second, bound as below.
+// in documents of 2048, 32 capped heads of 128: 0.60 to 0.62 ms, 4.1e11 operations in 3 products, 0.68e15 a
+// second, bound as below.
 template <typename T, int DT, bool CAP, bool BIAS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(const AttnParams p) {
   typedef Tile<T, DT> L;
@@ -226,7 +227,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(co
 // the exponentials of the other.  The registers just suffice: k's rows are read anew
 // for each walk and the addresses made in each step, since a spilled value's load
 // waits for the next tile's copies too (0.72 against 1.10 ms).  16384 tokens in documents of 2048, 32
-// capped heads of 128 in 8 groups: 0.72 ms, 4 products of 2.75e11 operations in it, 0.76e15 a second;
+// capped heads of 128 in 8 groups: 0.69 to 0.72 ms, 5.5e11 operations in 4 products, 0.79e15 a second;
 // bound by the chain of LDS reads, products and exponentials of two waves.
 template <typename T, int DT, bool CAP, bool BIAS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attn_dkv_kernel(const AttnParams p) {

@@ -45,10 +45,10 @@ template <int MODE> constexpr bool kMajorB = MODE == kFfnDw;
 // are 64 KB, 1024 cycles of a CU's 64 bytes a cycle: spread over two quarters (1024
 // cycles) they cost 8 to 10% less than in one.  One workgroup a CU walks over its tiles, and the
 // steps of all of them are one stream, so that the copies never drain between tiles.
-// Power sets the pace on data (MFMAs busy 60% of the cycles at 1.5 to 1.8 GHz):
+// Power sets the pace on data (MFMAs busy 61% (gate) to 71% of the cycles at 1.5 to 1.8 GHz):
 // lines touched ahead in L2, and copies spread over three quarters, made no difference.
 // Measured, T x hidden x I, bf16: 65536 x 1536 x 4096 forward (g and u) 1.46 ms, 1.13e15 operations
-// a second; 8192 x 4096 x 14336 gradients 3.2 to 3.3 ms, 1.75e15.
+// a second; 8192 x 4096 x 14336 gradients, dn 1.54 ms, 1.25e15, dw 1.49 ms, 1.29e15, dg and du 0.2 ms.
 // A gate tile's 256 rows are 128 channels of both matrices, 64 + 64 a wave, so
 // that a wave holds g and u of the same channels and tokens.
 struct FfnTiles {
