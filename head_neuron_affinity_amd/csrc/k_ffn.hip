@@ -676,7 +676,10 @@ hipError_t launch_ffn_t(const FfnMmParams& p0, int mode, hipStream_t st) {
     }
     if (v == k128) return launch_tile<T, kFfnGate, 128, 128, 2, 2, 1, 2>(p, st);
     if (v == k64) return launch_tile<T, kFfnGate, 64, 64, 2, 2, 2, 2>(p, st);
-    return launch_tile<T, kFfnGate, 64, 32, 2, 1, 2, 2>(p, st);
+    // bf16's few tokens wait for the weights: a third stage, still two workgroups a CU (weights from
+    // HBM: 1 x 4096 x 14336 45.7 us against 48.3 with two, 8 x 1536 x 4096 10.5 against 12.8; in cache 6.2 against
+    // 6.0); fp32's many tiles for three (219 x 1000 x 2531: 37 with two stages, 41 with three)
+    return launch_tile<T, kFfnGate, 64, 32, 2, 1, 2, sizeof(T) == 2 ? 3 : 2>(p, st);
   }
   if (mode == kFfnDw) {
     if (v == kBig) {
