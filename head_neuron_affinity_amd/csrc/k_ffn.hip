@@ -576,7 +576,7 @@ __global__ __launch_bounds__(256) void ffn_join_kernel(const float* part, int sp
 
 // dg = dh u silu'(g), du = dh silu(g) in rows of I8 = I rounded up to 8 elements,
 // zeros behind I (they are k of dn's product).  A thread has 8 channels of a token;
-// rows that start on any element are loaded one element at a time.
+// those of rows that start on any element are put together from words (element loads at a row's end).
 template <typename T, bool WIDE>
 __global__ __launch_bounds__(256) void ffn_grad_kernel(const T* dh, const T* g, const T* u, int64_t chunks, int I, int I8, T* dg, T* du) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // of 8 channels
@@ -593,10 +593,27 @@ __global__ __launch_bounds__(256) void ffn_grad_kernel(const T* dh, const T* g, 
     const int64_t t = (uint64_t)i < (1ull << 32) ? (uint32_t)i / (uint32_t)(I8 / 8) : i / (I8 / 8);
     const int c = (int)(8 * (i - t * (I8 / 8)));
     const int64_t o = t * I + c;
+    if (c + 8 <= I) {
 #pragma unroll
-    for (int s = 0; s < 3; ++s)
+      for (int s = 0; s < 3; ++s) {
+        if constexpr (sizeof(T) == 4) {
+          __builtin_memcpy(x[s], src[s] + o, sizeof(x[s]));
+        } else {
+          const uint32_t odd = (uint32_t)o & 1;                // whole words from o - odd on, and the eighth element
+          uint32_t w[5];
+          __builtin_memcpy(w, __builtin_assume_aligned(src[s] + (o - odd), 4), 16);
+          w[4] = *reinterpret_cast<const uint16_t*>(src[s] + o + 7);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[s][e] = c + e < I ? src[s][o + e] : (T)0.f;
+          for (int e = 0; e < 4; ++e) w[e] = odd ? w[e] >> 16 | w[e + 1] << 16 : w[e];
+          __builtin_memcpy(x[s], w, 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < 3; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[s][e] = c + e < I ? src[s][o + e] : (T)0.f;
+    }
   }
   typename Four<T>::type og[2], ou[2];
 #pragma unroll
